@@ -14,7 +14,7 @@ import os
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libmtpspec.so")
 
-F32, BF16 = 0, 1
+F32, BF16, F16 = 0, 1, 2
 STATUS_BAD_DRAFT_ID = 0x1
 STATUS_BAD_PARAM = 0x2
 STATUS_TIMEOUT = 0x4
@@ -58,6 +58,12 @@ def load():
         "mtp_draft_steps": ([p, p, p, p, p, p, p, p, p, f32, i64, i64, i64, i32, p, p, p, sz, p, p],
                             C.c_int),
         "mtp_draft_steps_workspace_bytes": ([i64, i64, i64], sz),
+        "mtp_latent_append": ([p, i64, p, i64, p, f32, p, i64, i32, p, p, i64, i32, i32, p, i64, i64,
+                               p, i64, i32, i64, p, i64, i64, p, i64, i64, i32, C.c_int, p, p],
+                              C.c_int),
+        "mtp_latent_attn": ([p, i64, i64, i64, p, i64, i32, i64, p, i64, p, i64, i32, i32, i32, i32,
+                             f32, p, i64, i64, i64, p, C.c_int, p, sz, p, p], C.c_int),
+        "mtp_latent_attn_workspace_bytes": ([i64, i32, i32, i32, i32], sz),
         "mtpspec_status_string": ([C.c_int], C.c_char_p),
         "mtpspec_launch_count": ([], C.c_uint64),
         "mtpspec_selftest_wait_timeout": ([C.c_int, C.c_uint32, C.c_void_p, C.c_void_p], C.c_int),
@@ -346,3 +352,103 @@ def spec_verify_sample_static(target_logits, draft_logits, draft_ids, temperatur
     _call("spec_verify_sample_static", *head, *tail,
           _arg(status, "status", _I32, 1, optional=True), _stream(stream))
     return out_tokens, num_accepted
+
+
+# ---------------------------------------------------------------- latent attention
+
+_HALF_CODES = None
+
+
+def _view(t, name, shape, like=None):
+    """(pointer, strides in elements) of a 16-bit tensor of `shape` on the GPU whose last axis
+    is contiguous; `like` gives the type it has to have."""
+    global _HALF_CODES
+    if _HALF_CODES is None:
+        import torch
+        _HALF_CODES = {torch.bfloat16: BF16, torch.float16: F16}
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not isinstance(t, _kinds()["tensor"]):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype not in _HALF_CODES or (like is not None and t.dtype != like):
+        raise TypeError(f"{name} must hold {like or 'bfloat16 or float16'} values, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    st = t.stride()
+    if shape[-1] > 1 and st[-1] != 1:
+        raise ValueError(f"{name}'s last axis must be contiguous")
+    return t.data_ptr(), [0 if n == 1 else s for n, s in zip(shape, st)]
+
+
+def _cache_view(cache, like, W):
+    """(pointer, pages, page size, page stride) of a paged cache [pages, page_size, W]."""
+    if cache is None or cache.dim() != 3:
+        raise ValueError("cache must be [pages, page_size, L + R]")
+    n, P, _ = cache.shape
+    ptr, st = _view(cache, "cache", (n, P, W), like)
+    if P > 1 and st[1] != W:
+        raise ValueError("the rows of a cache page must be contiguous")
+    return ptr, n, P, st[0] if n > 1 else P * W
+
+
+def mtp_latent_append(latent, rot, cos_sin, tok_row, positions, block_table, cache, norm_w=None,
+                      eps: float = 0.0, interleaved: bool = True, q_rot=None, q_out=None,
+                      status=None, stream=None):
+    """Tokens [T, L] and [T, R] into the paged cache [pages, page_size, L + R], rotated by
+    cos_sin [max_pos, R]; q_out[T, Hq, R] = the rotated q_rot (see
+    include/libmtpspec/latent.h).  Row strides, and token and head strides, may be any
+    multiple of 8 elements."""
+    T, L = latent.shape
+    R = rot.shape[1]
+    dt = latent.dtype
+    B, max_pages = block_table.shape
+    lp, ls = _view(latent, "latent", (T, L))
+    rp, rs = _view(rot, "rot", (T, R), dt)
+    cp, pages, P, page_stride = _cache_view(cache, dt, L + R)
+    if cos_sin.dim() != 2 or cos_sin.shape[1] != R:
+        raise ValueError(f"cos_sin must be [max_pos, {R}]")
+    queries = (None, 0, 0, None, 0, 0, 0)
+    if q_rot is not None or q_out is not None:
+        if q_rot is None or q_out is None:
+            raise ValueError("q_rot and q_out go together")
+        Hq = q_rot.shape[1]
+        qp, qs = _view(q_rot, "q_rot", (T, Hq, R), dt)
+        op, os_ = _view(q_out, "q_out", (T, Hq, R), dt)
+        queries = (qp, qs[0], qs[1], op, os_[0], os_[1], Hq)
+    if norm_w is not None and norm_w.dtype != dt:
+        raise TypeError(f"norm_w must hold {dt} values, got {norm_w.dtype}")
+    _call("mtp_latent_append", lp, ls[0], rp, rs[0],
+          _arg(norm_w, "norm_w", _HALF, L, optional=True), float(eps),
+          _arg(cos_sin, "cos_sin", _F32), cos_sin.shape[0], int(bool(interleaved)),
+          _arg(tok_row, "tok_row", _I32, T), _arg(positions, "positions", _I32, T), T, L, R,
+          _arg(block_table, "block_table", _I32), B, max_pages, cp, pages, P, page_stride,
+          *queries, _HALF_CODES[dt], _arg(status, "status", _I32, 1, optional=True),
+          _stream(stream))
+    return cache
+
+
+def mtp_latent_attn_workspace_bytes(B: int, T: int, Hq: int, L: int, R: int) -> int:
+    return int(load().mtp_latent_attn_workspace_bytes(int(B), int(T), int(Hq), int(L), int(R)))
+
+
+def mtp_latent_attn(q, cache, block_table, kv_len, out, scale: float, lse=None, workspace=None,
+                    status=None, stream=None):
+    """out[B, T, Hq, L]: attention of q[B, T, Hq, L + R] over the paged cache, query t of row b
+    seeing positions below kv_len[b] - (T - 1 - t) (see include/libmtpspec/latent.h)."""
+    B, T, Hq, W = q.shape
+    L = out.shape[-1]
+    dt = q.dtype
+    qp, qs = _view(q, "q", (B, T, Hq, W))
+    op, os_ = _view(out, "out", (B, T, Hq, L), dt)
+    cp, pages, P, page_stride = _cache_view(cache, dt, W)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must be [{B}, max_pages]")
+    wp, ws = _ws(workspace)
+    _call("mtp_latent_attn", qp, qs[0], qs[1], qs[2], cp, pages, P, page_stride,
+          _arg(block_table, "block_table", _I32), block_table.shape[1],
+          _arg(kv_len, "kv_len", _I32, B), B, T, Hq, L, W - L, float(scale), op, os_[0], os_[1],
+          os_[2], _arg(lse, "lse", _F32, B * T * Hq, optional=True), _HALF_CODES[dt], wp, ws,
+          _arg(status, "status", _I32, 1, optional=True), _stream(stream))
+    return out

@@ -42,7 +42,8 @@ def _stamp() -> str:
     h = hashlib.sha256()
     files = _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh")) +
                                 glob.glob(os.path.join(CSRC, "*.h")) +
-                                [os.path.join(ROOT, "include", "libmtpspec.h")])
+                                [os.path.join(ROOT, "include", "libmtpspec.h")] +
+                                sorted(glob.glob(os.path.join(ROOT, "include", "libmtpspec", "*.h"))))
     for f in files:
         h.update(f.encode())
         with open(f, "rb") as fh:

@@ -434,3 +434,167 @@ MTPSPEC_API int spec_verify_sample_static(const void *target_logits, const void 
     a.status = status;
     return launched(mtpspec::run_verify_sample_static(a, s));
 }
+
+// ---------------------------------------------------------------- latent attention
+
+namespace {
+
+constexpr int64_t kMaxLatentRows = 1 << 20;
+constexpr int32_t kMaxHeads = 1024;
+constexpr int64_t kMaxStride = (int64_t{1} << 39) - 8;  // elements: a tensor map strides below 2^40 bytes
+
+bool is_half(int dtype) { return dtype == MTPSPEC_BF16 || dtype == MTPSPEC_F16; }
+bool latent_sizes(int32_t L, int32_t R) {
+    return L >= 64 && L <= 512 && L % 64 == 0 && R >= 16 && R <= 64 && R % 16 == 0;
+}
+bool cache_sizes(int64_t num_pages, int32_t page_size, int64_t page_stride, int64_t max_pages,
+                 int32_t row) {
+    return num_pages >= 1 && num_pages <= kMaxV && max_pages >= 1 && max_pages <= kMaxV &&
+           page_size >= 8 && page_size <= (1 << 24) && page_size % 8 == 0 &&
+           page_stride >= static_cast<int64_t>(page_size) * row && page_stride <= kMaxStride &&
+           page_stride % 8 == 0;
+}
+// A stride over `n` items of `item` elements each: 16-byte steps, and no overlap.
+bool stride_ok(int64_t stride, int64_t n, int64_t item) {
+    return stride % 8 == 0 && stride <= kMaxStride && (n <= 1 ? stride >= 0 : stride >= item);
+}
+
+}  // namespace
+
+MTPSPEC_API int mtp_latent_append(
+    const void *latent, int64_t latent_stride, const void *rot, int64_t rot_stride,
+    const void *norm_w, float eps, const float *cos_sin, int64_t max_pos, int32_t interleaved,
+    const int32_t *tok_row, const int32_t *positions, int64_t T, int32_t L, int32_t R,
+    const int32_t *block_table, int64_t B, int64_t max_pages, void *cache, int64_t num_pages,
+    int32_t page_size, int64_t page_stride, const void *q_rot, int64_t q_rot_tok_stride,
+    int64_t q_rot_head_stride, void *q_out, int64_t q_out_tok_stride, int64_t q_out_head_stride,
+    int32_t Hq, int dtype, int32_t *status, void *stream) {
+    if (!is_half(dtype)) return MTPSPEC_ERR_DTYPE;
+    if (T < 0 || T > kMaxTokens || B < 1 || B > kMaxLatentRows || max_pos < 1 || max_pos > kMaxV ||
+        !latent_sizes(L, R) || !cache_sizes(num_pages, page_size, page_stride, max_pages, L + R))
+        return MTPSPEC_ERR_SHAPE;
+    if (!stride_ok(latent_stride, T, L) || !stride_ok(rot_stride, T, R)) return MTPSPEC_ERR_SHAPE;
+    const bool queries = q_rot != nullptr || q_out != nullptr;
+    if (queries) {
+        if (!q_rot || !q_out) return MTPSPEC_ERR_ARG;
+        if (Hq < 1 || Hq > kMaxHeads || !stride_ok(q_rot_head_stride, Hq, R) ||
+            !stride_ok(q_out_head_stride, Hq, R) || !stride_ok(q_rot_tok_stride, T, R) ||
+            !stride_ok(q_out_tok_stride, T, R))
+            return MTPSPEC_ERR_SHAPE;
+    }
+    if (!(eps >= 0.0f)) return MTPSPEC_ERR_ARG;
+    if (T == 0) return MTPSPEC_OK;
+    if (!latent || !rot || !cos_sin || !tok_row || !positions || !block_table || !cache)
+        return MTPSPEC_ERR_ARG;
+    if (!aligned(latent, 16) || !aligned(rot, 16) || !aligned(norm_w, 16) || !aligned(cos_sin, 16) ||
+        !aligned(tok_row, 4) || !aligned(positions, 4) || !aligned(block_table, 4) ||
+        !aligned(cache, 16) || !aligned(q_rot, 16) || !aligned(q_out, 16) || !aligned(status, 4))
+        return MTPSPEC_ERR_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int rc = prepare_device(s);
+    if (rc != MTPSPEC_OK) return rc;
+    mtpspec::LatentAppendArgs a = {};
+    a.latent = static_cast<const uint16_t *>(latent);
+    a.rot = static_cast<const uint16_t *>(rot);
+    a.norm_w = static_cast<const uint16_t *>(norm_w);
+    a.latent_stride = latent_stride;
+    a.rot_stride = rot_stride;
+    a.eps = eps;
+    a.cos_sin = cos_sin;
+    a.interleaved = interleaved;
+    a.tok_row = tok_row;
+    a.positions = positions;
+    a.T = T;
+    a.L = L;
+    a.R = R;
+    a.block_table = block_table;
+    a.B = B;
+    a.max_pages = max_pages;
+    const int64_t slots = max_pages * page_size;
+    a.pos_end = max_pos < slots ? max_pos : slots;
+    a.cache = static_cast<uint16_t *>(cache);
+    a.num_pages = num_pages;
+    a.page_stride = page_stride;
+    a.page_size = page_size;
+    a.q_rot = static_cast<const uint16_t *>(q_rot);
+    a.q_out = static_cast<uint16_t *>(q_out);
+    a.q_rot_tok = q_rot_tok_stride;
+    a.q_rot_head = q_rot_head_stride;
+    a.q_out_tok = q_out_tok_stride;
+    a.q_out_head = q_out_head_stride;
+    a.Hq = Hq;
+    a.status = status;
+    return launched(mtpspec::run_latent_append(a, dtype, s));
+}
+
+namespace {
+
+bool attn_sizes(int64_t B, int32_t T, int32_t Hq, int32_t L, int32_t R) {
+    return B >= 0 && B <= kMaxLatentRows && T >= 1 && T <= 256 && Hq >= 1 && Hq <= kMaxHeads &&
+           static_cast<int64_t>(T) * Hq <= 65536 && B * T * Hq <= kMaxV && latent_sizes(L, R);
+}
+bool good_scale(float s) { return s > 0.0f && s - s == 0.0f; }
+
+}  // namespace
+
+MTPSPEC_API size_t mtp_latent_attn_workspace_bytes(int64_t B, int32_t T, int32_t Hq, int32_t L,
+                                                   int32_t R) {
+    if (!attn_sizes(B, T, Hq, L, R) || B == 0) return 0;
+    return mtpspec::latent_attn_workspace_bytes(B, T, Hq, L);
+}
+
+MTPSPEC_API int mtp_latent_attn(const void *q, int64_t q_row_stride, int64_t q_tok_stride,
+                                int64_t q_head_stride, const void *cache, int64_t num_pages,
+                                int32_t page_size, int64_t page_stride, const int32_t *block_table,
+                                int64_t max_pages, const int32_t *kv_len, int64_t B, int32_t T,
+                                int32_t Hq, int32_t L, int32_t R, float scale, void *out,
+                                int64_t out_row_stride, int64_t out_tok_stride,
+                                int64_t out_head_stride, float *lse, int dtype, void *workspace,
+                                size_t workspace_bytes, int32_t *status, void *stream) {
+    if (!is_half(dtype)) return MTPSPEC_ERR_DTYPE;
+    if (!attn_sizes(B, T, Hq, L, R) ||
+        !cache_sizes(num_pages, page_size, page_stride, max_pages, L + R))
+        return MTPSPEC_ERR_SHAPE;
+    if (!stride_ok(q_row_stride, B, L + R) || !stride_ok(q_tok_stride, T, L + R) ||
+        !stride_ok(q_head_stride, Hq, L + R) || !stride_ok(out_row_stride, B, L) ||
+        !stride_ok(out_tok_stride, T, L) || !stride_ok(out_head_stride, Hq, L))
+        return MTPSPEC_ERR_SHAPE;
+    if (!good_scale(scale)) return MTPSPEC_ERR_ARG;
+    if (B == 0) return MTPSPEC_OK;
+    if (!q || !cache || !block_table || !kv_len || !out) return MTPSPEC_ERR_ARG;
+    if (!aligned(q, 16) || !aligned(cache, 16) || !aligned(block_table, 4) || !aligned(kv_len, 4) ||
+        !aligned(out, 16) || !aligned(lse, 4) || !aligned(status, 4))
+        return MTPSPEC_ERR_ARG;
+    if (!workspace || workspace_bytes < mtpspec::latent_attn_workspace_bytes(B, T, Hq, L))
+        return MTPSPEC_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return MTPSPEC_ERR_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int rc = prepare_device(s);
+    if (rc != MTPSPEC_OK) return rc;
+    mtpspec::LatentAttnArgs a = {};
+    a.q = static_cast<const uint16_t *>(q);
+    a.q_row = q_row_stride;
+    a.q_tok = q_tok_stride;
+    a.q_head = q_head_stride;
+    a.cache = static_cast<const uint16_t *>(cache);
+    a.num_pages = num_pages;
+    a.page_stride = page_stride;
+    a.page_size = page_size;
+    a.block_table = block_table;
+    a.max_pages = max_pages;
+    a.kv_len = kv_len;
+    a.B = B;
+    a.T = T;
+    a.Hq = Hq;
+    a.L = L;
+    a.R = R;
+    a.scale = scale;
+    a.out = static_cast<uint16_t *>(out);
+    a.out_row = out_row_stride;
+    a.out_tok = out_tok_stride;
+    a.out_head = out_head_stride;
+    a.lse = lse;
+    a.workspace = workspace;
+    a.status = status;
+    return launched(mtpspec::run_latent_attn(a, dtype, s));
+}

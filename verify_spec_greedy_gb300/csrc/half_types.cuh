@@ -1,0 +1,49 @@
+// The 16-bit element types of the latent attention, as tags, and their conversions.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace mtpspec {
+
+struct Bf16 {
+    static constexpr uint32_t mma_format = 1;  // operand format field of kind::f16
+    static __device__ __forceinline__ float2 widen2(uint32_t v) {
+        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+    }
+    static __device__ __forceinline__ uint32_t narrow2(float a, float b) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+};
+
+struct F16 {
+    static constexpr uint32_t mma_format = 0;
+    static __device__ __forceinline__ float2 widen2(uint32_t v) {
+        return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+    }
+    static __device__ __forceinline__ uint32_t narrow2(float a, float b) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ void half8_to_float(const uint4 &v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 p = T::widen2(w[i]);
+        f[2 * i] = p.x;
+        f[2 * i + 1] = p.y;
+    }
+}
+template <typename T>
+__device__ __forceinline__ uint4 float_to_half8(const float (&f)[8]) {
+    return make_uint4(T::narrow2(f[0], f[1]), T::narrow2(f[2], f[3]), T::narrow2(f[4], f[5]),
+                      T::narrow2(f[6], f[7]));
+}
+
+}  // namespace mtpspec

@@ -209,3 +209,52 @@ size_t draft_steps_workspace_bytes(int64_t M, int64_t H, int64_t V);
 cudaError_t run_draft_steps(const DraftStepsArgs &a, cudaStream_t stream);
 
 }  // namespace mtpspec
+
+namespace mtpspec {
+
+// The draft head's latent attention (latent_append.cu, latent_attn.cu);
+// 16-bit arrays are passed as their bit patterns, strides are in elements.
+struct LatentAppendArgs {
+    const uint16_t *latent, *rot, *norm_w;  // norm_w may be nullptr
+    int64_t latent_stride, rot_stride;
+    float eps;
+    const float *cos_sin;
+    int interleaved;
+    const int32_t *tok_row, *positions;
+    int64_t T;
+    int32_t L, R;
+    const int32_t *block_table;
+    int64_t B, max_pages, pos_end;  // positions lie in [0, pos_end)
+    uint16_t *cache;
+    int64_t num_pages, page_stride;
+    int32_t page_size;
+    const uint16_t *q_rot;  // or nullptr
+    uint16_t *q_out;
+    int64_t q_rot_tok, q_rot_head, q_out_tok, q_out_head;
+    int32_t Hq;
+    int32_t *status;
+};
+cudaError_t run_latent_append(const LatentAppendArgs &a, int dtype, cudaStream_t stream);
+
+struct LatentAttnArgs {
+    const uint16_t *q;
+    int64_t q_row, q_tok, q_head;
+    const uint16_t *cache;
+    int64_t num_pages, page_stride;
+    int32_t page_size;
+    const int32_t *block_table;
+    int64_t max_pages;
+    const int32_t *kv_len;
+    int64_t B;
+    int32_t T, Hq, L, R;
+    float scale;
+    uint16_t *out;
+    int64_t out_row, out_tok, out_head;
+    float *lse;  // or nullptr
+    void *workspace;
+    int32_t *status;
+};
+size_t latent_attn_workspace_bytes(int64_t B, int32_t T, int32_t Hq, int32_t L);
+cudaError_t run_latent_attn(const LatentAttnArgs &a, int dtype, cudaStream_t stream);
+
+}  // namespace mtpspec
