@@ -401,7 +401,7 @@ uint64_t mtpspec_launch_count(void);
 }
 #endif
 
-/* The draft head's latent attention: mtp_latent_append, mtp_latent_attn. */
+/* The draft head's latent attention: mtp_latent_append, mtp_latent_attn, mtp_latent_prefill. */
 #include "libmtpspec/latent.h"
 
 #endif /* LIBMTPSPEC_H */

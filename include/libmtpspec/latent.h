@@ -106,6 +106,39 @@ int mtp_latent_attn(const void *q, int64_t q_row_stride, int64_t q_tok_stride,
 /* Bytes of device workspace mtp_latent_attn needs; 0 for sizes it would reject. */
 size_t mtp_latent_attn_workspace_bytes(int64_t B, int32_t T, int32_t Hq, int32_t L, int32_t R);
 
+/*
+ * mtp_latent_prefill — attention over whole prompts in the expanded form: the latents have
+ * been multiplied by the up-projections, which gives each head its own N key values and V
+ * values a token; the R rotated key values stay shared by the heads.  The tokens of all B
+ * sequences lie one after another: queries cu_q[b] .. cu_q[b+1] - 1 and keys cu_k[b] ..
+ * cu_k[b+1] - 1 belong to sequence b.  With nq and nk of them, query i sees the keys
+ *     j <= i + nk - nq
+ * (the sequence's last query sees every key; nk > nq is a chunk behind a cached prefix).
+ *     s_j = scale * (q[i][h][0..N) . kv[j][h][0..N) + q[i][h][N..N+R) . rot[j])
+ *     out[i][h] = sum_j softmax(s)_j kv[j][h][N..N+V),   lse[i][h] = ln sum_j e^(s_j)
+ * A query that sees nothing has out = 0 and lse = -inf; precision as in mtp_latent_attn.
+ *
+ *   q    [Tq, Hq, N + R] with token and head strides
+ *   kv   [Tk, Hq, N + V] with token and head strides (a token's key, then its value)
+ *   rot  [Tk, R], row stride rot_stride, rotated
+ *   cu_q, cu_k int32 [B + 1], not decreasing, from 0 to Tq and Tk
+ *   out  [Tq, Hq, V] with token and head strides       lse float [Tq, Hq] or NULL
+ *   status int32 [1] or NULL: MTPSPEC_STATUS_BAD_PARAM is OR-ed in for a bound out of range
+ *        or out of order (taken as the nearest good one); MTPSPEC_STATUS_TIMEOUT if a wait
+ *        gave up.
+ * N and V are 64 or 128; 16 <= R <= 64 with R % 16 == 0; 0 <= Tq, Tk <= 2^24 (Tk >= 1 when
+ * Tq > 0), 1 <= B <= 65536, 1 <= Hq <= 1024, scale finite and above
+ * 0.  Queries outside every sequence
+ * are not written.  One launch.
+ */
+int mtp_latent_prefill(const void *q, int64_t q_tok_stride, int64_t q_head_stride,
+                       const void *kv, int64_t kv_tok_stride, int64_t kv_head_stride,
+                       const void *rot, int64_t rot_stride, const int32_t *cu_q,
+                       const int32_t *cu_k, int64_t B, int64_t Tq, int64_t Tk, int32_t Hq,
+                       int32_t N, int32_t R, int32_t V, float scale, void *out,
+                       int64_t out_tok_stride, int64_t out_head_stride, float *lse, int dtype,
+                       int32_t *status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

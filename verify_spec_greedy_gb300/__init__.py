@@ -11,7 +11,7 @@ from ._binding import (  # noqa: F401
     mtp_draft_steps, mtp_draft_steps_workspace_bytes, mtp_lm_head_greedy,
     mtp_lm_head_greedy_workspace_bytes, mtp_lm_head_topk, mtp_lm_head_topk_workspace_bytes,
     mtp_state_fixup, mtp_state_snapshot,
-    mtp_latent_append, mtp_latent_attn, mtp_latent_attn_workspace_bytes,
+    mtp_latent_append, mtp_latent_attn, mtp_latent_attn_workspace_bytes, mtp_latent_prefill,
     spec_verify_greedy,
     spec_verify_sample, spec_verify_sample_static, spec_verify_workspace_bytes,
     status_string)

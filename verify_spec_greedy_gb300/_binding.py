@@ -64,6 +64,8 @@ def load():
         "mtp_latent_attn": ([p, i64, i64, i64, p, i64, i32, i64, p, i64, p, i64, i32, i32, i32, i32,
                              f32, p, i64, i64, i64, p, C.c_int, p, sz, p, p], C.c_int),
         "mtp_latent_attn_workspace_bytes": ([i64, i32, i32, i32, i32], sz),
+        "mtp_latent_prefill": ([p, i64, i64, p, i64, i64, p, i64, p, p, i64, i64, i64, i32, i32, i32,
+                                i32, f32, p, i64, i64, p, C.c_int, p, p], C.c_int),
         "mtpspec_status_string": ([C.c_int], C.c_char_p),
         "mtpspec_launch_count": ([], C.c_uint64),
         "mtpspec_selftest_wait_timeout": ([C.c_int, C.c_uint32, C.c_void_p, C.c_void_p], C.c_int),
@@ -451,4 +453,26 @@ def mtp_latent_attn(q, cache, block_table, kv_len, out, scale: float, lse=None, 
           _arg(kv_len, "kv_len", _I32, B), B, T, Hq, L, W - L, float(scale), op, os_[0], os_[1],
           os_[2], _arg(lse, "lse", _F32, B * T * Hq, optional=True), _HALF_CODES[dt], wp, ws,
           _arg(status, "status", _I32, 1, optional=True), _stream(stream))
+    return out
+
+
+def mtp_latent_prefill(q, kv, rot, cu_q, cu_k, out, scale: float, lse=None, status=None,
+                       stream=None):
+    """out[Tq, Hq, V]: attention over whole prompts, q[Tq, Hq, N + R] with kv[Tk, Hq, N + V] and
+    the heads' shared rot[Tk, R], sequences bounded by cu_q and cu_k [B + 1] (see
+    include/libmtpspec/latent.h)."""
+    Tq, Hq, D = q.shape
+    Tk, R = rot.shape
+    V = out.shape[-1]
+    N = D - R
+    dt = q.dtype
+    qp, qs = _view(q, "q", (Tq, Hq, D))
+    kp, ks = _view(kv, "kv", (Tk, Hq, N + V), dt)
+    rp, rs = _view(rot, "rot", (Tk, R), dt)
+    op, os_ = _view(out, "out", (Tq, Hq, V), dt)
+    B = cu_q.numel() - 1
+    _call("mtp_latent_prefill", qp, qs[0], qs[1], kp, ks[0], ks[1], rp, rs[0],
+          _arg(cu_q, "cu_q", _I32, B + 1), _arg(cu_k, "cu_k", _I32, B + 1), B, Tq, Tk, Hq, N, R, V,
+          float(scale), op, os_[0], os_[1], _arg(lse, "lse", _F32, Tq * Hq, optional=True),
+          _HALF_CODES[dt], _arg(status, "status", _I32, 1, optional=True), _stream(stream))
     return out

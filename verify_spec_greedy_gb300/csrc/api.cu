@@ -441,6 +441,7 @@ namespace {
 
 constexpr int64_t kMaxLatentRows = 1 << 20;
 constexpr int32_t kMaxHeads = 1024;
+constexpr int64_t kMaxPromptTokens = 1 << 24;
 constexpr int64_t kMaxStride = (int64_t{1} << 39) - 8;  // elements: a tensor map strides below 2^40 bytes
 
 bool is_half(int dtype) { return dtype == MTPSPEC_BF16 || dtype == MTPSPEC_F16; }
@@ -597,4 +598,57 @@ MTPSPEC_API int mtp_latent_attn(const void *q, int64_t q_row_stride, int64_t q_t
     a.workspace = workspace;
     a.status = status;
     return launched(mtpspec::run_latent_attn(a, dtype, s));
+}
+
+MTPSPEC_API int mtp_latent_prefill(const void *q, int64_t q_tok_stride, int64_t q_head_stride,
+                                   const void *kv, int64_t kv_tok_stride, int64_t kv_head_stride,
+                                   const void *rot, int64_t rot_stride, const int32_t *cu_q,
+                                   const int32_t *cu_k, int64_t B, int64_t Tq, int64_t Tk,
+                                   int32_t Hq, int32_t N, int32_t R, int32_t V, float scale,
+                                   void *out, int64_t out_tok_stride, int64_t out_head_stride,
+                                   float *lse, int dtype, int32_t *status, void *stream) {
+    if (!is_half(dtype)) return MTPSPEC_ERR_DTYPE;
+    if (B < 1 || B > 65536 || Tq < 0 || Tq > kMaxPromptTokens || Tk < 0 || Tk > kMaxPromptTokens ||
+        (Tq > 0 && Tk < 1) || Hq < 1 || Hq > kMaxHeads || (N != 64 && N != 128) ||
+        (V != 64 && V != 128) || R < 16 || R > 64 || R % 16 != 0)
+        return MTPSPEC_ERR_SHAPE;
+    if (!stride_ok(q_tok_stride, Tq, N + R) || !stride_ok(q_head_stride, Hq, N + R) ||
+        !stride_ok(kv_tok_stride, Tk, N + V) || !stride_ok(kv_head_stride, Hq, N + V) ||
+        !stride_ok(rot_stride, Tk, R) || !stride_ok(out_tok_stride, Tq, V) ||
+        !stride_ok(out_head_stride, Hq, V))
+        return MTPSPEC_ERR_SHAPE;
+    if (!good_scale(scale)) return MTPSPEC_ERR_ARG;
+    if (Tq == 0) return MTPSPEC_OK;
+    if (!q || !kv || !rot || !cu_q || !cu_k || !out) return MTPSPEC_ERR_ARG;
+    if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(rot, 16) || !aligned(cu_q, 4) ||
+        !aligned(cu_k, 4) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(status, 4))
+        return MTPSPEC_ERR_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int rc = prepare_device(s);
+    if (rc != MTPSPEC_OK) return rc;
+    mtpspec::LatentPrefillArgs a = {};
+    a.q = static_cast<const uint16_t *>(q);
+    a.kv = static_cast<const uint16_t *>(kv);
+    a.rot = static_cast<const uint16_t *>(rot);
+    a.q_tok = q_tok_stride;
+    a.q_head = q_head_stride;
+    a.kv_tok = kv_tok_stride;
+    a.kv_head = kv_head_stride;
+    a.rot_stride = rot_stride;
+    a.cu_q = cu_q;
+    a.cu_k = cu_k;
+    a.B = B;
+    a.Tq = Tq;
+    a.Tk = Tk;
+    a.Hq = Hq;
+    a.N = N;
+    a.R = R;
+    a.V = V;
+    a.scale = scale;
+    a.out = static_cast<uint16_t *>(out);
+    a.out_tok = out_tok_stride;
+    a.out_head = out_head_stride;
+    a.lse = lse;
+    a.status = status;
+    return launched(mtpspec::run_latent_prefill(a, dtype, s));
 }

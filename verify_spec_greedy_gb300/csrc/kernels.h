@@ -212,7 +212,7 @@ cudaError_t run_draft_steps(const DraftStepsArgs &a, cudaStream_t stream);
 
 namespace mtpspec {
 
-// The draft head's latent attention (latent_append.cu, latent_attn.cu);
+// The draft head's latent attention (latent_append.cu, latent_attn.cu, latent_prefill.cu);
 // 16-bit arrays are passed as their bit patterns, strides are in elements.
 struct LatentAppendArgs {
     const uint16_t *latent, *rot, *norm_w;  // norm_w may be nullptr
@@ -256,5 +256,19 @@ struct LatentAttnArgs {
 };
 size_t latent_attn_workspace_bytes(int64_t B, int32_t T, int32_t Hq, int32_t L);
 cudaError_t run_latent_attn(const LatentAttnArgs &a, int dtype, cudaStream_t stream);
+
+struct LatentPrefillArgs {
+    const uint16_t *q, *kv, *rot;
+    int64_t q_tok, q_head, kv_tok, kv_head, rot_stride;
+    const int32_t *cu_q, *cu_k;
+    int64_t B, Tq, Tk;
+    int32_t Hq, N, R, V;
+    float scale;
+    uint16_t *out;
+    int64_t out_tok, out_head;
+    float *lse;  // or nullptr
+    int32_t *status;
+};
+cudaError_t run_latent_prefill(const LatentPrefillArgs &a, int dtype, cudaStream_t stream);
 
 }  // namespace mtpspec

@@ -1,0 +1,508 @@
+// Attention over whole prompts in the expanded form: every head has its own N key values and
+// V values a token, and the heads share the R rotated key values of a token.
+//
+// One pass over the keys with the running maximum and sum of a softmax.  A CTA takes 256
+// queries of one head as two tiles of 128 rows: while the tensor cores work on one tile's
+// products, the other tile's softmax runs, four warps a tile and a row a thread.  Tensor
+// memory holds both tiles' scores (128 columns each, whose first half becomes the weights,
+// the left operand of the second product) and outputs.  Keys and values stream through a
+// ring of 16 KB chunks (128 tokens x 64 columns) in the order in which they are used.  The
+// shared rotated part is read from its own array, so no key is ever put together in memory.
+#include <algorithm>
+
+#include "half_types.cuh"
+#include "kernels.h"
+#include "tcgen05.cuh"
+
+namespace mtpspec {
+namespace lpf {
+
+using namespace tg;
+
+constexpr int TM = 128;            // queries of a tile
+constexpr int TN = 128;            // keys of a tile
+constexpr int CHUNK = TN * 128;    // bytes of 128 rows x 64 columns of 16 bits
+constexpr int MAX_SLOTS = 10;
+constexpr int NTHREADS = 384;      // warp 0 TMA, 1 MMA, 3 TMEM; 4-7 and 8-11 softmax
+constexpr int SMEM_MAX = 232448;   // 227 KB a CTA
+constexpr float LAZY = 8.0f;       // the running maximum may lag by a factor of 2^8
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int S_COL = 0, O_COL = 256;  // tile t: + 128 t
+constexpr uint32_t POLL_LIMIT = 1u << 25;  // polls of some 20 ns: ~1 s
+
+struct Params {
+    const int32_t *cu_q, *cu_k;
+    int B, Tq, Tk, Hq, N, R, V, slots;
+    int ranks;      // query tiles (pairs) a head has at most
+    float scale2;   // scale * log2(e), above 0
+    uint16_t *out;
+    int64_t out_tok, out_head;
+    float *lse;
+    int32_t *status;
+};
+
+struct __align__(16) Shared {
+    uint64_t full[MAX_SLOTS], empty[MAX_SLOTS];
+    uint64_t q_full, s_full[2], p_ready[2], o_done[2], v_clean, drained;
+    int scan[NTHREADS / 32];
+    int q0, k0, nq, nk, pair;  // the CTA's sequence and the pair of tiles in it
+    uint32_t tmem;
+    volatile int abort;
+};
+constexpr int SMEM_EXTRA = static_cast<int>(sizeof(Shared)) + 1024;  // and the alignment
+
+__device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity) {
+    for (uint32_t it = 0; it < POLL_LIMIT; ++it) {
+        if (mbar_poll(bar, parity)) return true;
+        if (sh.abort) return false;
+    }
+    sh.abort = 1;
+    return false;
+}
+
+// A sequence's bounds in [0, n], in order.
+__device__ __forceinline__ int2 bounds(const int32_t *cu, int b, int n, bool &bad) {
+    const int c0 = cu[b], c1 = cu[b + 1];
+    const int a = min(max(c0, 0), n), e = min(max(c1, a), n);
+    bad |= a != c0 || e != c1;
+    return make_int2(a, e);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+    mma_bf16(d, a, b, idesc, accumulate);
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// A tile whose rows are the products' K axis and whose 64-column chunks are CHUNK apart.
+__device__ __forceinline__ uint64_t smem_desc_rows_k(uint32_t addr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(CHUNK >> 4) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+template <typename T>
+__host__ __device__ constexpr uint32_t idesc_of(int n, bool b_rows_k) {
+    return (1u << 4) | (T::mma_format << 7) | (T::mma_format << 10) |
+           (static_cast<uint32_t>(b_rows_k) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(TM >> 4) << 24);
+}
+
+// The ring's next slot and the phase it is in.
+struct Slot {
+    int i = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void advance(int slots) {
+        if (++i == slots) {
+            i = 0;
+            ph ^= 1;
+        }
+    }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(NTHREADS, 1)
+k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkv,
+                 const __grid_constant__ CUtensorMap mrot, const Params p) {
+    extern __shared__ uint8_t smem_dyn[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
+    const int kc = p.N / 64 + 1, vc = p.V / 64;  // chunks of a key tile and of a value tile
+    const uint32_t q_s = smem_addr(smem), ring = q_s + 2 * kc * CHUNK;
+    Shared &sh = *reinterpret_cast<Shared *>(smem + (2 * kc + p.slots) * CHUNK);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int head = blockIdx.x / p.ranks, rank = blockIdx.x - head * p.ranks;
+
+    // ---- which pair of tiles: a scan of the sequences' pairs, one run of sequences a thread
+    {
+        const int per = (p.B + NTHREADS - 1) / NTHREADS;
+        const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
+        bool bad = false;
+        int sum = 0;
+        for (int b = b0; b < b1; ++b) {
+            const int2 q = bounds(p.cu_q, b, p.Tq, bad);
+            sum += (q.y - q.x + 2 * TM - 1) / (2 * TM);
+        }
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) sh.scan[warp] = incl;
+        if (threadIdx.x == 0) sh.pair = -1;
+        __syncthreads();
+        int at = incl - sum;
+        for (int w = 0; w < warp; ++w) at += sh.scan[w];
+        for (int b = b0; b < b1 && at <= rank; ++b) {
+            const int2 q = bounds(p.cu_q, b, p.Tq, bad);
+            const int n = (q.y - q.x + 2 * TM - 1) / (2 * TM);
+            if (rank < at + n) {
+                const int2 k = bounds(p.cu_k, b, p.Tk, bad);
+                sh.q0 = q.x;
+                sh.nq = q.y - q.x;
+                sh.k0 = k.x;
+                sh.nk = k.y - k.x;
+                sh.pair = n - 1 - (rank - at);  // the longest first
+            }
+            at += n;
+        }
+        if (blockIdx.x == 0 && p.status) {
+            for (int b = b0; b < b1; ++b) bounds(p.cu_k, b, p.Tk, bad);
+            if (bad) atomicOr(p.status, MTPSPEC_STATUS_BAD_PARAM);
+        }
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < MAX_SLOTS; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], 1);
+        }
+        mbar_init(&sh.q_full, 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&sh.s_full[t], 1);
+            mbar_init(&sh.p_ready[t], 128);
+            mbar_init(&sh.o_done[t], 1);
+        }
+        mbar_init(&sh.v_clean, 128);
+        mbar_init(&sh.drained, 1);
+        sh.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_map(&mq);
+        prefetch_map(&mkv);
+        prefetch_map(&mrot);
+    }
+    __syncthreads();
+    if (sh.pair < 0) return;  // the grid has a CTA for every pair that there might be
+    if (warp == 3) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_addr(&sh.tmem)),
+                     "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    const int nq = sh.nq, nk = sh.nk, row0 = sh.pair * 2 * TM;
+    // key tiles that a tile of queries meets; its last query sees the most
+    const auto key_tiles = [&](int t) {
+        const int first = row0 + t * TM, last = min(first + TM, nq) - 1;
+        const int seen = last + nk - nq + 1;
+        return first >= nq || seen <= 0 ? 0 : (seen + TN - 1) / TN;
+    };
+    const int n0 = key_tiles(0), n1 = key_tiles(1), n = max(n0, n1);
+    const int last = n1 >= n0 ? 1 : 0;  // the tile of queries that uses every chunk last
+    const int tail = nk % TN != 0 && nk / TN < n ? nk / TN : -1;  // the tile that keys end in
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 0) {
+            if (elect_one()) {
+                // ---- producer
+                int filled = 0;
+                if (n > 0) {
+                    mbar_expect_tx(&sh.q_full, ((n0 > 0) + (n1 > 0)) * kc * CHUNK);
+                    for (int t = 0; t < 2; ++t)
+                        if ((t ? n1 : n0) > 0)
+                            for (int c = 0; c < kc; ++c)
+                                tma_load_3d(q_s + (t * kc + c) * CHUNK, &mq, c * 64, head,
+                                            sh.q0 + row0 + t * TM, &sh.q_full);
+                }
+                Slot s;
+                s.ph = 1;
+                for (int j = 0; j < n && !sh.abort; ++j)
+                    for (int c = 0; c < kc + vc; ++c) {
+                        if (!wait(sh, &sh.empty[s.i], s.ph)) break;
+                        const uint32_t dst = ring + s.i * CHUNK;
+                        mbar_expect_tx(&sh.full[s.i], CHUNK);
+                        if (c == kc - 1)
+                            tma_load_3d(dst, &mrot, 0, 0, sh.k0 + j * TN, &sh.full[s.i]);
+                        else
+                            tma_load_3d(dst, &mkv, c < kc ? c * 64 : p.N + (c - kc) * 64, head,
+                                        sh.k0 + j * TN, &sh.full[s.i]);
+                        ++filled;
+                        s.advance(p.slots);
+                    }
+                if (sh.abort) {  // let the copies in flight land
+                    for (int i = 0; i < p.slots; ++i) {
+                        const int f = (filled + p.slots - 1 - i) / p.slots;
+                        for (uint32_t it = 0; f > 0 && it < WAIT_LIMIT; ++it)
+                            if (mbar_test(&sh.full[i], (f - 1) & 1)) break;
+                    }
+                    if (n > 0)
+                        for (uint32_t it = 0; it < WAIT_LIMIT; ++it)
+                            if (mbar_test(&sh.q_full, 0)) break;
+                }
+            }
+        } else if (warp == 1) {
+            if (elect_one() && n > 0) {
+                // ---- MMA issuer: a tile's products, then its next scores, in turn
+                constexpr uint32_t id_s = idesc_of<T>(TN, false);
+                constexpr uint32_t id_o = idesc_of<T>(128, true), id_o64 = idesc_of<T>(64, true);
+                const uint64_t qd = smem_desc_sw128(q_s), kd = smem_desc_sw128(ring);
+                const uint64_t vd = smem_desc_rows_k(ring);
+                const int rot_steps = p.R / 16;
+                const auto scores = [&](Slot k, int t) {
+                    for (int c = 0; c < kc; ++c) {
+                        if (!wait(sh, &sh.full[k.i], k.ph)) return;
+                        tc_fence_after();
+                        const uint64_t a = qd + (t * kc + c) * (CHUNK >> 4);
+                        const uint64_t b = kd + k.i * (CHUNK >> 4);
+                        const int steps = c == kc - 1 ? rot_steps : 4;
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            if (u < steps)
+                                mma_ss(tmem + S_COL + t * 128, a + 2 * u, b + 2 * u, id_s, (c | u) != 0);
+                        if (t == last) mma_commit(&sh.empty[k.i]);
+                        k.advance(p.slots);
+                    }
+                    mma_commit(&sh.s_full[t]);
+                };
+                const auto products = [&](Slot v, int t, int j) {
+                    const uint32_t a = tmem + S_COL + t * 128, d = tmem + O_COL + t * 128;
+                    if (!wait(sh, &sh.full[v.i], v.ph)) return;
+                    Slot v1 = v;
+                    v1.advance(p.slots);
+                    if (vc == 2 && !wait(sh, &sh.full[v1.i], v1.ph)) return;
+                    tc_fence_after();
+                    if (vc == 2 && v1.i == v.i + 1) {
+                        const uint64_t b = vd + v.i * (CHUNK >> 4);
+#pragma unroll
+                        for (int u = 0; u < 8; ++u)
+                            mma_ts(d, a + 8 * u, b + u * (2048 >> 4), id_o, (j | u) != 0);
+                    } else {
+                        for (int c = 0; c < vc; ++c) {  // the chunks lie at the ring's two ends
+                            const uint64_t b = vd + (c ? v1.i : v.i) * (CHUNK >> 4);
+#pragma unroll
+                            for (int u = 0; u < 8; ++u)
+                                mma_ts(d + c * 64, a + 8 * u, b + u * (2048 >> 4), id_o64, (j | u) != 0);
+                        }
+                    }
+                    if (t == last) {
+                        mma_commit(&sh.empty[v.i]);
+                        if (vc == 2) mma_commit(&sh.empty[v1.i]);
+                    }
+                };
+                Slot v, k;  // the current tile's values, the next tile's keys
+                if (wait(sh, &sh.q_full, 0)) {
+                    tc_fence_after();
+                    if (n0 > 0) scores(k, 0);
+                    if (n1 > 0) scores(k, 1);
+                }
+                for (int j = 0; j < n && !sh.abort; ++j) {
+                    v = k;
+                    for (int c = 0; c < kc; ++c) v.advance(p.slots);
+                    k = v;
+                    for (int c = 0; c < vc; ++c) k.advance(p.slots);
+                    for (int t = 0; t < 2; ++t) {
+                        const int nt = t ? n1 : n0;
+                        if (j >= nt) continue;
+                        if (!wait(sh, &sh.p_ready[t], j & 1)) break;
+                        if (j == tail && !wait(sh, &sh.v_clean, 0)) break;
+                        products(v, t, j);
+                        if (j + 1 == nt) mma_commit(&sh.o_done[t]);
+                        if (j + 1 < nt) scores(k, t);
+                    }
+                }
+                mma_commit(&sh.drained);
+                for (uint32_t it = 0; it < WAIT_LIMIT; ++it)
+                    if (mbar_test(&sh.drained, 0)) break;
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        // ---- softmax: a thread a row
+        const int t = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
+        const int nt = t ? n1 : n0;
+        const int row = row0 + t * TM + r;
+        const int limit = row + nk - nq + 1;         // keys that this row sees
+        const int sure = row0 + t * TM + nk - nq + 1;  // that every row of the tile sees
+        const uint32_t lane_bits = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t s_t = tmem + lane_bits + S_COL + t * 128, o_t = tmem + lane_bits + O_COL + t * 128;
+        float m_ref = -INFINITY, l = 0.0f;
+        for (int j = 0; j < nt; ++j) {
+            wait(sh, &sh.s_full[t], j & 1);
+            tc_fence_after();
+            uint32_t x[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(s_t + 32 * c, x[c]);
+            tmem_wait_ld();
+            if (j == tail && t == last) {
+                // value rows behind the sequence's last key: whatever follows there must not
+                // meet the zero weights.  (The slots' earlier fills are used up by now, so
+                // the phase is this fill's.)
+                Slot v;
+                for (int c = kc; c < kc + vc; ++c) {
+                    const int fill = tail * (kc + vc) + c;
+                    v.i = fill % p.slots;
+                    v.ph = (fill / p.slots) & 1;
+                    wait(sh, &sh.full[v.i], v.ph);
+                    const int z0 = nk - tail * TN;
+                    for (int i = r; i < (TN - z0) * 8; i += 128)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                         ring + v.i * CHUNK + z0 * 128 + i * 16),
+                                     "r"(0)
+                                     : "memory");
+                }
+                fence_async_smem();
+                mbar_arrive(&sh.v_clean);
+            }
+            if (j * TN + TN > sure) {
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    if (j * TN + i >= limit) x[i >> 5][i & 31] = 0xFF800000u;
+            }
+            float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+                top4[i & 3] = fmaxf(top4[i & 3], __uint_as_float(x[i >> 5][i & 31]));
+            const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * p.scale2;
+            const bool raise = top > m_ref + LAZY;
+            if (j > 0 && __any_sync(0xFFFFFFFFu, raise)) {
+                // the scores came after the products of the tile before: the output is free
+                const float f = raise ? ex2(m_ref - top) : 1.0f;
+                l *= f;
+                for (int c = 0; c < p.V; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(o_t + c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                    tmem_st32(o_t + c, o);
+                }
+            }
+            if (raise) m_ref = top;
+            const float m_use = m_ref == -INFINITY ? 0.0f : m_ref;
+            float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t w[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int k = 64 * c + 2 * i;
+                    const float e0 = ex2(fmaf(__uint_as_float(x[k >> 5][k & 31]), p.scale2, -m_use));
+                    const float e1 = ex2(fmaf(__uint_as_float(x[k >> 5][(k & 31) + 1]), p.scale2, -m_use));
+                    part[(2 * i) & 3] += e0;
+                    part[(2 * i + 1) & 3] += e1;
+                    w[i] = T::narrow2(e0, e1);
+                }
+                tmem_st32(s_t + 32 * c, w);
+            }
+            tmem_wait_st();
+            l += (part[0] + part[1]) + (part[2] + part[3]);
+            tc_fence_before();
+            mbar_arrive(&sh.p_ready[t]);
+        }
+        if (nt > 0) {
+            wait(sh, &sh.o_done[t], 0);
+            tc_fence_after();
+        }
+        const bool real = row < nq;
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        const int64_t tok = sh.q0 + row;
+        if (real && p.lse) p.lse[tok * p.Hq + head] = l > 0.0f ? (m_ref + log2f(l)) * LN2 : -INFINITY;
+        uint16_t *dst = p.out + tok * p.out_tok + head * p.out_head;
+        for (int c = 0; c < p.V; c += 32) {
+            uint32_t o[32];
+            if (nt > 0) {
+                tmem_ld32(o_t + c, o);
+                tmem_wait_ld();
+            }
+            if (!real) continue;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                float f[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) f[u] = nt > 0 ? __uint_as_float(o[8 * v + u]) * inv : 0.0f;
+                *reinterpret_cast<uint4 *>(dst + c + 8 * v) = float_to_half8<T>(f);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && sh.abort && p.status) atomicOr(p.status, MTPSPEC_STATUS_TIMEOUT);
+    if (warp == 3) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(TMEM_COLS)
+                     : "memory");
+    }
+}
+
+template <typename T>
+cudaError_t launch(const CUtensorMap &mq, const CUtensorMap &mkv, const CUtensorMap &mrot,
+                   const Params &p, cudaStream_t stream) {
+    const int smem = (2 * (p.N / 64 + 1) + p.slots) * CHUNK + SMEM_EXTRA;
+    static AttrCache attr;
+    cudaError_t e = ensure_attr(k_latent_prefill<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem, attr);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = static_cast<unsigned>(p.ranks) * p.Hq;
+    k_latent_prefill<T><<<grid, NTHREADS, smem, stream>>>(mq, mkv, mrot, p);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) count_launches(1);
+    return e;
+}
+
+// A map of [tokens, heads, cols] 16-bit values, in boxes of 128 tokens x 64 columns of a head.
+bool token_map(CUtensorMap *m, const uint16_t *ptr, int64_t tokens, int64_t heads, int64_t cols,
+               int64_t tok_stride, int64_t head_stride) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    // an axis of one element may come with any stride
+    if (heads == 1) head_stride = cols + (-cols & 7);
+    if (tokens == 1) tok_stride = head_stride * heads;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(heads),
+                          static_cast<cuuint64_t>(tokens)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_stride) * 2,
+                             static_cast<cuuint64_t>(tok_stride) * 2};
+    cuuint32_t box[3] = {64, 1, 128};
+    cuuint32_t es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(ptr), dims, strides, box,
+              es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace lpf
+
+cudaError_t run_latent_prefill(const LatentPrefillArgs &a, int dtype, cudaStream_t stream) {
+    CUtensorMap mq, mkv, mrot;
+    if (!lpf::token_map(&mq, a.q, a.Tq, a.Hq, a.N + a.R, a.q_tok, a.q_head) ||
+        !lpf::token_map(&mkv, a.kv, a.Tk, a.Hq, a.N + a.V, a.kv_tok, a.kv_head) ||
+        !lpf::token_map(&mrot, a.rot, a.Tk, 1, a.R, a.rot_stride, a.R))
+        return cudaErrorInvalidValue;
+    lpf::Params p = {};
+    p.cu_q = a.cu_q;
+    p.cu_k = a.cu_k;
+    p.B = static_cast<int>(a.B);
+    p.Tq = static_cast<int>(a.Tq);
+    p.Tk = static_cast<int>(a.Tk);
+    p.Hq = a.Hq;
+    p.N = a.N;
+    p.R = a.R;
+    p.V = a.V;
+    const int q_bytes = 2 * (a.N / 64 + 1) * lpf::CHUNK;
+    p.slots = std::min<int>(lpf::MAX_SLOTS, (lpf::SMEM_MAX - lpf::SMEM_EXTRA - q_bytes) / lpf::CHUNK);
+    p.ranks = static_cast<int>((a.Tq + 2 * lpf::TM - 1) / (2 * lpf::TM) + a.B - 1);
+    p.scale2 = a.scale * lpf::LOG2E;
+    p.out = a.out;
+    p.out_tok = a.out_tok;
+    p.out_head = a.out_head;
+    p.lse = a.lse;
+    p.status = a.status;
+    return dtype == MTPSPEC_BF16 ? lpf::launch<Bf16>(mq, mkv, mrot, p, stream)
+                                 : lpf::launch<F16>(mq, mkv, mrot, p, stream);
+}
+
+}  // namespace mtpspec
