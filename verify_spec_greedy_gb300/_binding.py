@@ -88,10 +88,20 @@ def status_string(code: int) -> str:
     return load().mtpspec_status_string(int(code)).decode()
 
 
+_raw_stream = None
+
+
 def _stream(stream):
-    import torch
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without a Stream object around it (3 us a call)
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            _raw_stream = ((lambda: raw(torch._C._cuda_getDevice())) if raw is not None else
+                           (lambda: torch.cuda.current_stream().cuda_stream))
+            torch.cuda.init()
+        return _raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -358,30 +368,47 @@ def spec_verify_sample_static(target_logits, draft_logits, draft_ids, temperatur
 
 # ---------------------------------------------------------------- latent attention
 
-_HALF_CODES = None
+# The calls below run once a layer and step of a decode loop, so their checks are made for a
+# short way through when all is well; what fails one is looked at again for its message.
+_HALF_CODES = _INT = _FLOAT = None
+
+
+def _half_codes():
+    global _HALF_CODES, _INT, _FLOAT
+    import torch
+    _INT, _FLOAT = torch.int32, torch.float32
+    _HALF_CODES = {torch.bfloat16: BF16, torch.float16: F16}
+    return _HALF_CODES
 
 
 def _view(t, name, shape, like=None):
     """(pointer, strides in elements) of a 16-bit tensor of `shape` on the GPU whose last axis
-    is contiguous; `like` gives the type it has to have."""
-    global _HALF_CODES
-    if _HALF_CODES is None:
-        import torch
-        _HALF_CODES = {torch.bfloat16: BF16, torch.float16: F16}
+    is contiguous; `like` gives the type it has to have.  An axis of one has stride 0."""
     if t is None:
         raise ValueError(f"{name} is required")
     if not isinstance(t, _kinds()["tensor"]):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype not in _HALF_CODES or (like is not None and t.dtype != like):
+    codes = _HALF_CODES or _half_codes()
+    if (t.dtype is not like) if like is not None else (t.dtype not in codes):
         raise TypeError(f"{name} must hold {like or 'bfloat16 or float16'} values, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     st = t.stride()
-    if shape[-1] > 1 and st[-1] != 1:
+    if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}'s last axis must be contiguous")
-    return t.data_ptr(), [0 if n == 1 else s for n, s in zip(shape, st)]
+    if 1 in shape:
+        st = [0 if n == 1 else s for n, s in zip(shape, st)]
+    return t.data_ptr(), st
+
+
+def _vec(t, name, dtype, kind, numel=0):
+    """As _arg, for a tensor of one type."""
+    if (t is not None and t.dtype is dtype and t.is_cuda and t.is_contiguous() and
+            t.numel() >= numel):
+        return t.data_ptr()
+    return _arg(t, name, kind, numel)
 
 
 def _cache_view(cache, like, W):
@@ -402,6 +429,7 @@ def mtp_latent_append(latent, rot, cos_sin, tok_row, positions, block_table, cac
     cos_sin [max_pos, R]; q_out[T, Hq, R] = the rotated q_rot (see
     include/libmtpspec/latent.h).  Row strides, and token and head strides, may be any
     multiple of 8 elements."""
+    codes = _HALF_CODES or _half_codes()
     T, L = latent.shape
     R = rot.shape[1]
     dt = latent.dtype
@@ -423,10 +451,10 @@ def mtp_latent_append(latent, rot, cos_sin, tok_row, positions, block_table, cac
         raise TypeError(f"norm_w must hold {dt} values, got {norm_w.dtype}")
     _call("mtp_latent_append", lp, ls[0], rp, rs[0],
           _arg(norm_w, "norm_w", _HALF, L, optional=True), float(eps),
-          _arg(cos_sin, "cos_sin", _F32), cos_sin.shape[0], int(bool(interleaved)),
-          _arg(tok_row, "tok_row", _I32, T), _arg(positions, "positions", _I32, T), T, L, R,
-          _arg(block_table, "block_table", _I32), B, max_pages, cp, pages, P, page_stride,
-          *queries, _HALF_CODES[dt], _arg(status, "status", _I32, 1, optional=True),
+          _vec(cos_sin, "cos_sin", _FLOAT, _F32), cos_sin.shape[0], 1 if interleaved else 0,
+          _vec(tok_row, "tok_row", _INT, _I32, T), _vec(positions, "positions", _INT, _I32, T), T, L,
+          R, _vec(block_table, "block_table", _INT, _I32), B, max_pages, cp, pages, P, page_stride,
+          *queries, codes[dt], _arg(status, "status", _I32, 1, optional=True),
           _stream(stream))
     return cache
 
@@ -439,6 +467,7 @@ def mtp_latent_attn(q, cache, block_table, kv_len, out, scale: float, lse=None, 
                     status=None, stream=None):
     """out[B, T, Hq, L]: attention of q[B, T, Hq, L + R] over the paged cache, query t of row b
     seeing positions below kv_len[b] - (T - 1 - t) (see include/libmtpspec/latent.h)."""
+    codes = _HALF_CODES or _half_codes()
     B, T, Hq, W = q.shape
     L = out.shape[-1]
     dt = q.dtype
@@ -449,9 +478,9 @@ def mtp_latent_attn(q, cache, block_table, kv_len, out, scale: float, lse=None, 
         raise ValueError(f"block_table must be [{B}, max_pages]")
     wp, ws = _ws(workspace)
     _call("mtp_latent_attn", qp, qs[0], qs[1], qs[2], cp, pages, P, page_stride,
-          _arg(block_table, "block_table", _I32), block_table.shape[1],
-          _arg(kv_len, "kv_len", _I32, B), B, T, Hq, L, W - L, float(scale), op, os_[0], os_[1],
-          os_[2], _arg(lse, "lse", _F32, B * T * Hq, optional=True), _HALF_CODES[dt], wp, ws,
+          _vec(block_table, "block_table", _INT, _I32), block_table.shape[1],
+          _vec(kv_len, "kv_len", _INT, _I32, B), B, T, Hq, L, W - L, float(scale), op, os_[0], os_[1],
+          os_[2], lse if lse is None else _vec(lse, "lse", _FLOAT, _F32, B * T * Hq), codes[dt], wp, ws,
           _arg(status, "status", _I32, 1, optional=True), _stream(stream))
     return out
 
@@ -461,6 +490,7 @@ def mtp_latent_prefill(q, kv, rot, cu_q, cu_k, out, scale: float, lse=None, stat
     """out[Tq, Hq, V]: attention over whole prompts, q[Tq, Hq, N + R] with kv[Tk, Hq, N + V] and
     the heads' shared rot[Tk, R], sequences bounded by cu_q and cu_k [B + 1] (see
     include/libmtpspec/latent.h)."""
+    codes = _HALF_CODES or _half_codes()
     Tq, Hq, D = q.shape
     Tk, R = rot.shape
     V = out.shape[-1]
@@ -472,7 +502,7 @@ def mtp_latent_prefill(q, kv, rot, cu_q, cu_k, out, scale: float, lse=None, stat
     op, os_ = _view(out, "out", (Tq, Hq, V), dt)
     B = cu_q.numel() - 1
     _call("mtp_latent_prefill", qp, qs[0], qs[1], kp, ks[0], ks[1], rp, rs[0],
-          _arg(cu_q, "cu_q", _I32, B + 1), _arg(cu_k, "cu_k", _I32, B + 1), B, Tq, Tk, Hq, N, R, V,
-          float(scale), op, os_[0], os_[1], _arg(lse, "lse", _F32, Tq * Hq, optional=True),
-          _HALF_CODES[dt], _arg(status, "status", _I32, 1, optional=True), _stream(stream))
+          _vec(cu_q, "cu_q", _INT, _I32, B + 1), _vec(cu_k, "cu_k", _INT, _I32, B + 1), B, Tq, Tk, Hq,
+          N, R, V, float(scale), op, os_[0], os_[1],
+          lse if lse is None else _vec(lse, "lse", _FLOAT, _F32, Tq * Hq), codes[dt], _arg(status, "status", _I32, 1, optional=True), _stream(stream))
     return out

@@ -46,7 +46,8 @@ struct Params {
     uint16_t *out;
     int64_t out_row, out_tok, out_head;
     float *lse;
-    int2 *plan;      // [B * mgroups]: first and last group of a unit
+    int4 *plan;      // [GRID]: the unit that starts in a CTA and ends in another: row, row
+                     // tile, first and last group; row -1 if there is none
     float *part;     // [2 * GRID][rows][L] fp32, normalised partial outputs
     float *part_lse; // [2 * GRID][rows], base 2
     int rows_cap;    // rows of a partial: min(64, T * Hq)
@@ -58,21 +59,32 @@ __device__ __forceinline__ int row_len(const Params &p, int b) {
     const int n = p.kv_len[b];
     return n < 0 ? 0 : static_cast<int>(n < cap ? n : cap);
 }
-__device__ __forceinline__ int row_tiles(const Params &p, int b) {
-    return (row_len(p, b) + TN - 1) / TN;
-}
+__device__ __forceinline__ int tiles_of(int len) { return (len + TN - 1) / TN; }
 
-// How many of the groups take part, and the first tile of one of them: an even cut of all
-// units' tiles laid end to end.
-__device__ __forceinline__ int active_groups(const Params &p, int64_t total) {
-    return static_cast<int>(total < p.groups ? (total > 0 ? total : 1) : p.groups);
-}
-__device__ __forceinline__ int64_t first_tile(int64_t total, int active, int g) {
-    return total * g / active;
-}
-__device__ __forceinline__ int owner(int64_t total, int active, int64_t tile) {
-    return static_cast<int>(((tile + 1) * active - 1) / total);
-}
+// An even cut of all units' tiles laid end to end: of the groups that take part, the first
+// `rem` have per + 1 tiles, the others per.
+struct Cut {
+    int64_t total, per;
+    int active, rem;
+    __device__ __forceinline__ Cut(const Params &p, int64_t tiles) : total(tiles) {
+        active = static_cast<int>(tiles < p.groups ? tiles : p.groups);
+        if (tiles <= p.groups) {
+            per = 1;
+            rem = 0;
+        } else if (tiles < (int64_t{1} << 31)) {
+            per = static_cast<uint32_t>(tiles) / static_cast<uint32_t>(active);
+            rem = static_cast<int>(tiles - per * active);
+        } else {
+            per = tiles / active;
+            rem = static_cast<int>(tiles - per * active);
+        }
+    }
+    __device__ __forceinline__ int64_t first(int g) const { return per * g + (g < rem ? g : rem); }
+    __device__ __forceinline__ int owner(int64_t tile) const {
+        const int64_t big = (per + 1) * rem;
+        return static_cast<int>(tile < big ? tile / (per + 1) : rem + (tile - big) / per);
+    }
+};
 
 // A CTA's walk over its group's tiles, unit by unit; every role walks the same way.
 struct Walk {
@@ -88,7 +100,8 @@ struct Walk {
                 if (nt != 0 && ++mg < p.mgroups) break;
                 mg = 0;
                 if (++b >= p.B) return false;
-                nt = row_tiles(p, b);
+                len = row_len(p, b);
+                nt = tiles_of(len);
             }
             const int n = static_cast<int>(left < nt - off ? left : nt - off);
             ib = b;
@@ -99,7 +112,6 @@ struct Walk {
             off += n;
             left -= n;
         } while (imt >= p.mtiles);  // a unit of fewer row tiles than CTAs
-        len = row_len(p, ib);
         return true;
     }
 };
@@ -110,9 +122,6 @@ struct __align__(16) Shared {
     uint64_t drained;
     float xm[2][4][32];
     int2 box[RING][MAX_BOXES];
-    int64_t scan[NTHREADS / 32];
-    int64_t total;
-    int start_b, start_mg, start_off, start_nt;
     uint32_t tmem;
     volatile int abort;
 };
@@ -178,21 +187,24 @@ k_latent_attn(const __grid_constant__ CUtensorMap map, const Params p) {
     Shared &sh = *reinterpret_cast<Shared *>(smem + (1 + p.stages) * stage_bytes + CHUNK);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < MAX_STAGES * MAX_GROUPS; ++i) {
-            mbar_init(&sh.full[0][0] + i, 1);
-            mbar_init(&sh.empty[0][0] + i, 1);
+    if (warp == 0) {
+        if (lane < MAX_STAGES * MAX_GROUPS) {
+            mbar_init(&sh.full[0][0] + lane, 1);
+            mbar_init(&sh.empty[0][0] + lane, 1);
+        } else if (lane == 16) {
+            mbar_init(&sh.s_full[0], 1);
+            mbar_init(&sh.s_full[1], 1);
+            mbar_init(&sh.pv_done, 1);
+            mbar_init(&sh.drained, 1);
+            sh.abort = 0;
+        } else if (lane == 17) {
+            mbar_init(&sh.p_ready, 128);
+            mbar_init(&sh.q_ready, 128);
+            mbar_init(&sh.o_empty, 128);
+        } else if (lane == 18) {
+            prefetch_map(&map);
         }
-        mbar_init(&sh.s_full[0], 1);
-        mbar_init(&sh.s_full[1], 1);
-        mbar_init(&sh.p_ready, 128);
-        mbar_init(&sh.pv_done, 1);
-        mbar_init(&sh.q_ready, 128);
-        mbar_init(&sh.o_empty, 128);
-        mbar_init(&sh.drained, 1);
-        sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        prefetch_map(&map);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -201,54 +213,56 @@ k_latent_attn(const __grid_constant__ CUtensorMap map, const Params p) {
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    // ---- where this CTA starts: a scan of the rows' tiles, one run of rows a thread
-    const int per = (p.B + NTHREADS - 1) / NTHREADS;
-    const int r0 = min(p.B, static_cast<int>(threadIdx.x) * per), r1 = min(p.B, r0 + per);
+    pdl_wait_primary();
+    // ---- where this CTA starts.  Every warp finds it by itself, from a scan of the rows'
+    // tiles with a run of rows a lane: no role waits for another's.
+    const int per_lane = (p.B + 31) / 32;
+    const int r0 = min(p.B, lane * per_lane), r1 = min(p.B, r0 + per_lane);
     int64_t sum = 0;
-    for (int b = r0; b < r1; ++b) sum += static_cast<int64_t>(row_tiles(p, b)) * p.mgroups;
-    int64_t incl = sum;
+#pragma unroll 4
+    for (int b = r0; b < r1; ++b) sum += static_cast<int64_t>(tiles_of(row_len(p, b))) * p.mgroups;
+    int64_t at = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o) incl += v;
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, at, o);
+        if (lane >= o) at += v;
     }
-    if (lane == 31) sh.scan[warp] = incl;
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    int64_t before = 0, total = 0;
-    for (int w = 0; w < NTHREADS / 32; ++w) {
-        if (w < warp) before += sh.scan[w];
-        total += sh.scan[w];
-    }
-    const int active = active_groups(p, total);
+    const int64_t total = __shfl_sync(0xFFFFFFFFu, at, 31);
+    at -= sum;
+    const Cut cut(p, total);
     const int cta = blockIdx.x, group = cta / p.gs;
-    const int64_t t0 = group < active ? first_tile(total, active, group) : total;
-    const int64_t t1 = group < active ? first_tile(total, active, group + 1) : total;
-    int64_t at = before + incl - sum;
-    if (t0 < t1 && at <= t0 && t0 < at + sum) {
-        int b = r0;
-        for (;; ++b) {
-            const int64_t n = static_cast<int64_t>(row_tiles(p, b)) * p.mgroups;
-            if (t0 < at + n) break;
-            at += n;
-        }
-        sh.start_b = b;
-        sh.start_nt = row_tiles(p, b);
-        sh.start_mg = static_cast<int>((t0 - at) / sh.start_nt);
-        sh.start_off = static_cast<int>((t0 - at) % sh.start_nt);
-    }
-    __syncthreads();
-    const uint32_t tmem = sh.tmem;
+    const int64_t t0 = group < cut.active ? cut.first(group) : total;
+    const int64_t t1 = group < cut.active ? cut.first(group + 1) : total;
     Walk w;
     w.left = t1 - t0;
     w.lane = cta - group * p.gs;
-    if (w.left > 0) {
-        w.b = sh.start_b;
-        w.mg = sh.start_mg;
-        w.off = sh.start_off;
-        w.nt = sh.start_nt;
+    {
+        const bool mine = t0 < t1 && at <= t0 && t0 < at + sum;
+        int b = r0, n = 0, in = 0;
+        if (mine)
+            for (;; ++b) {
+                n = row_len(p, b);
+                const int64_t unit_tiles = static_cast<int64_t>(tiles_of(n)) * p.mgroups;
+                if (t0 < at + unit_tiles) break;
+                at += unit_tiles;
+            }
+        in = static_cast<int>(t0 - at);  // fewer than 2^31 tiles a row
+        const unsigned who = __ballot_sync(0xFFFFFFFFu, mine);
+        const int src = who ? __ffs(who) - 1 : 0;
+        w.b = __shfl_sync(0xFFFFFFFFu, b, src);
+        w.len = __shfl_sync(0xFFFFFFFFu, n, src);
+        w.off = __shfl_sync(0xFFFFFFFFu, in, src);
+        w.nt = tiles_of(w.len);
+        w.mg = 0;
+        if (p.mgroups > 1 && w.nt > 0) {
+            w.mg = w.off / w.nt;
+            w.off -= w.mg * w.nt;
+        }
     }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
 
     if (warp == 0) {
         if (elect_one()) {
@@ -318,6 +332,7 @@ k_latent_attn(const __grid_constant__ CUtensorMap map, const Params p) {
                     }
                 }
             }
+            pdl_launch_dependents();  // the joining kernel may be set up; it waits for this one
             // after an abort, let the copies in flight land (the last fill of each barrier)
             if (sh.abort)
                 for (int j = 0; j < p.stages; ++j)
@@ -443,6 +458,24 @@ k_latent_attn(const __grid_constant__ CUtensorMap map, const Params p) {
             mbar_arrive(&sh.q_ready);
         };
         if (more) load_q(nw);
+        // ---- rows without keys, and lengths out of range, while the first keys are on their way
+        for (int b = cta; b < p.B; b += GRID) {
+            const int n = p.kv_len[b];
+            if (tid == 0 && p.status && (n < 0 || n > p.max_pages * p.page_size))
+                atomicOr(p.status, MTPSPEC_STATUS_BAD_PARAM);
+            if (row_len(p, b) > 0) continue;
+            const int row_vecs = p.L / 8;
+            for (int i = tid; i < rows_all * row_vecs; i += 128) {
+                const int mm = i / row_vecs, v = i - mm * row_vecs, tt = mm / p.Hq;
+                *reinterpret_cast<uint4 *>(p.out + b * p.out_row + tt * p.out_tok +
+                                           (mm - tt * p.Hq) * p.out_head + v * 8) =
+                    make_uint4(0, 0, 0, 0);
+            }
+            if (p.lse)
+                for (int i = tid; i < rows_all; i += 128)
+                    p.lse[static_cast<int64_t>(b) * rows_all + i] = -INFINITY;
+        }
+        int4 cut_unit = make_int4(-1, 0, 0, 0);
         while (more) {
             w = nw;
             const int m = w.imt * TM + r;
@@ -545,52 +578,66 @@ k_latent_attn(const __grid_constant__ CUtensorMap map, const Params p) {
             const bool real = m < rows_all;
             const float inv = l > 0.0f ? 1.0f / l : 0.0f;
             const float lse2 = l > 0.0f ? m_ref + log2f(l) : -INFINITY;
-            const int t = m / p.Hq, h = m - t * p.Hq;
-            const int64_t prow =
-                static_cast<int64_t>(2 * cta + (w.i0 > 0 ? 0 : 1)) * p.rows_cap + r;
             if (real && half == 0) {
                 if (!whole)
-                    p.part_lse[prow] = lse2;
+                    p.part_lse[(2 * cta + (w.i0 > 0 ? 0 : 1)) * static_cast<int64_t>(p.rows_cap) + r] =
+                        lse2;
                 else if (p.lse)
-                    p.lse[(static_cast<int64_t>(w.ib) * p.T + t) * p.Hq + h] = lse2 * LN2;
+                    p.lse[static_cast<int64_t>(w.ib) * rows_all + m] = lse2 * LN2;
             }
-            if (tid == 0 && w.i0 == 0 && w.lane == 0) {
-                // this item starts its unit: the unit's last tile is int_ - 1 tiles on
-                const int64_t last = t1 - w.left - (w.i1 - w.i0) + w.int_ - 1;
-                p.plan[static_cast<int64_t>(w.ib) * p.mgroups + w.imt / p.gs] =
-                    make_int2(group, owner(total, active, last));
-            }
+            if (w.i0 == 0 && !whole)  // the unit starts here and goes on in other groups
+                cut_unit = make_int4(w.ib, w.imt, group,
+                                     cut.owner(t1 - w.left - (w.i1 - w.i0) + w.int_ - 1));
+            // A row a thread: stores of 32 bytes, a whole sector each, where the rows allow it
+            const int t = m / p.Hq, h = m - t * p.Hq;
             uint16_t *dst = p.out + w.ib * p.out_row + t * p.out_tok + h * p.out_head;
-            float *pdst = p.part + prow * p.L;
-            for (int o = 0; o < p.L;) {
-                const int n = piece_width(p.L - o);
-                for (int c = 0; c < n / 2; c += 32) {
-                    uint32_t a[32];
-                    tmem_ld32(trow + o / 2 + c, a);
-                    tmem_wait_ld();
-                    const int col = o + half * (n / 2) + c;
-                    if (!real) continue;
-                    if (whole) {
+            float *pdst = p.part + ((2 * cta + (w.i0 > 0 ? 0 : 1)) * static_cast<int64_t>(p.rows_cap) + r) * p.L;
+            const bool sectors = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
+            uint32_t a[2][32];
+            tmem_ld32(trow, a[0]);
+            int o = 0, n = piece_width(p.L), c = 0;
+#pragma unroll 2
+            for (int i = 0; i < p.L / 64; ++i) {
+                tmem_wait_ld();
+                if (i + 1 < p.L / 64) tmem_ld32(trow + 32 * (i + 1), a[(i + 1) & 1]);
+                const int col = o + half * (n / 2) + c;
+                c += 32;
+                if (c == n / 2) {
+                    o += n;
+                    n = piece_width(p.L - o);
+                    c = 0;
+                }
+                if (!real) continue;
+                float f[32];
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            float f[8];
+                for (int k = 0; k < 32; ++k) f[k] = __uint_as_float(a[i & 1][k]) * inv;
+                if (whole) {
 #pragma unroll
-                            for (int u = 0; u < 8; ++u) f[u] = __uint_as_float(a[8 * v + u]) * inv;
-                            *reinterpret_cast<uint4 *>(dst + col + 8 * v) = float_to_half8<T>(f);
+                    for (int v = 0; v < 2; ++v) {
+                        uint32_t x[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) x[k] = T::narrow2(f[16 * v + 2 * k], f[16 * v + 2 * k + 1]);
+                        if (sectors) {
+                            st_global_32B(dst + col + 16 * v, x);
+                        } else {
+                            *reinterpret_cast<uint4 *>(dst + col + 16 * v) = make_uint4(x[0], x[1], x[2], x[3]);
+                            *reinterpret_cast<uint4 *>(dst + col + 16 * v + 8) = make_uint4(x[4], x[5], x[6], x[7]);
                         }
-                    } else {
+                    }
+                } else {
 #pragma unroll
-                        for (int v = 0; v < 8; ++v)
-                            *reinterpret_cast<float4 *>(pdst + col + 4 * v) = make_float4(
-                                __uint_as_float(a[4 * v]) * inv, __uint_as_float(a[4 * v + 1]) * inv,
-                                __uint_as_float(a[4 * v + 2]) * inv, __uint_as_float(a[4 * v + 3]) * inv);
+                    for (int v = 0; v < 4; ++v) {
+                        uint32_t x[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) x[k] = __float_as_uint(f[8 * v + k]);
+                        st_global_32B(pdst + col + 8 * v, x);
                     }
                 }
-                o += n;
             }
             tc_fence_before();
             mbar_arrive(&sh.o_empty);
         }
+        if (tid == 0) p.plan[cta] = cut_unit;
     }
     tc_fence_before();
     __syncthreads();
@@ -605,75 +652,67 @@ k_latent_attn(const __grid_constant__ CUtensorMap map, const Params p) {
     }
 }
 
-// Units cut among CTAs: each row's partial outputs, weighted by their sums, become the
-// output.  Rows of empty sequences get zeros.  One warp a row of a unit.
+// Units cut among groups: each row's partial outputs, weighted by their sums, become the
+// output.  A CTA takes one row of the unit that starts in CTA blockIdx.y of the first kernel
+// and ends in another group; a thread takes four columns of every part, eight parts in flight.
 constexpr int JOIN_THREADS = 128;
 
 template <typename T>
 __global__ void __launch_bounds__(JOIN_THREADS) k_latent_join(const Params p) {
+    __shared__ float weight[GRID];
     pdl_wait_primary();
-    const int lane = threadIdx.x & 31;
-    const int rows_all = p.T * p.Hq;
-    const int64_t m_all = static_cast<int64_t>(blockIdx.x) * (JOIN_THREADS / 32) + (threadIdx.x >> 5);
-    const int b = static_cast<int>(m_all / rows_all);
-    if (b >= p.B) return;
-    const int m = static_cast<int>(m_all - static_cast<int64_t>(b) * rows_all);
-    const int t = m / p.Hq, h = m - t * p.Hq;
-    const int n = p.kv_len[b];
-    if (p.status && m == 0 && lane == 0 && (n < 0 || n > p.max_pages * p.page_size))
-        atomicOr(p.status, MTPSPEC_STATUS_BAD_PARAM);
-    uint16_t *dst = p.out + b * p.out_row + t * p.out_tok + h * p.out_head;
-    if (row_len(p, b) == 0) {
-        for (int c = lane * 8; c < p.L; c += 256) *reinterpret_cast<uint4 *>(dst + c) = make_uint4(0, 0, 0, 0);
-        if (p.lse && lane == 0) p.lse[m_all] = -INFINITY;
-        return;
-    }
-    const int mt = m / TM, mg = mt / p.gs, r = m - mt * TM;
-    const int2 span = p.plan[static_cast<int64_t>(b) * p.mgroups + mg];
-    if (span.x == span.y) return;
-    // the partial of a group: its second slot where the unit starts, else its first
-    const auto part_row = [&](int g) {
-        const int64_t cta = static_cast<int64_t>(g) * p.gs + (mt - mg * p.gs);
-        return (2 * cta + (g == span.x)) * p.rows_cap + r;
+    const int4 u = p.plan[blockIdx.y];
+    // (what an aborted call left there is checked)
+    if (u.x < 0 || u.x >= p.B || u.y < 0 || u.y >= p.mtiles || u.z < 0 || u.w >= p.groups) return;
+    const int r = blockIdx.x, m = u.y * TM + r, rows_all = p.T * p.Hq, parts = u.w - u.z + 1;
+    if (m >= rows_all || parts < 2) return;
+    // a group's partial of this row: the second slot where the unit starts, else the first
+    const int lane_cta = u.y % p.gs;
+    const auto part_row = [&](int i) {
+        const int64_t cta = static_cast<int64_t>(u.z + i) * p.gs + lane_cta;
+        return (2 * cta + (i == 0)) * p.rows_cap + r;
     };
-    float top = -INFINITY;
-    for (int c = span.x + lane; c <= span.y; c += 32)
-        top = fmaxf(top, p.part_lse[part_row(c)]);
+    // every warp finds the row's largest sum by itself
+    const int lane = threadIdx.x & 31;
+    float top = -INFINITY, sum = 0.0f;
+    for (int i = lane; i < parts; i += 32) top = fmaxf(top, p.part_lse[part_row(i)]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    float acc[2][8] = {}, sum = 0.0f;
-    if (top > -INFINITY)
-        for (int c = span.x; c <= span.y; ++c) {
-            const int64_t row = part_row(c);
-            const float wgt = exp2f(p.part_lse[row] - top);
-            sum += wgt;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int col = lane * 8 + 256 * k;
-                if (col < p.L) {
-                    const float4 v0 = *reinterpret_cast<const float4 *>(p.part + row * p.L + col);
-                    const float4 v1 = *reinterpret_cast<const float4 *>(p.part + row * p.L + col + 4);
-                    acc[k][0] += wgt * v0.x;
-                    acc[k][1] += wgt * v0.y;
-                    acc[k][2] += wgt * v0.z;
-                    acc[k][3] += wgt * v0.w;
-                    acc[k][4] += wgt * v1.x;
-                    acc[k][5] += wgt * v1.y;
-                    acc[k][6] += wgt * v1.z;
-                    acc[k][7] += wgt * v1.w;
-                }
-            }
-        }
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int col = lane * 8 + 256 * k;
-        if (col >= p.L) continue;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) acc[k][u] *= inv;
-        *reinterpret_cast<uint4 *>(dst + col) = float_to_half8<T>(acc[k]);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    for (int i = lane; i < parts; i += 32) {
+        const float w = exp2f(p.part_lse[part_row(i)] - ref);
+        sum += w;
+        if (threadIdx.x < 32) weight[i] = w;
     }
-    if (p.lse && lane == 0) p.lse[m_all] = sum > 0.0f ? (top + log2f(sum)) * LN2 : -INFINITY;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    __syncthreads();
+    const int col = threadIdx.x * 4;
+    if (col < p.L) {
+        const float *src = p.part + col;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int i = 0; i < parts; i += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (i + k < parts) v[k] = *reinterpret_cast<const float4 *>(src + part_row(i + k) * p.L);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (i + k < parts) {
+                    const float w = weight[i + k];
+                    acc.x += w * v[k].x;
+                    acc.y += w * v[k].y;
+                    acc.z += w * v[k].z;
+                    acc.w += w * v[k].w;
+                }
+        }
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        const int t = m / p.Hq, h = m - t * p.Hq;
+        *reinterpret_cast<uint2 *>(p.out + u.x * p.out_row + t * p.out_tok + h * p.out_head + col) =
+            make_uint2(T::narrow2(acc.x * inv, acc.y * inv), T::narrow2(acc.z * inv, acc.w * inv));
+    }
+    if (p.lse && threadIdx.x == 0)
+        p.lse[static_cast<int64_t>(u.x) * rows_all + m] = sum > 0.0f ? (top + log2f(sum)) * LN2 : -INFINITY;
 }
 
 size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
@@ -682,7 +721,7 @@ struct Layout {
     size_t plan, part, lse, total;
     int mtiles, gs, mgroups, rows_cap;
 };
-Layout layout(int64_t B, int64_t rows, int32_t L) {
+Layout layout(int64_t rows, int32_t L) {
     Layout y;
     y.mtiles = static_cast<int>((rows + TM - 1) / TM);
     // CTAs that share their keys walk them side by side, so that the keys leave HBM once;
@@ -691,7 +730,7 @@ Layout layout(int64_t B, int64_t rows, int32_t L) {
     y.gs = (y.mtiles + y.mgroups - 1) / y.mgroups;
     y.rows_cap = static_cast<int>(std::min<int64_t>(rows, TM));
     y.plan = 0;
-    y.part = align256(static_cast<size_t>(B) * y.mgroups * sizeof(int2));
+    y.part = align256(GRID * sizeof(int4));
     y.lse = y.part + align256(static_cast<size_t>(2 * GRID) * y.rows_cap * L * 4);
     y.total = y.lse + align256(static_cast<size_t>(2 * GRID) * y.rows_cap * 4);
     return y;
@@ -703,17 +742,19 @@ cudaError_t launch(const CUtensorMap &map, const Params &p, cudaStream_t stream)
     static AttrCache attr;
     cudaError_t e = ensure_attr(k_latent_attn<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem, attr);
     if (e != cudaSuccess) return e;
-    k_latent_attn<T><<<GRID, NTHREADS, smem, stream>>>(map, p);
-    e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(GRID);
+    cfg.blockDim = dim3(NTHREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = pdl_attr();  // set up beside the end of whatever the stream runs before
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, k_latent_attn<T>, map, p);
     if (e != cudaSuccess) return e;
     count_launches(1);
-    const int64_t rows = static_cast<int64_t>(p.B) * p.T * p.Hq;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((rows + JOIN_THREADS / 32 - 1) / (JOIN_THREADS / 32)));
+    cfg.gridDim = dim3(p.rows_cap, p.groups * p.gs);
     cfg.blockDim = dim3(JOIN_THREADS);
-    cfg.stream = stream;
-    cfg.attrs = pdl_attr();
-    cfg.numAttrs = 1;
+    cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, k_latent_join<T>, p);
     if (e == cudaSuccess) count_launches(1);
     return e;
@@ -722,7 +763,8 @@ cudaError_t launch(const CUtensorMap &map, const Params &p, cudaStream_t stream)
 }  // namespace lat
 
 size_t latent_attn_workspace_bytes(int64_t B, int32_t T, int32_t Hq, int32_t L) {
-    return lat::layout(B, static_cast<int64_t>(T) * Hq, L).total;
+    (void)B;
+    return lat::layout(static_cast<int64_t>(T) * Hq, L).total;
 }
 
 cudaError_t run_latent_attn(const LatentAttnArgs &a, int dtype, cudaStream_t stream) {
@@ -741,7 +783,7 @@ cudaError_t run_latent_attn(const LatentAttnArgs &a, int dtype, cudaStream_t str
            boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    const lat::Layout y = lat::layout(a.B, static_cast<int64_t>(a.T) * a.Hq, a.L);
+    const lat::Layout y = lat::layout(static_cast<int64_t>(a.T) * a.Hq, a.L);
     unsigned char *ws = static_cast<unsigned char *>(a.workspace);
     lat::Params p = {};
     p.q = a.q;
@@ -772,7 +814,7 @@ cudaError_t run_latent_attn(const LatentAttnArgs &a, int dtype, cudaStream_t str
     p.out_tok = a.out_tok;
     p.out_head = a.out_head;
     p.lse = a.lse;
-    p.plan = reinterpret_cast<int2 *>(ws + y.plan);
+    p.plan = reinterpret_cast<int4 *>(ws + y.plan);
     p.part = reinterpret_cast<float *>(ws + y.part);
     p.part_lse = reinterpret_cast<float *>(ws + y.lse);
     p.rows_cap = y.rows_cap;

@@ -22,7 +22,6 @@ using namespace tg;
 constexpr int TM = 128;            // queries of a tile
 constexpr int TN = 128;            // keys of a tile
 constexpr int CHUNK = TN * 128;    // bytes of 128 rows x 64 columns of 16 bits
-constexpr int MAX_SLOTS = 10;
 constexpr int NTHREADS = 384;      // warp 0 TMA, 1 MMA, 3 TMEM; 4-7 and 8-11 softmax
 constexpr int SMEM_MAX = 232448;   // 227 KB a CTA
 constexpr float LAZY = 8.0f;       // the running maximum may lag by a factor of 2^8
@@ -43,7 +42,8 @@ struct Params {
 };
 
 struct __align__(16) Shared {
-    uint64_t full[MAX_SLOTS], empty[MAX_SLOTS];
+    // a tile's keys (rotated part included) and its values, by the tile's number mod 2
+    uint64_t k_full[2], v_full[2], k_free[2], v_free[2];
     uint64_t q_full, s_full[2], p_ready[2], o_done[2], v_clean, drained;
     int scan[NTHREADS / 32];
     int q0, k0, nq, nk, pair;  // the CTA's sequence and the pair of tiles in it
@@ -61,6 +61,12 @@ __device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity)
     return false;
 }
 
+// The bounded wait of a CTA that leaves, whatever the abort flag says.
+__device__ __forceinline__ void wait_out(uint64_t *bar, uint32_t parity) {
+    for (uint32_t it = 0; it < WAIT_LIMIT; ++it)
+        if (mbar_test(bar, parity)) return;
+}
+
 // A sequence's bounds in [0, n], in order.
 __device__ __forceinline__ int2 bounds(const int32_t *cu, int b, int n, bool &bad) {
     const int c0 = cu[b], c1 = cu[b + 1];
@@ -69,28 +75,35 @@ __device__ __forceinline__ int2 bounds(const int32_t *cu, int b, int n, bool &ba
     return make_int2(a, e);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
-    mma_bf16(d, a, b, idesc, accumulate);
+// Descriptors go about as their low words (address and leading offset); the high word is one
+// for all tiles: 8-row groups every 1024 bytes, version 1, 128-byte swizzle.
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+// Rows of the tile are the products' K axis in `rows_k` form, whose 64-column chunks are
+// CHUNK apart; else they are its M or N axis.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, bool rows_k) {
+    return ((addr & 0x3FFFFu) >> 4) | ((rows_k ? CHUNK >> 4 : 1u) << 16);
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+// D[128, n] (+)= A[128, 16] B[16, n], A from shared memory or (_ts) from tensor memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                        uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "mov.b64 da, {%1, %5};\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(DESC_HI)
         : "memory");
 }
-// A tile whose rows are the products' K axis and whose 64-column chunks are CHUNK apart.
-__device__ __forceinline__ uint64_t smem_desc_rows_k(uint32_t addr) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(CHUNK >> 4) << 16;
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;
-    d |= static_cast<uint64_t>(1) << 46;
-    d |= static_cast<uint64_t>(2) << 61;
-    return d;
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(DESC_HI)
+        : "memory");
 }
 template <typename T>
 __host__ __device__ constexpr uint32_t idesc_of(int n, bool b_rows_k) {
@@ -99,28 +112,22 @@ __host__ __device__ constexpr uint32_t idesc_of(int n, bool b_rows_k) {
            (static_cast<uint32_t>(TM >> 4) << 24);
 }
 
-// The ring's next slot and the phase it is in.
-struct Slot {
-    int i = 0;
-    uint32_t ph = 0;
-    __device__ __forceinline__ void advance(int slots) {
-        if (++i == slots) {
-            i = 0;
-            ph ^= 1;
-        }
-    }
-};
+// The slot `n` behind slot s of the ring.
+__device__ __forceinline__ int slot_behind(int s, int n, int slots) {
+    return s + n >= slots ? s + n - slots : s + n;
+}
 
-template <typename T>
+// KC, VC: the 64-column chunks of a key tile (N / 64 + 1 with the rotated one) and of a value
+// tile (V / 64).
+template <typename T, int KC, int VC>
 __global__ void __launch_bounds__(NTHREADS, 1)
 k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkv,
                  const __grid_constant__ CUtensorMap mrot, const Params p) {
     extern __shared__ uint8_t smem_dyn[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
-    const int kc = p.N / 64 + 1, vc = p.V / 64;  // chunks of a key tile and of a value tile
-    const uint32_t q_s = smem_addr(smem), ring = q_s + 2 * kc * CHUNK;
-    Shared &sh = *reinterpret_cast<Shared *>(smem + (2 * kc + p.slots) * CHUNK);
+    const uint32_t q_s = smem_addr(smem), ring = q_s + 2 * KC * CHUNK;
+    Shared &sh = *reinterpret_cast<Shared *>(smem + (2 * KC + p.slots) * CHUNK);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int head = blockIdx.x / p.ranks, rank = blockIdx.x - head * p.ranks;
 
@@ -164,12 +171,12 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         }
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < MAX_SLOTS; ++i) {
-            mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.empty[i], 1);
-        }
         mbar_init(&sh.q_full, 1);
         for (int t = 0; t < 2; ++t) {
+            mbar_init(&sh.k_full[t], 1);
+            mbar_init(&sh.v_full[t], 1);
+            mbar_init(&sh.k_free[t], 1);
+            mbar_init(&sh.v_free[t], 1);
             mbar_init(&sh.s_full[t], 1);
             mbar_init(&sh.p_ready[t], 128);
             mbar_init(&sh.o_done[t], 1);
@@ -211,114 +218,122 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         if (warp == 0) {
             if (elect_one()) {
                 // ---- producer
-                int filled = 0;
                 if (n > 0) {
-                    mbar_expect_tx(&sh.q_full, ((n0 > 0) + (n1 > 0)) * kc * CHUNK);
+                    mbar_expect_tx(&sh.q_full, ((n0 > 0) + (n1 > 0)) * KC * CHUNK);
                     for (int t = 0; t < 2; ++t)
                         if ((t ? n1 : n0) > 0)
-                            for (int c = 0; c < kc; ++c)
-                                tma_load_3d(q_s + (t * kc + c) * CHUNK, &mq, c * 64, head,
+                            for (int c = 0; c < KC; ++c)
+                                tma_load_3d(q_s + (t * KC + c) * CHUNK, &mq, c * 64, head,
                                             sh.q0 + row0 + t * TM, &sh.q_full);
                 }
-                Slot s;
-                s.ph = 1;
-                for (int j = 0; j < n && !sh.abort; ++j)
-                    for (int c = 0; c < kc + vc; ++c) {
-                        if (!wait(sh, &sh.empty[s.i], s.ph)) break;
-                        const uint32_t dst = ring + s.i * CHUNK;
-                        mbar_expect_tx(&sh.full[s.i], CHUNK);
-                        if (c == kc - 1)
-                            tma_load_3d(dst, &mrot, 0, 0, sh.k0 + j * TN, &sh.full[s.i]);
+                // The ring holds at most two tiles' chunks, so a slot's last use was in one of
+                // the two tiles before; what was waited for once is not waited for again.
+                int slot = 0, k_done = -1, v_done = -1;
+                int j = 0;
+                for (; j < n && !sh.abort; ++j) {
+#pragma unroll
+                    for (int c = 0; c < KC + VC; ++c) {
+                        const int was = j * (KC + VC) + c - p.slots;  // the chunk there before
+                        if (was >= 0) {
+                            const int wj = was < (j - 1) * (KC + VC) ? j - 2 : was < j * (KC + VC) ? j - 1 : j;
+                            const bool keys = was - wj * (KC + VC) < KC;
+                            int &done = keys ? k_done : v_done;
+                            if (wj > done) {
+                                if (!wait(sh, keys ? &sh.k_free[wj & 1] : &sh.v_free[wj & 1], (wj >> 1) & 1))
+                                    break;
+                                done = wj;
+                            }
+                        }
+                        uint64_t *bar = c < KC ? &sh.k_full[j & 1] : &sh.v_full[j & 1];
+                        if (c == 0) mbar_expect_tx(bar, KC * CHUNK);
+                        if (c == KC) mbar_expect_tx(bar, VC * CHUNK);
+                        const uint32_t dst = ring + slot * CHUNK;
+                        if (c == KC - 1)
+                            tma_load_3d(dst, &mrot, 0, 0, sh.k0 + j * TN, bar);
                         else
-                            tma_load_3d(dst, &mkv, c < kc ? c * 64 : p.N + (c - kc) * 64, head,
-                                        sh.k0 + j * TN, &sh.full[s.i]);
-                        ++filled;
-                        s.advance(p.slots);
+                            tma_load_3d(dst, &mkv, c < KC ? c * 64 : p.N + (c - KC) * 64, head,
+                                        sh.k0 + j * TN, bar);
+                        slot = slot_behind(slot, 1, p.slots);
                     }
-                if (sh.abort) {  // let the copies in flight land
-                    for (int i = 0; i < p.slots; ++i) {
-                        const int f = (filled + p.slots - 1 - i) / p.slots;
-                        for (uint32_t it = 0; f > 0 && it < WAIT_LIMIT; ++it)
-                            if (mbar_test(&sh.full[i], (f - 1) & 1)) break;
+                }
+                if (sh.abort) {
+                    // let the copies in flight land: the last two tiles' and the queries' (a
+                    // fill that was cut off never completes: its wait runs to the limit)
+                    for (int i = max(0, j - 2); i < j; ++i) {
+                        wait_out(&sh.k_full[i & 1], (i >> 1) & 1);
+                        wait_out(&sh.v_full[i & 1], (i >> 1) & 1);
                     }
-                    if (n > 0)
-                        for (uint32_t it = 0; it < WAIT_LIMIT; ++it)
-                            if (mbar_test(&sh.q_full, 0)) break;
+                    if (n > 0) wait_out(&sh.q_full, 0);
                 }
             }
         } else if (warp == 1) {
-            if (elect_one() && n > 0) {
+            if (elect_one()) {
                 // ---- MMA issuer: a tile's products, then its next scores, in turn
                 constexpr uint32_t id_s = idesc_of<T>(TN, false);
-                constexpr uint32_t id_o = idesc_of<T>(128, true), id_o64 = idesc_of<T>(64, true);
-                const uint64_t qd = smem_desc_sw128(q_s), kd = smem_desc_sw128(ring);
-                const uint64_t vd = smem_desc_rows_k(ring);
-                const int rot_steps = p.R / 16;
-                const auto scores = [&](Slot k, int t) {
-                    for (int c = 0; c < kc; ++c) {
-                        if (!wait(sh, &sh.full[k.i], k.ph)) return;
-                        tc_fence_after();
-                        const uint64_t a = qd + (t * kc + c) * (CHUNK >> 4);
-                        const uint64_t b = kd + k.i * (CHUNK >> 4);
-                        const int steps = c == kc - 1 ? rot_steps : 4;
+                constexpr uint32_t id_o = idesc_of<T>(VC * 64, true), id_o64 = idesc_of<T>(64, true);
+                const uint32_t qd = desc_lo(q_s, false), kd = desc_lo(ring, false);
+                const uint32_t vd = desc_lo(ring, true);
+                const auto scores = [&](int slot, int t) {
+                    const uint32_t d = tmem + S_COL + t * 128, a = qd + t * (KC * (CHUNK >> 4));
 #pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            if (u < steps)
-                                mma_ss(tmem + S_COL + t * 128, a + 2 * u, b + 2 * u, id_s, (c | u) != 0);
-                        if (t == last) mma_commit(&sh.empty[k.i]);
-                        k.advance(p.slots);
+                    for (int c = 0; c < KC; ++c) {
+                        const uint32_t b = kd + slot_behind(slot, c, p.slots) * (CHUNK >> 4);
+                        if (c < KC - 1 || p.R == 64) {
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                mma_ss(d, a + c * (CHUNK >> 4) + 2 * u, b + 2 * u, id_s, (c | u) != 0);
+                        } else {  // the rotated chunk's columns beyond R are zeros: not worth a step
+                            for (int u = 0; u < p.R / 16; ++u)
+                                mma_ss(d, a + c * (CHUNK >> 4) + 2 * u, b + 2 * u, id_s, 1);
+                        }
                     }
                     mma_commit(&sh.s_full[t]);
                 };
-                const auto products = [&](Slot v, int t, int j) {
+                const auto products = [&](int slot, int t, int j) {
                     const uint32_t a = tmem + S_COL + t * 128, d = tmem + O_COL + t * 128;
-                    if (!wait(sh, &sh.full[v.i], v.ph)) return;
-                    Slot v1 = v;
-                    v1.advance(p.slots);
-                    if (vc == 2 && !wait(sh, &sh.full[v1.i], v1.ph)) return;
-                    tc_fence_after();
-                    if (vc == 2 && v1.i == v.i + 1) {
-                        const uint64_t b = vd + v.i * (CHUNK >> 4);
+                    const uint32_t b = vd + slot * (CHUNK >> 4);
+                    if (VC == 1 || slot + 1 < p.slots) {
 #pragma unroll
                         for (int u = 0; u < 8; ++u)
                             mma_ts(d, a + 8 * u, b + u * (2048 >> 4), id_o, (j | u) != 0);
-                    } else {
-                        for (int c = 0; c < vc; ++c) {  // the chunks lie at the ring's two ends
-                            const uint64_t b = vd + (c ? v1.i : v.i) * (CHUNK >> 4);
+                    } else {  // the chunks lie at the ring's two ends
 #pragma unroll
-                            for (int u = 0; u < 8; ++u)
-                                mma_ts(d + c * 64, a + 8 * u, b + u * (2048 >> 4), id_o64, (j | u) != 0);
+                        for (int u = 0; u < 8; ++u) {
+                            mma_ts(d, a + 8 * u, b + u * (2048 >> 4), id_o64, (j | u) != 0);
+                            mma_ts(d + 64, a + 8 * u, vd + u * (2048 >> 4), id_o64, (j | u) != 0);
                         }
                     }
-                    if (t == last) {
-                        mma_commit(&sh.empty[v.i]);
-                        if (vc == 2) mma_commit(&sh.empty[v1.i]);
-                    }
                 };
-                Slot v, k;  // the current tile's values, the next tile's keys
-                if (wait(sh, &sh.q_full, 0)) {
+                int k = 0;  // the slot of the next tile's keys
+                if (n > 0 && wait(sh, &sh.q_full, 0) && wait(sh, &sh.k_full[0], 0)) {
                     tc_fence_after();
                     if (n0 > 0) scores(k, 0);
                     if (n1 > 0) scores(k, 1);
+                    mma_commit(&sh.k_free[0]);
                 }
                 for (int j = 0; j < n && !sh.abort; ++j) {
-                    v = k;
-                    for (int c = 0; c < kc; ++c) v.advance(p.slots);
-                    k = v;
-                    for (int c = 0; c < vc; ++c) k.advance(p.slots);
+                    const int v = slot_behind(k, KC, p.slots);
+                    k = slot_behind(v, VC, p.slots);
+                    if (!wait(sh, &sh.v_full[j & 1], (j >> 1) & 1)) break;
+                    if (j + 1 < n && !wait(sh, &sh.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1)) break;
+                    if (j == tail && !wait(sh, &sh.v_clean, 0)) break;
+#pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         const int nt = t ? n1 : n0;
                         if (j >= nt) continue;
                         if (!wait(sh, &sh.p_ready[t], j & 1)) break;
-                        if (j == tail && !wait(sh, &sh.v_clean, 0)) break;
+                        tc_fence_after();
                         products(v, t, j);
+                        if (t == last) mma_commit(&sh.v_free[j & 1]);
                         if (j + 1 == nt) mma_commit(&sh.o_done[t]);
-                        if (j + 1 < nt) scores(k, t);
+                        if (j + 1 < nt) {
+                            scores(k, t);
+                            if (t == last) mma_commit(&sh.k_free[(j + 1) & 1]);
+                        }
                     }
                 }
                 mma_commit(&sh.drained);
-                for (uint32_t it = 0; it < WAIT_LIMIT; ++it)
-                    if (mbar_test(&sh.drained, 0)) break;
+                wait_out(&sh.drained, 0);
             }
         }
     } else {
@@ -341,19 +356,15 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             tmem_wait_ld();
             if (j == tail && t == last) {
                 // value rows behind the sequence's last key: whatever follows there must not
-                // meet the zero weights.  (The slots' earlier fills are used up by now, so
-                // the phase is this fill's.)
-                Slot v;
-                for (int c = kc; c < kc + vc; ++c) {
-                    const int fill = tail * (kc + vc) + c;
-                    v.i = fill % p.slots;
-                    v.ph = (fill / p.slots) & 1;
-                    wait(sh, &sh.full[v.i], v.ph);
-                    const int z0 = nk - tail * TN;
+                // meet the zero weights.  (The barrier's fill before this one is used up by
+                // now, so the phase is this fill's.)
+                wait(sh, &sh.v_full[tail & 1], (tail >> 1) & 1);
+                const int z0 = nk - tail * TN;
+#pragma unroll
+                for (int c = KC; c < KC + VC; ++c) {
+                    const uint32_t v = ring + ((tail * (KC + VC) + c) % p.slots) * CHUNK + z0 * 128;
                     for (int i = r; i < (TN - z0) * 8; i += 128)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                         ring + v.i * CHUNK + z0 * 128 + i * 16),
-                                     "r"(0)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + i * 16), "r"(0)
                                      : "memory");
                 }
                 fence_async_smem();
@@ -387,18 +398,17 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             const float m_use = m_ref == -INFINITY ? 0.0f : m_ref;
             float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t w[32];
+            for (int c = 0; c < 4; ++c) {
+                uint32_t w[16];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int k = 64 * c + 2 * i;
-                    const float e0 = ex2(fmaf(__uint_as_float(x[k >> 5][k & 31]), p.scale2, -m_use));
-                    const float e1 = ex2(fmaf(__uint_as_float(x[k >> 5][(k & 31) + 1]), p.scale2, -m_use));
+                for (int i = 0; i < 16; ++i) {
+                    const float e0 = ex2(fmaf(__uint_as_float(x[c][2 * i]), p.scale2, -m_use));
+                    const float e1 = ex2(fmaf(__uint_as_float(x[c][2 * i + 1]), p.scale2, -m_use));
                     part[(2 * i) & 3] += e0;
                     part[(2 * i + 1) & 3] += e1;
                     w[i] = T::narrow2(e0, e1);
                 }
-                tmem_st32(s_t + 32 * c, w);
+                tmem_st16(s_t + 16 * c, w);
             }
             tmem_wait_st();
             l += (part[0] + part[1]) + (part[2] + part[3]);
@@ -441,18 +451,26 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     }
 }
 
-template <typename T>
+template <typename T, int KC, int VC>
 cudaError_t launch(const CUtensorMap &mq, const CUtensorMap &mkv, const CUtensorMap &mrot,
                    const Params &p, cudaStream_t stream) {
-    const int smem = (2 * (p.N / 64 + 1) + p.slots) * CHUNK + SMEM_EXTRA;
+    const int smem = (2 * KC + p.slots) * CHUNK + SMEM_EXTRA;
     static AttrCache attr;
-    cudaError_t e = ensure_attr(k_latent_prefill<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem, attr);
+    cudaError_t e = ensure_attr(k_latent_prefill<T, KC, VC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem, attr);
     if (e != cudaSuccess) return e;
     const unsigned grid = static_cast<unsigned>(p.ranks) * p.Hq;
-    k_latent_prefill<T><<<grid, NTHREADS, smem, stream>>>(mq, mkv, mrot, p);
+    k_latent_prefill<T, KC, VC><<<grid, NTHREADS, smem, stream>>>(mq, mkv, mrot, p);
     e = cudaGetLastError();
     if (e == cudaSuccess) count_launches(1);
     return e;
+}
+
+template <typename T>
+cudaError_t pick(const CUtensorMap &mq, const CUtensorMap &mkv, const CUtensorMap &mrot,
+                 const Params &p, cudaStream_t s) {
+    if (p.N == 128)
+        return p.V == 128 ? launch<T, 3, 2>(mq, mkv, mrot, p, s) : launch<T, 3, 1>(mq, mkv, mrot, p, s);
+    return p.V == 128 ? launch<T, 2, 2>(mq, mkv, mrot, p, s) : launch<T, 2, 1>(mq, mkv, mrot, p, s);
 }
 
 // A map of [tokens, heads, cols] 16-bit values, in boxes of 128 tokens x 64 columns of a head.
@@ -493,7 +511,8 @@ cudaError_t run_latent_prefill(const LatentPrefillArgs &a, int dtype, cudaStream
     p.R = a.R;
     p.V = a.V;
     const int q_bytes = 2 * (a.N / 64 + 1) * lpf::CHUNK;
-    p.slots = std::min<int>(lpf::MAX_SLOTS, (lpf::SMEM_MAX - lpf::SMEM_EXTRA - q_bytes) / lpf::CHUNK);
+    p.slots = std::min<int>(2 * (a.N / 64 + 1 + a.V / 64),
+                            (lpf::SMEM_MAX - lpf::SMEM_EXTRA - q_bytes) / lpf::CHUNK);
     p.ranks = static_cast<int>((a.Tq + 2 * lpf::TM - 1) / (2 * lpf::TM) + a.B - 1);
     p.scale2 = a.scale * lpf::LOG2E;
     p.out = a.out;
@@ -501,8 +520,8 @@ cudaError_t run_latent_prefill(const LatentPrefillArgs &a, int dtype, cudaStream
     p.out_head = a.out_head;
     p.lse = a.lse;
     p.status = a.status;
-    return dtype == MTPSPEC_BF16 ? lpf::launch<Bf16>(mq, mkv, mrot, p, stream)
-                                 : lpf::launch<F16>(mq, mkv, mrot, p, stream);
+    return dtype == MTPSPEC_BF16 ? lpf::pick<Bf16>(mq, mkv, mrot, p, stream)
+                                 : lpf::pick<F16>(mq, mkv, mrot, p, stream);
 }
 
 }  // namespace mtpspec
