@@ -112,6 +112,15 @@ __host__ __device__ constexpr uint32_t idesc_of(int n, bool b_rows_k) {
            (static_cast<uint32_t>(TM >> 4) << 24);
 }
 
+// Keys from `seen` on are hidden: 64 scores of a row, two halves.
+__device__ __forceinline__ void mask64(uint32_t (&a)[32], uint32_t (&b)[32], int seen) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        if (i >= seen) a[i] = 0xFF800000u;
+        if (i + 32 >= seen) b[i] = 0xFF800000u;
+    }
+}
+
 // The slot `n` behind slot s of the ring.
 __device__ __forceinline__ int slot_behind(int s, int n, int slots) {
     return s + n >= slots ? s + n - slots : s + n;
@@ -214,7 +223,7 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     const int tail = nk % TN != 0 && nk / TN < n ? nk / TN : -1;  // the tile that keys end in
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (warp == 0) {
             if (elect_one()) {
                 // ---- producer
@@ -315,7 +324,7 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                     const int v = slot_behind(k, KC, p.slots);
                     k = slot_behind(v, VC, p.slots);
                     if (!wait(sh, &sh.v_full[j & 1], (j >> 1) & 1)) break;
-                    if (j + 1 < n && !wait(sh, &sh.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1)) break;
+                    bool keys = false;  // tile j + 1's have been waited for
                     if (j == tail && !wait(sh, &sh.v_clean, 0)) break;
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
@@ -327,6 +336,8 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                         if (t == last) mma_commit(&sh.v_free[j & 1]);
                         if (j + 1 == nt) mma_commit(&sh.o_done[t]);
                         if (j + 1 < nt) {
+                            if (!keys && !wait(sh, &sh.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1)) break;
+                            keys = true;
                             scores(k, t);
                             if (t == last) mma_commit(&sh.k_free[(j + 1) & 1]);
                         }
@@ -337,7 +348,7 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---- softmax: a thread a row
         const int t = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
         const int nt = t ? n1 : n0;
@@ -350,10 +361,6 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         for (int j = 0; j < nt; ++j) {
             wait(sh, &sh.s_full[t], j & 1);
             tc_fence_after();
-            uint32_t x[4][32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(s_t + 32 * c, x[c]);
-            tmem_wait_ld();
             if (j == tail && t == last) {
                 // value rows behind the sequence's last key: whatever follows there must not
                 // meet the zero weights.  (The barrier's fill before this one is used up by
@@ -370,48 +377,61 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 fence_async_smem();
                 mbar_arrive(&sh.v_clean);
             }
-            if (j * TN + TN > sure) {
-#pragma unroll
-                for (int i = 0; i < 128; ++i)
-                    if (j * TN + i >= limit) x[i >> 5][i & 31] = 0xFF800000u;
-            }
+            const bool masked = j * TN + TN > sure;
+            uint32_t x[4][32];
+            tmem_ld32(s_t, x[0]);
+            tmem_ld32(s_t + 32, x[1]);
+            tmem_wait_ld();
+            tmem_ld32(s_t + 64, x[2]);
+            tmem_ld32(s_t + 96, x[3]);
+            if (masked) mask64(x[0], x[1], limit - j * TN);
             float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 128; ++i)
-                top4[i & 3] = fmaxf(top4[i & 3], __uint_as_float(x[i >> 5][i & 31]));
+            for (int i = 0; i < 32; ++i)
+                top4[i & 3] = max3(top4[i & 3], __uint_as_float(x[0][i]), __uint_as_float(x[1][i]));
+            tmem_wait_ld();
+            if (masked) mask64(x[2], x[3], limit - j * TN - 64);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                top4[i & 3] = max3(top4[i & 3], __uint_as_float(x[2][i]), __uint_as_float(x[3][i]));
             const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * p.scale2;
             const bool raise = top > m_ref + LAZY;
             if (j > 0 && __any_sync(0xFFFFFFFFu, raise)) {
                 // the scores came after the products of the tile before: the output is free
                 const float f = raise ? ex2(m_ref - top) : 1.0f;
                 l *= f;
-                for (int c = 0; c < p.V; c += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(o_t + c, o);
+                for (int c = 0; c < p.V; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(o_t + c, o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                    tmem_st32(o_t + c, o);
+                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                    tmem_st16(o_t + c, o);
                 }
             }
             if (raise) m_ref = top;
             const float m_use = m_ref == -INFINITY ? 0.0f : m_ref;
-            float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            const uint64_t scale_2 = pack2(p.scale2, p.scale2), minus_m = pack2(-m_use, -m_use);
+            uint64_t part[2] = {0, 0};  // two pairs of sums
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 uint32_t w[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float e0 = ex2(fmaf(__uint_as_float(x[c][2 * i]), p.scale2, -m_use));
-                    const float e1 = ex2(fmaf(__uint_as_float(x[c][2 * i + 1]), p.scale2, -m_use));
-                    part[(2 * i) & 3] += e0;
-                    part[(2 * i + 1) & 3] += e1;
+                    float e0, e1;
+                    unpack2(fma2(pack2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])),
+                                 scale_2, minus_m), e0, e1);
+                    e0 = ex2(e0);
+                    e1 = ex2(e1);
+                    part[i & 1] = add2(part[i & 1], pack2(e0, e1));
                     w[i] = T::narrow2(e0, e1);
                 }
                 tmem_st16(s_t + 16 * c, w);
             }
             tmem_wait_st();
-            l += (part[0] + part[1]) + (part[2] + part[3]);
+            float l0, l1;
+            unpack2(add2(part[0], part[1]), l0, l1);
+            l += l0 + l1;
             tc_fence_before();
             mbar_arrive(&sh.p_ready[t]);
         }
