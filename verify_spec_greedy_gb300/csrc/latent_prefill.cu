@@ -3,7 +3,7 @@
 //
 // One pass over the keys with the running maximum and sum of a softmax.  A CTA takes 256
 // queries of one head as two tiles of 128 rows: while the tensor cores work on one tile's
-// products, the other tile's softmax runs, four warps a tile and a row a thread.  Tensor
+// products, the other tile's softmax runs, eight warps a tile.  Tensor
 // memory holds both tiles' scores (128 columns each, whose first half becomes the weights,
 // the left operand of the second product) and outputs.  Keys and values stream through a
 // ring of 16 KB chunks (128 tokens x 64 columns) in the order in which they are used.  The
@@ -22,11 +22,12 @@ using namespace tg;
 constexpr int TM = 128;            // queries of a tile
 constexpr int TN = 128;            // keys of a tile
 constexpr int CHUNK = TN * 128;    // bytes of 128 rows x 64 columns of 16 bits
-constexpr int NTHREADS = 384;      // warp 0 TMA, 1 MMA, 3 TMEM; 4-7 and 8-11 softmax
+constexpr int NTHREADS = 640;      // warp 0 TMA, 1 MMA, 2 prefetch, 3 TMEM; 4-11, 12-19 softmax
 constexpr int SMEM_MAX = 232448;   // 227 KB a CTA
 constexpr float LAZY = 8.0f;       // the running maximum may lag by a factor of 2^8
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr uint32_t TMEM_COLS = 512;
+constexpr unsigned WAVE = 152;     // SMs of a GB300, one CTA each
 constexpr int S_COL = 0, O_COL = 256;  // tile t: + 128 t
 constexpr uint32_t POLL_LIMIT = 1u << 25;  // polls of some 20 ns: ~1 s
 
@@ -45,12 +46,11 @@ struct __align__(16) Shared {
     // a tile's keys (rotated part included) and its values, by the tile's number mod 2
     uint64_t k_full[2], v_full[2], k_free[2], v_free[2];
     uint64_t q_full, s_full[2], p_ready[2], o_done[2], v_clean, drained;
-    int scan[NTHREADS / 32];
-    int q0, k0, nq, nk, pair;  // the CTA's sequence and the pair of tiles in it
     uint32_t tmem;
     volatile int abort;
+    float other[2][2][TM];  // what the two threads of a row tell each other, by tile and half
 };
-constexpr int SMEM_EXTRA = static_cast<int>(sizeof(Shared)) + 1024;  // and the alignment
+constexpr int SMEM_EXTRA = static_cast<int>(sizeof(Shared));
 
 __device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity) {
     for (uint32_t it = 0; it < POLL_LIMIT; ++it) {
@@ -112,13 +112,38 @@ __host__ __device__ constexpr uint32_t idesc_of(int n, bool b_rows_k) {
            (static_cast<uint32_t>(TM >> 4) << 24);
 }
 
-// Keys from `seen` on are hidden: 64 scores of a row, two halves.
-__device__ __forceinline__ void mask64(uint32_t (&a)[32], uint32_t (&b)[32], int seen) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        if (i >= seen) a[i] = 0xFF800000u;
-        if (i + 32 >= seen) b[i] = 0xFF800000u;
+__device__ __forceinline__ int pairs_of(int2 q) { return (q.y - q.x + 2 * TM - 1) / (2 * TM); }
+
+// A CTA's sequence and the pair of query tiles in it; pair -1: none.
+struct Work {
+    int q0, nq, k0, nk, pair;
+};
+// The pair of number `rank`, for a warp whose lanes hold sequences b0 .. b1 - 1, with `at`
+// pairs before them and `sum` of their own.  A sequence's longest pair comes first.
+__device__ __forceinline__ Work find_work(const Params &p, int b0, int b1, int at, int sum, int rank) {
+    Work w = {0, 0, 0, 0, -1};
+    const bool mine = at <= rank && rank < at + sum;
+    if (mine) {
+        bool bad = false;
+        for (int b = b0; b < b1; ++b) {
+            const int2 q = bounds(p.cu_q, b, p.Tq, bad);
+            const int n = pairs_of(q);
+            if (rank < at + n) {
+                const int2 k = bounds(p.cu_k, b, p.Tk, bad);
+                w = {q.x, q.y - q.x, k.x, k.y - k.x, n - 1 - (rank - at)};
+                break;
+            }
+            at += n;
+        }
     }
+    const unsigned who = __ballot_sync(0xFFFFFFFFu, mine);
+    const int src = who ? __ffs(who) - 1 : 0;
+    w.q0 = __shfl_sync(0xFFFFFFFFu, w.q0, src);
+    w.nq = __shfl_sync(0xFFFFFFFFu, w.nq, src);
+    w.k0 = __shfl_sync(0xFFFFFFFFu, w.k0, src);
+    w.nk = __shfl_sync(0xFFFFFFFFu, w.nk, src);
+    w.pair = __shfl_sync(0xFFFFFFFFu, w.pair, src);
+    return w;
 }
 
 // The slot `n` behind slot s of the ring.
@@ -132,51 +157,50 @@ template <typename T, int KC, int VC>
 __global__ void __launch_bounds__(NTHREADS, 1)
 k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkv,
                  const __grid_constant__ CUtensorMap mrot, const Params p) {
-    extern __shared__ uint8_t smem_dyn[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's period
     const uint32_t q_s = smem_addr(smem), ring = q_s + 2 * KC * CHUNK;
     Shared &sh = *reinterpret_cast<Shared *>(smem + (2 * KC + p.slots) * CHUNK);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int head = blockIdx.x / p.ranks, rank = blockIdx.x - head * p.ranks;
 
-    // ---- which pair of tiles: a scan of the sequences' pairs, one run of sequences a thread
+    // ---- which pair of tiles.  Every warp finds it by itself, from a scan of the sequences'
+    // pairs with a run of sequences a lane.
+    Work my;
     {
-        const int per = (p.B + NTHREADS - 1) / NTHREADS;
-        const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
+        const int per = (p.B + 31) / 32;
+        const int b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
         bool bad = false;
         int sum = 0;
-        for (int b = b0; b < b1; ++b) {
-            const int2 q = bounds(p.cu_q, b, p.Tq, bad);
-            sum += (q.y - q.x + 2 * TM - 1) / (2 * TM);
-        }
-        int incl = sum;
+        for (int b = b0; b < b1; ++b) sum += pairs_of(bounds(p.cu_q, b, p.Tq, bad));
+        int at = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-            if (lane >= o) incl += v;
+            const int v = __shfl_up_sync(0xFFFFFFFFu, at, o);
+            if (lane >= o) at += v;
         }
-        if (lane == 31) sh.scan[warp] = incl;
-        if (threadIdx.x == 0) sh.pair = -1;
-        __syncthreads();
-        int at = incl - sum;
-        for (int w = 0; w < warp; ++w) at += sh.scan[w];
-        for (int b = b0; b < b1 && at <= rank; ++b) {
-            const int2 q = bounds(p.cu_q, b, p.Tq, bad);
-            const int n = (q.y - q.x + 2 * TM - 1) / (2 * TM);
-            if (rank < at + n) {
-                const int2 k = bounds(p.cu_k, b, p.Tk, bad);
-                sh.q0 = q.x;
-                sh.nq = q.y - q.x;
-                sh.k0 = k.x;
-                sh.nk = k.y - k.x;
-                sh.pair = n - 1 - (rank - at);  // the longest first
-            }
-            at += n;
-        }
-        if (blockIdx.x == 0 && p.status) {
+        at -= sum;
+        my = find_work(p, b0, b1, at, sum, rank);
+        if (blockIdx.x == 0 && p.status && warp == 0) {
             for (int b = b0; b < b1; ++b) bounds(p.cu_k, b, p.Tk, bad);
             if (bad) atomicOr(p.status, MTPSPEC_STATUS_BAD_PARAM);
+        }
+        if (my.pair < 0) return;  // the grid has a CTA for every pair that there might be
+        if (warp == 2) {
+            // The CTA that comes one wave later begins with its queries and first keys: they
+            // go to L2 now, so that it does not begin with the way from HBM.
+            const unsigned next = blockIdx.x + WAVE;
+            if (next < gridDim.x) {
+                const int h = next / p.ranks;
+                const Work w = find_work(p, b0, b1, at, sum, static_cast<int>(next) - h * p.ranks);
+                if (w.pair >= 0 && elect_one()) {
+                    for (int t = 0; t < 2; ++t)
+                        for (int c = 0; c < KC; ++c)
+                            tma_prefetch_3d(&mq, c * 64, h, w.q0 + (w.pair * 2 + t) * TM);
+                    for (int c = 0; c < KC + VC; ++c)
+                        if (c != KC - 1)
+                            tma_prefetch_3d(&mkv, c < KC ? c * 64 : p.N + (c - KC) * 64, h, w.k0);
+                }
+            }
         }
     }
     if (threadIdx.x == 0) {
@@ -187,10 +211,10 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             mbar_init(&sh.k_free[t], 1);
             mbar_init(&sh.v_free[t], 1);
             mbar_init(&sh.s_full[t], 1);
-            mbar_init(&sh.p_ready[t], 128);
+            mbar_init(&sh.p_ready[t], 256);
             mbar_init(&sh.o_done[t], 1);
         }
-        mbar_init(&sh.v_clean, 128);
+        mbar_init(&sh.v_clean, 256);
         mbar_init(&sh.drained, 1);
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -198,8 +222,6 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         prefetch_map(&mkv);
         prefetch_map(&mrot);
     }
-    __syncthreads();
-    if (sh.pair < 0) return;  // the grid has a CTA for every pair that there might be
     if (warp == 3) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_addr(&sh.tmem)),
@@ -211,7 +233,7 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    const int nq = sh.nq, nk = sh.nk, row0 = sh.pair * 2 * TM;
+    const int nq = my.nq, nk = my.nk, row0 = my.pair * 2 * TM;
     // key tiles that a tile of queries meets; its last query sees the most
     const auto key_tiles = [&](int t) {
         const int first = row0 + t * TM, last = min(first + TM, nq) - 1;
@@ -223,7 +245,6 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     const int tail = nk % TN != 0 && nk / TN < n ? nk / TN : -1;  // the tile that keys end in
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (warp == 0) {
             if (elect_one()) {
                 // ---- producer
@@ -233,7 +254,7 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                         if ((t ? n1 : n0) > 0)
                             for (int c = 0; c < KC; ++c)
                                 tma_load_3d(q_s + (t * KC + c) * CHUNK, &mq, c * 64, head,
-                                            sh.q0 + row0 + t * TM, &sh.q_full);
+                                            my.q0 + row0 + t * TM, &sh.q_full);
                 }
                 // The ring holds at most two tiles' chunks, so a slot's last use was in one of
                 // the two tiles before; what was waited for once is not waited for again.
@@ -258,10 +279,10 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                         if (c == KC) mbar_expect_tx(bar, VC * CHUNK);
                         const uint32_t dst = ring + slot * CHUNK;
                         if (c == KC - 1)
-                            tma_load_3d(dst, &mrot, 0, 0, sh.k0 + j * TN, bar);
+                            tma_load_3d(dst, &mrot, 0, 0, my.k0 + j * TN, bar);
                         else
                             tma_load_3d(dst, &mkv, c < KC ? c * 64 : p.N + (c - KC) * 64, head,
-                                        sh.k0 + j * TN, bar);
+                                        my.k0 + j * TN, bar);
                         slot = slot_behind(slot, 1, p.slots);
                     }
                 }
@@ -348,19 +369,30 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        // ---- softmax: a thread a row
-        const int t = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
+        // ---- softmax: two threads a row, 64 of a tile's 128 keys each.  (With one thread a row
+        // the chain scores - weights - products of a tile took longer than the tensor cores
+        // need for both tiles.)
+        const int t = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, r = (warp & 3) * 32 + lane;
         const int nt = t ? n1 : n0;
         const int row = row0 + t * TM + r;
-        const int limit = row + nk - nq + 1;         // keys that this row sees
+        const int limit = row + nk - nq + 1;           // keys that this row sees
         const int sure = row0 + t * TM + nk - nq + 1;  // that every row of the tile sees
         const uint32_t lane_bits = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_t = tmem + lane_bits + S_COL + t * 128, o_t = tmem + lane_bits + O_COL + t * 128;
+        const int pair_bar = 1 + t * 4 + (warp & 3);
+        // this thread's value for the row's other thread, and the other's
+        const auto swap = [&](float v) {
+            sh.other[t][half][r] = v;
+            asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+            return sh.other[t][half ^ 1][r];
+        };
         float m_ref = -INFINITY, l = 0.0f;
         for (int j = 0; j < nt; ++j) {
             wait(sh, &sh.s_full[t], j & 1);
             tc_fence_after();
+            uint32_t x[2][32];
+            tmem_ld32(s_t + half * 64, x[0]);
+            tmem_ld32(s_t + half * 64 + 32, x[1]);
             if (j == tail && t == last) {
                 // value rows behind the sequence's last key: whatever follows there must not
                 // meet the zero weights.  (The barrier's fill before this one is used up by
@@ -370,37 +402,37 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
 #pragma unroll
                 for (int c = KC; c < KC + VC; ++c) {
                     const uint32_t v = ring + ((tail * (KC + VC) + c) % p.slots) * CHUNK + z0 * 128;
-                    for (int i = r; i < (TN - z0) * 8; i += 128)
+                    for (int i = half * 128 + r; i < (TN - z0) * 8; i += 256)
                         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + i * 16), "r"(0)
                                      : "memory");
                 }
                 fence_async_smem();
                 mbar_arrive(&sh.v_clean);
             }
-            const bool masked = j * TN + TN > sure;
-            uint32_t x[4][32];
-            tmem_ld32(s_t, x[0]);
-            tmem_ld32(s_t + 32, x[1]);
             tmem_wait_ld();
-            tmem_ld32(s_t + 64, x[2]);
-            tmem_ld32(s_t + 96, x[3]);
-            if (masked) mask64(x[0], x[1], limit - j * TN);
+            if (j * TN + TN > sure) {
+                const int seen = limit - j * TN - half * 64;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    if (i >= seen) x[0][i] = 0xFF800000u;
+                    if (i + 32 >= seen) x[1][i] = 0xFF800000u;
+                }
+            }
             float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int i = 0; i < 32; ++i)
                 top4[i & 3] = max3(top4[i & 3], __uint_as_float(x[0][i]), __uint_as_float(x[1][i]));
-            tmem_wait_ld();
-            if (masked) mask64(x[2], x[3], limit - j * TN - 64);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                top4[i & 3] = max3(top4[i & 3], __uint_as_float(x[2][i]), __uint_as_float(x[3][i]));
-            const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * p.scale2;
+            const float mine = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
+            // (the second barrier of a tile is p_ready: nobody writes the next value before
+            // the products have taken both threads' weights)
+            const float top = fmaxf(mine, swap(mine)) * p.scale2;
             const bool raise = top > m_ref + LAZY;
             if (j > 0 && __any_sync(0xFFFFFFFFu, raise)) {
                 // the scores came after the products of the tile before: the output is free
                 const float f = raise ? ex2(m_ref - top) : 1.0f;
                 l *= f;
-                for (int c = 0; c < p.V; c += 16) {
+#pragma unroll
+                for (int c = half * (VC * 32); c < (half + 1) * (VC * 32); c += 16) {
                     uint32_t o[16];
                     tmem_ld16(o_t + c, o);
                     tmem_wait_ld();
@@ -414,7 +446,7 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             const uint64_t scale_2 = pack2(p.scale2, p.scale2), minus_m = pack2(-m_use, -m_use);
             uint64_t part[2] = {0, 0};  // two pairs of sums
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 2; ++c) {
                 uint32_t w[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -426,7 +458,7 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                     part[i & 1] = add2(part[i & 1], pack2(e0, e1));
                     w[i] = T::narrow2(e0, e1);
                 }
-                tmem_st16(s_t + 16 * c, w);
+                tmem_st16(s_t + half * 32 + 16 * c, w);
             }
             tmem_wait_st();
             float l0, l1;
@@ -439,25 +471,40 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             wait(sh, &sh.o_done[t], 0);
             tc_fence_after();
         }
+        l += swap(l);
         const bool real = row < nq;
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-        const int64_t tok = sh.q0 + row;
-        if (real && p.lse) p.lse[tok * p.Hq + head] = l > 0.0f ? (m_ref + log2f(l)) * LN2 : -INFINITY;
-        uint16_t *dst = p.out + tok * p.out_tok + head * p.out_head;
-        for (int c = 0; c < p.V; c += 32) {
-            uint32_t o[32];
-            if (nt > 0) {
-                tmem_ld32(o_t + c, o);
-                tmem_wait_ld();
-            }
-            if (!real) continue;
+        const int64_t tok = my.q0 + row;
+        if (real && half == 0 && p.lse)
+            p.lse[tok * p.Hq + head] = l > 0.0f ? (m_ref + log2f(l)) * LN2 : -INFINITY;
+        uint16_t *dst = p.out + tok * p.out_tok + head * p.out_head + half * (VC * 32);
+        // 32 bytes a store, a whole sector, where the rows allow it
+        const bool sectors = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
+        uint32_t o[VC][32];
+        if (nt > 0) {
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                float f[8];
+            for (int c = 0; c < VC; ++c) tmem_ld32(o_t + half * (VC * 32) + 32 * c, o[c]);
+            tmem_wait_ld();
+        }
+        if (real) {
 #pragma unroll
-                for (int u = 0; u < 8; ++u) f[u] = nt > 0 ? __uint_as_float(o[8 * v + u]) * inv : 0.0f;
-                *reinterpret_cast<uint4 *>(dst + c + 8 * v) = float_to_half8<T>(f);
-            }
+            for (int c = 0; c < VC; ++c)
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    uint32_t y[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        y[u] = nt > 0 ? T::narrow2(__uint_as_float(o[c][16 * v + 2 * u]) * inv,
+                                                   __uint_as_float(o[c][16 * v + 2 * u + 1]) * inv)
+                                      : 0u;
+                    uint16_t *d = dst + c * 32 + v * 16;
+                    if (sectors) {
+                        st_global_32B(d, y);
+                    } else {
+                        *reinterpret_cast<uint4 *>(d) = make_uint4(y[0], y[1], y[2], y[3]);
+                        *reinterpret_cast<uint4 *>(d + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+                    }
+                }
         }
     }
     tc_fence_before();
