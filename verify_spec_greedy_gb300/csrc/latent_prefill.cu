@@ -75,35 +75,26 @@ __device__ __forceinline__ int2 bounds(const int32_t *cu, int b, int n, bool &ba
     return make_int2(a, e);
 }
 
-// Descriptors go about as their low words (address and leading offset); the high word is one
-// for all tiles: 8-row groups every 1024 bytes, version 1, 128-byte swizzle.
-constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
-// Rows of the tile are the products' K axis in `rows_k` form, whose 64-column chunks are
-// CHUNK apart; else they are its M or N axis.
-__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, bool rows_k) {
-    return ((addr & 0x3FFFFu) >> 4) | ((rows_k ? CHUNK >> 4 : 1u) << 16);
-}
-// D[128, n] (+)= A[128, 16] B[16, n], A from shared memory or (_ts) from tensor memory.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+// D[128, n] (+)= A[128, 16] B[16, n], A from tensor memory.  (Descriptors stay 64-bit values
+// from end to end: put together inside the asm they cost ten instructions a product.)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                        uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "mov.b64 da, {%1, %5};\n\t"
-        "mov.b64 db, {%2, %5};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(DESC_HI)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "mov.b64 db, {%2, %5};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(DESC_HI)
-        : "memory");
+// A tile whose rows are the products' K axis and whose 64-column chunks are CHUNK apart.
+__device__ __forceinline__ uint64_t smem_desc_rows_k(uint32_t addr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(CHUNK >> 4) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
 }
 template <typename T>
 __host__ __device__ constexpr uint32_t idesc_of(int n, bool b_rows_k) {
@@ -119,18 +110,36 @@ struct Work {
     int q0, nq, k0, nk, pair;
 };
 // The pair of number `rank`, for a warp whose lanes hold sequences b0 .. b1 - 1, with `at`
-// pairs before them and `sum` of their own.  A sequence's longest pair comes first.
+// pairs before them and `sum` of their own.  Up to 32 sequences (one a lane), pairs go by
+// their place in their sequence, the furthest first; beyond, sequence by sequence.
 __device__ __forceinline__ Work find_work(const Params &p, int b0, int b1, int at, int sum, int rank) {
     Work w = {0, 0, 0, 0, -1};
-    const bool mine = at <= rank && rank < at + sum;
+    bool mine = at <= rank && rank < at + sum;
+    int pair = at + sum - 1 - rank;
+    if (p.B > 1 && p.B <= 32) {
+        mine = false;
+        pair = sum;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) pair = max(pair, __shfl_xor_sync(0xFFFFFFFFu, pair, o));
+        while (--pair >= 0) {
+            const unsigned has = __ballot_sync(0xFFFFFFFFu, sum > pair);
+            const int n = __popc(has);
+            if (rank < n) {
+                const unsigned below = has & ((1u << (threadIdx.x & 31)) - 1);
+                mine = sum > pair && __popc(below) == rank;
+                break;
+            }
+            rank -= n;
+        }
+    }
     if (mine) {
         bool bad = false;
         for (int b = b0; b < b1; ++b) {
             const int2 q = bounds(p.cu_q, b, p.Tq, bad);
             const int n = pairs_of(q);
-            if (rank < at + n) {
+            if (p.B <= 32 || rank < at + n) {
                 const int2 k = bounds(p.cu_k, b, p.Tk, bad);
-                w = {q.x, q.y - q.x, k.x, k.y - k.x, n - 1 - (rank - at)};
+                w = {q.x, q.y - q.x, k.x, k.y - k.x, p.B <= 32 ? pair : n - 1 - (rank - at)};
                 break;
             }
             at += n;
@@ -161,7 +170,9 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     const uint32_t q_s = smem_addr(smem), ring = q_s + 2 * KC * CHUNK;
     Shared &sh = *reinterpret_cast<Shared *>(smem + (2 * KC + p.slots) * CHUNK);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int head = blockIdx.x / p.ranks, rank = blockIdx.x - head * p.ranks;
+    // heads side by side, the longest pairs of all of them first: what is left at the end is
+    // short, and CTAs that share a head's keys walk them at the same time
+    const int rank = blockIdx.x / p.Hq, head = blockIdx.x - rank * p.Hq;
 
     // ---- which pair of tiles.  Every warp finds it by itself, from a scan of the sequences'
     // pairs with a run of sequences a lane.
@@ -190,8 +201,8 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             // go to L2 now, so that it does not begin with the way from HBM.
             const unsigned next = blockIdx.x + WAVE;
             if (next < gridDim.x) {
-                const int h = next / p.ranks;
-                const Work w = find_work(p, b0, b1, at, sum, static_cast<int>(next) - h * p.ranks);
+                const int nr = next / p.Hq, h = next - nr * p.Hq;
+                const Work w = find_work(p, b0, b1, at, sum, nr);
                 if (w.pair >= 0 && elect_one()) {
                     for (int t = 0; t < 2; ++t)
                         for (int c = 0; c < KC; ++c)
@@ -301,27 +312,28 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 // ---- MMA issuer: a tile's products, then its next scores, in turn
                 constexpr uint32_t id_s = idesc_of<T>(TN, false);
                 constexpr uint32_t id_o = idesc_of<T>(VC * 64, true), id_o64 = idesc_of<T>(64, true);
-                const uint32_t qd = desc_lo(q_s, false), kd = desc_lo(ring, false);
-                const uint32_t vd = desc_lo(ring, true);
+                const uint64_t qd = smem_desc_sw128(q_s), kd = smem_desc_sw128(ring);
+                const uint64_t vd = smem_desc_rows_k(ring);
                 const auto scores = [&](int slot, int t) {
-                    const uint32_t d = tmem + S_COL + t * 128, a = qd + t * (KC * (CHUNK >> 4));
+                    const uint32_t d = tmem + S_COL + t * 128;
+                    const uint64_t a = qd + t * (KC * (CHUNK >> 4));
 #pragma unroll
                     for (int c = 0; c < KC; ++c) {
-                        const uint32_t b = kd + slot_behind(slot, c, p.slots) * (CHUNK >> 4);
+                        const uint64_t b = kd + slot_behind(slot, c, p.slots) * (CHUNK >> 4);
                         if (c < KC - 1 || p.R == 64) {
 #pragma unroll
                             for (int u = 0; u < 4; ++u)
-                                mma_ss(d, a + c * (CHUNK >> 4) + 2 * u, b + 2 * u, id_s, (c | u) != 0);
+                                mma_bf16(d, a + c * (CHUNK >> 4) + 2 * u, b + 2 * u, id_s, (c | u) != 0);
                         } else {  // the rotated chunk's columns beyond R are zeros: not worth a step
                             for (int u = 0; u < p.R / 16; ++u)
-                                mma_ss(d, a + c * (CHUNK >> 4) + 2 * u, b + 2 * u, id_s, 1);
+                                mma_bf16(d, a + c * (CHUNK >> 4) + 2 * u, b + 2 * u, id_s, 1);
                         }
                     }
                     mma_commit(&sh.s_full[t]);
                 };
                 const auto products = [&](int slot, int t, int j) {
                     const uint32_t a = tmem + S_COL + t * 128, d = tmem + O_COL + t * 128;
-                    const uint32_t b = vd + slot * (CHUNK >> 4);
+                    const uint64_t b = vd + slot * (CHUNK >> 4);
                     if (VC == 1 || slot + 1 < p.slots) {
 #pragma unroll
                         for (int u = 0; u < 8; ++u)
@@ -393,7 +405,7 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             uint32_t x[2][32];
             tmem_ld32(s_t + half * 64, x[0]);
             tmem_ld32(s_t + half * 64 + 32, x[1]);
-            if (j == tail && t == last) {
+            if (__builtin_expect(j == tail && t == last, 0)) {
                 // value rows behind the sequence's last key: whatever follows there must not
                 // meet the zero weights.  (The barrier's fill before this one is used up by
                 // now, so the phase is this fill's.)
@@ -410,7 +422,7 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 mbar_arrive(&sh.v_clean);
             }
             tmem_wait_ld();
-            if (j * TN + TN > sure) {
+            if (__builtin_expect(j * TN + TN > sure, 0)) {
                 const int seen = limit - j * TN - half * 64;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
@@ -427,7 +439,7 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             // the products have taken both threads' weights)
             const float top = fmaxf(mine, swap(mine)) * p.scale2;
             const bool raise = top > m_ref + LAZY;
-            if (j > 0 && __any_sync(0xFFFFFFFFu, raise)) {
+            if (__builtin_expect(j > 0 && __any_sync(0xFFFFFFFFu, raise), 0)) {
                 // the scores came after the products of the tile before: the output is free
                 const float f = raise ? ex2(m_ref - top) : 1.0f;
                 l *= f;
