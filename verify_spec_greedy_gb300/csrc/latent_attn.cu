@@ -19,8 +19,8 @@ using namespace tg;
 constexpr int TM = 64;            // (token, head) rows of a unit
 constexpr int TN = 64;            // keys of a tile
 constexpr int CHUNK = TN * 128;   // bytes of 64 rows x 64 columns of 16 bits
-constexpr int MAX_STAGES = 4;
-constexpr int MAX_GROUPS = 4;     // the rotated chunk, then pieces of 256, 128 and 64 columns
+constexpr int MAX_SLOTS = 8;      // the ring of the latents' pieces
+constexpr int MAX_ROT_SLOTS = 4;  // and the one of the rotated parts
 constexpr int MAX_BOXES = 8;      // boxes of a tile's chunk: pages of at least eight rows
 constexpr int RING = 2;           // tiles whose boxes are known: the current and the next
 constexpr int NTHREADS = 192;     // warp 0 TMA, warp 1 MMA and TMEM, warps 2-5 softmax
@@ -29,8 +29,7 @@ constexpr int GRID = 152;         // one CTA per SM of a GB300
 constexpr float LAZY = 8.0f;      // the running maximum may lag by a factor of 2^8
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr uint32_t POLL_LIMIT = 1u << 25;  // polls of some 20 ns: ~1 s
-constexpr int S_COL = 256;        // TMEM columns: output 0 .. L/2 - 1, scores 2 x 32 from here
-constexpr uint32_t TMEM_COLS = 512;
+constexpr int TMEM_COLS = 512;    // output L/2, then scores 2 x 32
 
 struct Params {
     const uint16_t *q;
@@ -38,7 +37,7 @@ struct Params {
     const int32_t *block_table, *kv_len;
     int64_t max_pages;
     int num_pages, page_size, box_rows;
-    int B, T, Hq, L, R, stages;
+    int B, T, Hq, L, R;
     int mtiles;          // row tiles of a sequence
     int gs, mgroups;     // CTAs that walk the same keys, one row tile each; such groups a sequence
     int groups;          // groups of CTAs in the grid
@@ -117,7 +116,7 @@ struct Walk {
 };
 
 struct __align__(16) Shared {
-    uint64_t full[MAX_STAGES][MAX_GROUPS], empty[MAX_STAGES][MAX_GROUPS];
+    uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], rot_full[MAX_ROT_SLOTS], rot_empty[MAX_ROT_SLOTS];
     uint64_t s_full[2], p_ready, pv_done, q_ready, o_empty;
     uint64_t drained;
     float xm[2][4][32];
@@ -127,7 +126,7 @@ struct __align__(16) Shared {
 };
 
 constexpr int SMEM_MAX = 232448;                                        // 227 KB a CTA
-constexpr int SMEM_EXTRA = static_cast<int>(sizeof(Shared)) + 1024;    // and the alignment
+constexpr int SMEM_EXTRA = static_cast<int>(sizeof(Shared));
 
 // A bounded wait; once any wait of the CTA has given up, the others return at once, and the
 // roles run to their ends without touching what they could not wait for.
@@ -138,6 +137,12 @@ __device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity)
     }
     sh.abort = 1;
     return false;
+}
+
+// Of a CTA that leaves after an abort: the last of a barrier's `fills` lands, or the limit.
+__device__ __forceinline__ void wait_out(uint64_t *bar, int fills) {
+    for (uint32_t it = 0; fills > 0 && it < WAIT_LIMIT; ++it)
+        if (mbar_test(bar, (fills - 1) & 1)) return;
 }
 
 // D[64, n] (+)= A[64, 16] B[16, n] with the 64 rows' accumulator folded into 128 lanes: lanes
@@ -169,28 +174,73 @@ __host__ __device__ constexpr uint32_t idesc_of(int n, bool b_rows_k) {
            (static_cast<uint32_t>(TM >> 4) << 24);
 }
 
-// The output's columns in pieces of 256, 128 and 64 (the widths of the folded accumulator).
-__device__ __forceinline__ int piece_width(int left) {
-    return left >= 256 ? 256 : (left >= 128 ? 128 : 64);
+// What follows from L = 64 NL alone.  The output's columns come in pieces of 256, 128 and 64
+// (the widths of the folded accumulator); a slot of the latents' ring holds one piece.
+template <int NL>
+struct Sizes {
+    static constexpr int L = 64 * NL, CHUNKS = NL + 1;  // with the rotated chunk
+    static constexpr int PIECES = (NL >> 2) + ((NL >> 1) & 1) + (NL & 1);
+    static __host__ __device__ constexpr int first(int k) {  // piece k's first chunk
+        return k < (NL >> 2) ? 4 * k : (k == (NL >> 2) && ((NL >> 1) & 1) ? (NL & ~3) : (NL & ~1));
+    }
+    static __host__ __device__ constexpr int width(int k) {  // its chunks
+        return k < (NL >> 2) ? 4 : (k == (NL >> 2) && ((NL >> 1) & 1) ? 2 : 1);
+    }
+    static constexpr int UNIT = width(0);
+    static constexpr int ROT_SLOTS = NL < 7 ? 4 : 2;
+    static constexpr int LEFT = SMEM_MAX - SMEM_EXTRA - (CHUNKS + 1 + ROT_SLOTS) * CHUNK;
+    static constexpr int SLOTS = LEFT / (UNIT * CHUNK) < MAX_SLOTS ? LEFT / (UNIT * CHUNK) : MAX_SLOTS;
+    static constexpr int SLOT_BYTES = UNIT * CHUNK;
+    static constexpr int S_COL = L / 2;  // tensor memory: behind the output
+    static constexpr int SMEM = (CHUNKS + 1 + ROT_SLOTS) * CHUNK + SLOTS * SLOT_BYTES + SMEM_EXTRA;
+    static_assert(SLOTS > PIECES, "a tile and the start of the next");
+};
+
+// The cache's maps.  `wide` and `one` see a row's latents as L / 64 chunks of 64 values, so
+// that one copy brings four chunks (or one) of a box's rows, chunk by chunk, as the products
+// want them; `rot` brings the 64 columns from L on, zeros beyond the row's end.
+struct Maps {
+    CUtensorMap wide, one, rot;
+};
+template <typename Z>
+__device__ __forceinline__ void piece_load(const Maps &m, int k, uint32_t dst, int box, int box_rows,
+                                           int row, int page, uint64_t *bar) {
+    if (Z::width(k) == 4 && box_rows == TN) {
+        tma_load_4d(dst, &m.wide, 0, row, Z::first(k), page, bar);
+    } else {
+        // (a box of fewer rows than a tile would put its chunks too close together)
+#pragma unroll
+        for (int c = 0; c < Z::width(k); ++c)
+            tma_load_4d(dst + c * CHUNK + box * box_rows * 128, &m.one, 0, row, Z::first(k) + c, page, bar);
+    }
+}
+template <typename Z>
+__device__ __forceinline__ void piece_prefetch(const Maps &m, int k, int box_rows, int row, int page) {
+    if (Z::width(k) == 4 && box_rows == TN) {
+        tma_prefetch_4d(&m.wide, 0, row, Z::first(k), page);
+    } else {
+#pragma unroll
+        for (int c = 0; c < Z::width(k); ++c) tma_prefetch_4d(&m.one, 0, row, Z::first(k) + c, page);
+    }
 }
 
-template <typename T>
+template <typename T, int NL>
 __global__ void __launch_bounds__(NTHREADS, 1)
-k_latent_attn(const __grid_constant__ CUtensorMap map, const Params p) {
-    extern __shared__ uint8_t smem_dyn[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
-    const int nchunks = p.L / 64 + 1;
-    const uint32_t base = smem_addr(smem);
-    const uint32_t q_s = base, p_s = base + nchunks * CHUNK, kv_s = p_s + CHUNK;
-    const int stage_bytes = nchunks * CHUNK;
-    Shared &sh = *reinterpret_cast<Shared *>(smem + (1 + p.stages) * stage_bytes + CHUNK);
+k_latent_attn(const __grid_constant__ Maps maps, const Params p) {
+    extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's period
+    using Z = Sizes<NL>;
+    const uint32_t q_s = smem_addr(smem), p_s = q_s + Z::CHUNKS * CHUNK, kv_s = p_s + CHUNK;
+    const uint32_t rot_s = kv_s + Z::SLOTS * Z::SLOT_BYTES;
+    Shared &sh = *reinterpret_cast<Shared *>(smem + Z::SMEM - SMEM_EXTRA);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (warp == 0) {
-        if (lane < MAX_STAGES * MAX_GROUPS) {
-            mbar_init(&sh.full[0][0] + lane, 1);
-            mbar_init(&sh.empty[0][0] + lane, 1);
+        if (lane < MAX_SLOTS) {
+            mbar_init(&sh.full[lane], 1);
+            mbar_init(&sh.empty[lane], 1);
+        } else if (lane < MAX_SLOTS + MAX_ROT_SLOTS) {
+            mbar_init(&sh.rot_full[lane - MAX_SLOTS], 1);
+            mbar_init(&sh.rot_empty[lane - MAX_SLOTS], 1);
         } else if (lane == 16) {
             mbar_init(&sh.s_full[0], 1);
             mbar_init(&sh.s_full[1], 1);
@@ -202,7 +252,9 @@ k_latent_attn(const __grid_constant__ CUtensorMap map, const Params p) {
             mbar_init(&sh.q_ready, 128);
             mbar_init(&sh.o_empty, 128);
         } else if (lane == 18) {
-            prefetch_map(&map);
+            prefetch_map(&maps.wide);
+            prefetch_map(&maps.one);
+            prefetch_map(&maps.rot);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -219,8 +271,13 @@ k_latent_attn(const __grid_constant__ CUtensorMap map, const Params p) {
     const int per_lane = (p.B + 31) / 32;
     const int r0 = min(p.B, lane * per_lane), r1 = min(p.B, r0 + per_lane);
     int64_t sum = 0;
-#pragma unroll 4
-    for (int b = r0; b < r1; ++b) sum += static_cast<int64_t>(tiles_of(row_len(p, b))) * p.mgroups;
+    int len_of[8];  // the first eight of them stay in registers
+#pragma unroll
+    for (int i = 0; i < 8; ++i) len_of[i] = r0 + i < r1 ? row_len(p, r0 + i) : 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += tiles_of(len_of[i]);
+    for (int b = r0 + 8; b < r1; ++b) sum += tiles_of(row_len(p, b));
+    sum *= p.mgroups;
     int64_t at = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -239,13 +296,29 @@ k_latent_attn(const __grid_constant__ CUtensorMap map, const Params p) {
     {
         const bool mine = t0 < t1 && at <= t0 && t0 < at + sum;
         int b = r0, n = 0, in = 0;
-        if (mine)
-            for (;; ++b) {
+        if (mine) {
+            bool found = false;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (!found) {
+                    n = len_of[i];
+                    const int64_t unit_tiles = static_cast<int64_t>(tiles_of(n)) * p.mgroups;
+                    found = t0 < at + unit_tiles;
+                    if (!found) {
+                        at += unit_tiles;
+                        ++b;
+                    }
+                }
+            while (!found) {
                 n = row_len(p, b);
                 const int64_t unit_tiles = static_cast<int64_t>(tiles_of(n)) * p.mgroups;
-                if (t0 < at + unit_tiles) break;
-                at += unit_tiles;
+                found = t0 < at + unit_tiles;
+                if (!found) {
+                    at += unit_tiles;
+                    ++b;
+                }
             }
+        }
         in = static_cast<int>(t0 - at);  // fewer than 2^31 tiles a row
         const unsigned who = __ballot_sync(0xFFFFFFFFu, mine);
         const int src = who ? __ffs(who) - 1 : 0;
@@ -266,81 +339,103 @@ k_latent_attn(const __grid_constant__ CUtensorMap map, const Params p) {
 
     if (warp == 0) {
         if (elect_one()) {
-            // ---- producer: a tile's chunks group by group, in boxes that stay within a
-            // page.  Each box's page is looked up a tile ahead.
+            // ---- producer: a tile's pieces, in boxes that stay within a page
             const int boxes = TN / p.box_rows;
-            int g = 0, k = 0, s = 0;
-            uint32_t ph = 1;  // phase of stage s's release
+            int filled = 0, rot_filled = 0;  // pieces and rotated chunks on their way or there
+            int s = 0, rs = 0;               // the next slot of either ring
+            uint32_t ph = 1, rph = 1;        // phase of its release
             while (!sh.abort && w.next(p)) {
                 const int32_t *table = p.block_table + w.ib * p.max_pages;
-                int f = w.i0;  // the next tile to look up
-                for (int tile = w.i0; tile < w.i1; ++tile, ++g) {
-                    for (; f < w.i1 && f < tile + RING; ++f) {
-                        int key = f * TN, pi = key / p.page_size, row = key - pi * p.page_size;
-                        int page[MAX_BOXES], off[MAX_BOXES];
+                int f = w.i0;  // the next tile to look up: its pages' numbers are being read
+                int pi = f * TN / p.page_size, row = f * TN - pi * p.page_size;
+                int page[MAX_BOXES], at[MAX_BOXES];
+                const auto look = [&]() {
+                    int key = f * TN;
 #pragma unroll
-                        for (int i = 0; i < MAX_BOXES; ++i) {
-                            page[i] = p.num_pages;  // beyond the last page: TMA fills zeros
-                            off[i] = row;
-                            if (i < boxes && key < w.len) {
-                                page[i] = table[pi];
-                                key += p.box_rows;
-                                row += p.box_rows;
-                                if (row == p.page_size) {
-                                    row = 0;
-                                    ++pi;
-                                }
+                    for (int i = 0; i < MAX_BOXES; ++i) {
+                        at[i] = row;
+                        page[i] = p.num_pages;  // beyond the last page: TMA fills zeros
+                        if (i < boxes && key < w.len) {
+                            page[i] = table[pi];
+                            key += p.box_rows;
+                            row += p.box_rows;
+                            if (row == p.page_size) {
+                                row = 0;
+                                ++pi;
                             }
-                        }
-#pragma unroll
-                        for (int i = 0; i < MAX_BOXES; ++i) {
-                            if (i >= boxes) break;
-                            if (static_cast<unsigned>(page[i]) > static_cast<unsigned>(p.num_pages) ||
-                                (page[i] == p.num_pages && f * TN + i * p.box_rows < w.len)) {
-                                page[i] = p.num_pages;
-                                if (p.status) atomicOr(p.status, MTPSPEC_STATUS_BAD_PARAM);
-                            }
-                            sh.box[f % RING][i] = make_int2(page[i], off[i]);
                         }
                     }
-                    int o = 0;
-                    for (k = 0; k < MAX_GROUPS; ++k) {
-                        // group 0: the rotated chunk; group k: the output's k-th piece
-                        if (k > 0 && o >= p.L) break;
-                        const int c0 = k == 0 ? nchunks - 1 : o / 64;
-                        const int n = k == 0 ? 1 : piece_width(p.L - o) / 64;
-                        if (k > 0) o += n * 64;
-                        if (!wait(sh, &sh.empty[s][k], ph)) break;
-                        mbar_expect_tx(&sh.full[s][k], n * CHUNK);
-                        uint32_t dst = kv_s + s * stage_bytes + c0 * CHUNK;
+                };
+                // tile f's boxes are known now (and, with `early`, go to L2)
+                const auto settle = [&](bool early) {
+                    int first_key = f * TN;
 #pragma unroll
-                        for (int i = 0; i < MAX_BOXES; ++i) {
-                            if (i >= boxes) break;
+                    for (int i = 0; i < MAX_BOXES; ++i) {
+                        if (i >= boxes) break;
+                        if (first_key < w.len && static_cast<unsigned>(page[i]) >= static_cast<unsigned>(p.num_pages)) {
+                            page[i] = p.num_pages;
+                            if (p.status) atomicOr(p.status, MTPSPEC_STATUS_BAD_PARAM);
+                        }
+                        first_key += p.box_rows;
+                        sh.box[f % RING][i] = make_int2(page[i], at[i]);
+                        if (early) {
+#pragma unroll
+                            for (int k = 0; k < Z::PIECES; ++k)
+                                piece_prefetch<Z>(maps, k, p.box_rows, at[i], page[i]);
+                            tma_prefetch_3d(&maps.rot, Z::L, at[i], page[i]);
+                        }
+                    }
+                    if (++f < w.i1) look();
+                };
+                look();
+                for (int tile = w.i0; tile < w.i1; ++tile) {
+                    if (f <= tile) settle(false);
+#pragma unroll
+                    for (int k = 0; k < Z::PIECES; ++k) {
+                        if (!wait(sh, &sh.empty[s], ph)) break;
+                        mbar_expect_tx(&sh.full[s], Z::width(k) * CHUNK);
+                        ++filled;
+                        const uint32_t dst = kv_s + s * Z::SLOT_BYTES;
+#pragma unroll 1
+                        for (int i = 0; i < boxes; ++i) {
                             const int2 x = sh.box[tile % RING][i];
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                if (c < n)
-                                    tma_load_3d(dst + c * CHUNK, &map, (c0 + c) * 64, x.y, x.x,
-                                                &sh.full[s][k]);
-                            dst += p.box_rows * 128;
+                            piece_load<Z>(maps, k, dst, i, p.box_rows, x.y, x.x, &sh.full[s]);
+                        }
+                        if (++s == Z::SLOTS) {
+                            s = 0;
+                            ph ^= 1;
                         }
                     }
-                    if (sh.abort) break;
-                    if (++s == p.stages) {
-                        s = 0;
-                        ph ^= 1;
+                    // The next tile goes to L2 as soon as this one's pieces are under way: what
+                    // its slots wait for is then the way from L2, which leaves them sooner to
+                    // the tile after.  (64 rows x 8k keys x 256 query rows 241 -> 217 us; two
+                    // or four tiles ahead 221; in boxes smaller than a tile, four times the
+                    // copies, it costs more than it gives: 150 -> 161 us.)
+                    if (p.box_rows == TN && f < w.i1) settle(true);
+                    if (sh.abort || !wait(sh, &sh.rot_empty[rs], rph)) break;
+                    mbar_expect_tx(&sh.rot_full[rs], CHUNK);
+                    ++rot_filled;
+                    uint32_t dst = rot_s + rs * CHUNK;
+#pragma unroll 1
+                    for (int i = 0; i < boxes; ++i) {
+                        const int2 x = sh.box[tile % RING][i];
+                        tma_load_3d(dst, &maps.rot, Z::L, x.y, x.x, &sh.rot_full[rs]);
+                        dst += p.box_rows * 128;
+                    }
+                    if (++rs == Z::ROT_SLOTS) {
+                        rs = 0;
+                        rph ^= 1;
                     }
                 }
             }
             pdl_launch_dependents();  // the joining kernel may be set up; it waits for this one
             // after an abort, let the copies in flight land (the last fill of each barrier)
-            if (sh.abort)
-                for (int j = 0; j < p.stages; ++j)
-                    for (int i = 0; i < MAX_GROUPS; ++i) {
-                        const int n = (g + p.stages - 1 - j) / p.stages + (j == s && i < k);
-                        for (uint32_t it = 0; n > 0 && it < WAIT_LIMIT; ++it)
-                            if (mbar_test(&sh.full[j][i], (n - 1) & 1)) break;
-                    }
+            if (sh.abort) {
+                for (int j = 0; j < Z::SLOTS; ++j)
+                    wait_out(&sh.full[j], (filled + Z::SLOTS - 1 - j) / Z::SLOTS);
+                for (int j = 0; j < Z::ROT_SLOTS; ++j)
+                    wait_out(&sh.rot_full[j], (rot_filled + Z::ROT_SLOTS - 1 - j) / Z::ROT_SLOTS);
+            }
         }
     } else if (warp == 1) {
         if (elect_one()) {
@@ -349,37 +444,45 @@ k_latent_attn(const __grid_constant__ CUtensorMap map, const Params p) {
             // there is issued, the products first, since they free the stage.
             constexpr uint32_t id_qk = idesc_of<T>(TN, false);
             const uint64_t qd = smem_desc_sw128(q_s), pd = smem_desc_sw128(p_s);
+            const uint64_t kd = smem_desc_sw128(kv_s), rd = smem_desc_sw128(rot_s);
+            const uint64_t vd = smem_desc_rows_k(kv_s);
             int item = 0;
-            int sa = 0, sb = 0;           // the stages of tiles a and b
-            uint32_t pa = 0, par = 0;     // phase of stage sa; parity of tile a's number
-            int ahead = 0;                // tiles whose scores are issued, products not
-            uint32_t pb = 0, idle = 0;    // parity of tile b's number
-            bool first = true;            // tile b is the item's first
-            auto products = [&]() {       // false: not ready
+            int sa = 0, sb = 0, ra = 0;            // the next slots of tiles a and b
+            uint32_t pa = 0, pra = 0, par = 0;     // their phases; parity of tile a's number
+            int ahead = 0;                         // tiles whose scores are issued, products not
+            uint32_t pb = 0, idle = 0;             // parity of tile b's number
+            bool first = true;                     // tile b is the item's first
+            auto products = [&]() {
                 if (ahead == 0 || !mbar_poll(&sh.p_ready, pb)) {
                     if (++idle > POLL_LIMIT) sh.abort = 1;
-                    return false;
+                    return;
                 }
-                if (first && item > 0 && !wait(sh, &sh.o_empty, (item - 1) & 1)) return false;
+                if (first && item > 0 && !wait(sh, &sh.o_empty, (item - 1) & 1)) return;
                 tc_fence_after();
-                const uint64_t vd0 = smem_desc_rows_k(kv_s + sb * stage_bytes);
-                for (int c = 0, k = 1; c < p.L; ++k) {
-                    const int n = piece_width(p.L - c);
-                    const uint32_t id = idesc_of<T>(n, true);
-                    const uint64_t vd = vd0 + (c / 64) * (CHUNK >> 4);
+#pragma unroll
+                for (int k = 0; k < Z::PIECES; ++k) {
+                    const uint32_t id = idesc_of<T>(Z::width(k) * 64, true);
+                    const uint64_t v = vd + sb * (Z::SLOT_BYTES >> 4);
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
-                        mma_ws(tmem + c / 2, pd + 2 * u, vd + u * (2048 >> 4), id, !first || u > 0);
-                    mma_commit(&sh.empty[sb][k]);
-                    c += n;
+                        mma_ws(tmem + Z::first(k) * 32, pd + 2 * u, v + u * (2048 >> 4), id, !first || u > 0);
+                    mma_commit(&sh.empty[sb]);
+                    if (++sb == Z::SLOTS) sb = 0;
                 }
                 mma_commit(&sh.pv_done);
-                if (++sb == p.stages) sb = 0;
                 pb ^= 1;
                 --ahead;
                 first = false;
                 idle = 0;
-                return true;
+            };
+            // waits for a fill, with products between the polls
+            auto filled = [&](uint64_t *bar, uint32_t phase) {
+                do {
+                    products();
+                } while (!mbar_poll(bar, phase) && !sh.abort);
+                idle = 0;
+                tc_fence_after();
+                return !sh.abort;
             };
             while (!sh.abort && w.next(p)) {
                 if (!wait(sh, &sh.q_ready, item & 1)) break;
@@ -387,66 +490,60 @@ k_latent_attn(const __grid_constant__ CUtensorMap map, const Params p) {
                 first = true;
                 for (int tile = w.i0; tile < w.i1 && !sh.abort; ++tile) {
                     while (ahead > 1 && !sh.abort) products();  // the scores' buffer is free
-                    const uint64_t kd0 = smem_desc_sw128(kv_s + sa * stage_bytes);
-                    const uint32_t d = tmem + S_COL + par * (TN / 2);
-                    int o = 0;
+                    const uint32_t d = tmem + Z::S_COL + par * (TN / 2);
+                    // chunk c of the queries against the same chunk of the keys
+                    const auto scores = [&](int c, uint64_t k) {
 #pragma unroll
-                    for (int k = 0; k < MAX_GROUPS; ++k) {
-                        if (k > 0 && o >= p.L) break;
-                        const int c0 = k == 0 ? nchunks - 1 : o / 64;
-                        const int n = k == 0 ? 1 : piece_width(p.L - o) / 64;
-                        if (k > 0) o += n * 64;
-                        do {
-                            products();
-                        } while (!mbar_poll(&sh.full[sa][k], pa) && !sh.abort);
-                        if (sh.abort) break;
-                        idle = 0;
-                        tc_fence_after();
-                        const uint64_t ad = qd + c0 * (CHUNK >> 4), bd = kd0 + c0 * (CHUNK >> 4);
+                        for (int u = 0; u < 4; ++u)
+                            mma_ws(d, qd + c * (CHUNK >> 4) + 2 * u, k + 2 * u, id_qk, (c | u) != 0);
+                    };
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            if (c >= n) break;
+                    for (int k = 0; k < Z::PIECES; ++k) {
+                        if (!filled(&sh.full[sa], pa)) break;
+                        const uint64_t key = kd + sa * (Z::SLOT_BYTES >> 4);
 #pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                mma_ws(d, ad + c * (CHUNK >> 4) + 2 * u, bd + c * (CHUNK >> 4) + 2 * u,
-                                       id_qk, (k | c | u) != 0);
+                        for (int i = 0; i < Z::width(k); ++i) scores(Z::first(k) + i, key + i * (CHUNK >> 4));
+                        if (++sa == Z::SLOTS) {
+                            sa = 0;
+                            pa ^= 1;
                         }
-                        if (k == 0) mma_commit(&sh.empty[sa][0]);
                     }
+                    if (sh.abort || !filled(&sh.rot_full[ra], pra)) break;
+                    scores(NL, rd + ra * (CHUNK >> 4));
                     mma_commit(&sh.s_full[par]);
+                    mma_commit(&sh.rot_empty[ra]);
+                    if (++ra == Z::ROT_SLOTS) {
+                        ra = 0;
+                        pra ^= 1;
+                    }
                     ++ahead;
                     par ^= 1;
-                    if (++sa == p.stages) {
-                        sa = 0;
-                        pa ^= 1;
-                    }
                 }
                 while (ahead > 0 && !sh.abort) products();
                 ++item;
             }
             mma_commit(&sh.drained);
-            for (uint32_t it = 0; it < WAIT_LIMIT; ++it)
-                if (mbar_test(&sh.drained, 0)) break;
+            wait_out(&sh.drained, 1);
         }
     } else {
         // ---- softmax: a pair of threads a row, 32 of a tile's 64 keys each
         const int wq = warp & 3, half = wq >> 1, r = (wq & 1) * 32 + lane;
         const int tid = threadIdx.x - SOFTMAX0;
         const uint32_t trow = tmem + (static_cast<uint32_t>(wq * 32) << 16);
-        const int vecs = (p.L + p.R) / 8, vecs_all = nchunks * 8;
+        const int vecs = (Z::L + p.R) / 8;
         const int rows_all = p.T * p.Hq;
-        int g = 0, slot = 0, stage = 0;
+        int g = 0, slot = 0, piece_slot = 0;
         Walk nw = w;  // one item ahead: its queries are loaded before this item's epilogue
         bool more = nw.next(p);
         auto load_q = [&](const Walk &k) {
-            // two threads a row, every other vector each; what lies beyond is zero
+            // two threads a row, every other vector each; what lies beyond the row is zero
             const int row = tid >> 1, m = k.imt * TM + row;
             const bool real = m < rows_all;
             const int t = real ? m / p.Hq : 0, h = real ? m - t * p.Hq : 0;
             const uint16_t *src = p.q + (k.ib * p.q_row + t * p.q_tok + h * p.q_head);
             const uint32_t dst = q_s + row * 128;
 #pragma unroll 4
-            for (int v = tid & 1; v < vecs_all; v += 2) {
+            for (int v = tid & 1; v < Z::CHUNKS * 8; v += 2) {
                 const bool in = real && v < vecs;
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
                                  dst + (v >> 3) * CHUNK + (((v & 7) ^ (row & 7)) << 4)),
@@ -464,7 +561,7 @@ k_latent_attn(const __grid_constant__ CUtensorMap map, const Params p) {
             if (tid == 0 && p.status && (n < 0 || n > p.max_pages * p.page_size))
                 atomicOr(p.status, MTPSPEC_STATUS_BAD_PARAM);
             if (row_len(p, b) > 0) continue;
-            const int row_vecs = p.L / 8;
+            const int row_vecs = Z::L / 8;
             for (int i = tid; i < rows_all * row_vecs; i += 128) {
                 const int mm = i / row_vecs, v = i - mm * row_vecs, tt = mm / p.Hq;
                 *reinterpret_cast<uint4 *>(p.out + b * p.out_row + tt * p.out_tok +
@@ -485,21 +582,20 @@ k_latent_attn(const __grid_constant__ CUtensorMap map, const Params p) {
             for (int tile = w.i0; tile < w.i1; ++tile, ++g) {
                 wait(sh, &sh.s_full[g & 1], (g >> 1) & 1);
                 tc_fence_after();
-                uint32_t raw[32];
-                tmem_ld32(trow + S_COL + (g & 1) * (TN / 2), raw);
+                uint32_t x[32];
+                tmem_ld32(trow + Z::S_COL + (g & 1) * (TN / 2), x);
                 tmem_wait_ld();
-                float x[32], top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(raw[i]);
-                if (tile * TN + TN > sure) {
-                    const int k0 = tile * TN + half * 32;
+                if (__builtin_expect(tile * TN + TN > sure, 0)) {
+                    const int seen = limit - (tile * TN + half * 32);
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (k0 + i >= limit) x[i] = -INFINITY;
+                        if (i >= seen) x[i] = 0xFF800000u;
                 }
+                float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int i = 0; i < 32; ++i) top4[i & 3] = fmaxf(top4[i & 3], x[i]);
-                float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+                for (int i = 0; i < 32; i += 2)
+                    top4[(i >> 1) & 3] = max3(top4[(i >> 1) & 3], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+                float top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
                 sh.xm[slot][wq][lane] = top;
                 asm volatile("bar.sync %0, 64;" ::"r"(1 + (wq & 1)) : "memory");
                 top = fmaxf(top, sh.xm[slot][wq ^ 2][lane]) * p.scale2;
@@ -508,26 +604,32 @@ k_latent_attn(const __grid_constant__ CUtensorMap map, const Params p) {
                 const float m_old = m_ref;
                 if (raise) m_ref = top;
                 const float m_use = m_ref == -INFINITY ? 0.0f : m_ref;
-                float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                const uint64_t scale_2 = pack2(p.scale2, p.scale2), minus_m = pack2(-m_use, -m_use);
+                uint64_t part[2] = {0, 0};  // two pairs of sums
                 uint4 weights[4];
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                     float e[8];
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        e[u] = ex2(fmaf(x[8 * v + u], p.scale2, -m_use));
-                        part[u & 3] += e[u];
+                    for (int u = 0; u < 4; ++u) {
+                        float e0, e1;
+                        unpack2(fma2(pack2(__uint_as_float(x[8 * v + 2 * u]), __uint_as_float(x[8 * v + 2 * u + 1])),
+                                     scale_2, minus_m), e0, e1);
+                        e[2 * u] = ex2(e0);
+                        e[2 * u + 1] = ex2(e1);
+                        part[u & 1] = add2(part[u & 1], pack2(e[2 * u], e[2 * u + 1]));
                     }
                     weights[v] = float_to_half8<T>(e);
                 }
                 // the products of the tile before are done: the weights' buffer and the
                 // output are free to change
                 if (g > 0) wait(sh, &sh.pv_done, (g - 1) & 1);
-                if (tile > w.i0 && __any_sync(0xFFFFFFFFu, raise)) {
+                if (__builtin_expect(tile > w.i0 && __any_sync(0xFFFFFFFFu, raise), 0)) {
                     tc_fence_after();
                     const float f = raise ? ex2(m_old - m_ref) : 1.0f;
                     l *= f;
-                    for (int c = 0; c < p.L / 2; c += 32) {
+#pragma unroll 1
+                    for (int c = 0; c < Z::L / 2; c += 32) {
                         uint32_t o[32];
                         tmem_ld32(trow + c, o);
                         tmem_wait_ld();
@@ -537,7 +639,9 @@ k_latent_attn(const __grid_constant__ CUtensorMap map, const Params p) {
                     }
                     tmem_wait_st();
                 }
-                l += (part[0] + part[1]) + (part[2] + part[3]);
+                float l0, l1;
+                unpack2(add2(part[0], part[1]), l0, l1);
+                l += l0 + l1;
                 const uint32_t prow = p_s + r * 128;
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
@@ -546,23 +650,29 @@ k_latent_attn(const __grid_constant__ CUtensorMap map, const Params p) {
                                  "r"(weights[v].x), "r"(weights[v].y), "r"(weights[v].z),
                                  "r"(weights[v].w)
                                  : "memory");
-                if (tile * TN + TN > w.len) {
+                if (__builtin_expect(tile * TN + TN > w.len, 0)) {
                     // rows of the tile beyond the sequence: whatever the page holds there
                     // must not meet the zero weights
-                    const uint32_t v = kv_s + stage * stage_bytes;
-                    const int z0 = w.len - tile * TN;
-                    for (int i = tid; i < (TN - z0) * 8 * (p.L / 64); i += 128) {
-                        const int c = i / ((TN - z0) * 8), j = i - c * ((TN - z0) * 8);
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                         v + c * CHUNK + z0 * 128 + j * 16),
-                                     "r"(0)
-                                     : "memory");
+                    const int z0 = w.len - tile * TN, vec = (TN - z0) * 8;
+                    int at = piece_slot;
+#pragma unroll 1
+                    for (int k = 0; k < Z::PIECES; ++k) {
+                        const uint32_t v = kv_s + at * Z::SLOT_BYTES + z0 * 128;
+                        for (int i = tid; i < vec * Z::width(k); i += 128) {
+                            const int c = i / vec;
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                             v + c * CHUNK + (i - c * vec) * 16),
+                                         "r"(0)
+                                         : "memory");
+                        }
+                        if (++at == Z::SLOTS) at = 0;
                     }
                 }
                 fence_async_smem();
                 tc_fence_before();
                 mbar_arrive(&sh.p_ready);
-                if (++stage == p.stages) stage = 0;
+                piece_slot += Z::PIECES;
+                if (piece_slot >= Z::SLOTS) piece_slot -= Z::SLOTS;
             }
             // ---- this item's scores are all read: its queries may be replaced
             more = nw.next(p);
@@ -588,35 +698,37 @@ k_latent_attn(const __grid_constant__ CUtensorMap map, const Params p) {
             if (w.i0 == 0 && !whole)  // the unit starts here and goes on in other groups
                 cut_unit = make_int4(w.ib, w.imt, group,
                                      cut.owner(t1 - w.left - (w.i1 - w.i0) + w.int_ - 1));
-            // A row a thread: stores of 32 bytes, a whole sector each, where the rows allow it
+            // A row a thread: stores of 32 bytes, a whole sector each, where the rows allow it.
+            // (The store unit takes a sector of each of 32 rows at a time, 6000 cycles for 64
+            // rows; changing places among four lanes first, for whole lines, cost more in
+            // shuffles and registers than it saved: 154 -> 175 us in all at 256 rows.)
             const int t = m / p.Hq, h = m - t * p.Hq;
             uint16_t *dst = p.out + w.ib * p.out_row + t * p.out_tok + h * p.out_head;
-            float *pdst = p.part + ((2 * cta + (w.i0 > 0 ? 0 : 1)) * static_cast<int64_t>(p.rows_cap) + r) * p.L;
+            float *pdst = p.part + ((2 * cta + (w.i0 > 0 ? 0 : 1)) * static_cast<int64_t>(p.rows_cap) + r) * Z::L;
             const bool sectors = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
             uint32_t a[2][32];
             tmem_ld32(trow, a[0]);
-            int o = 0, n = piece_width(p.L), c = 0;
+            int k = 0, c = 0;  // the piece and the accumulator column in its half
 #pragma unroll 2
-            for (int i = 0; i < p.L / 64; ++i) {
+            for (int i = 0; i < NL; ++i) {
                 tmem_wait_ld();
-                if (i + 1 < p.L / 64) tmem_ld32(trow + 32 * (i + 1), a[(i + 1) & 1]);
-                const int col = o + half * (n / 2) + c;
+                if (i + 1 < NL) tmem_ld32(trow + 32 * (i + 1), a[(i + 1) & 1]);
+                const int col = Z::first(k) * 64 + half * (Z::width(k) * 32) + c;
                 c += 32;
-                if (c == n / 2) {
-                    o += n;
-                    n = piece_width(p.L - o);
+                if (c == Z::width(k) * 32) {
+                    ++k;
                     c = 0;
                 }
                 if (!real) continue;
                 float f[32];
 #pragma unroll
-                for (int k = 0; k < 32; ++k) f[k] = __uint_as_float(a[i & 1][k]) * inv;
+                for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(a[i & 1][j]) * inv;
                 if (whole) {
 #pragma unroll
                     for (int v = 0; v < 2; ++v) {
                         uint32_t x[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) x[k] = T::narrow2(f[16 * v + 2 * k], f[16 * v + 2 * k + 1]);
+                        for (int j = 0; j < 8; ++j) x[j] = T::narrow2(f[16 * v + 2 * j], f[16 * v + 2 * j + 1]);
                         if (sectors) {
                             st_global_32B(dst + col + 16 * v, x);
                         } else {
@@ -629,7 +741,7 @@ k_latent_attn(const __grid_constant__ CUtensorMap map, const Params p) {
                     for (int v = 0; v < 4; ++v) {
                         uint32_t x[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) x[k] = __float_as_uint(f[8 * v + k]);
+                        for (int j = 0; j < 8; ++j) x[j] = __float_as_uint(f[8 * v + j]);
                         st_global_32B(pdst + col + 8 * v, x);
                     }
                 }
@@ -653,65 +765,86 @@ k_latent_attn(const __grid_constant__ CUtensorMap map, const Params p) {
 }
 
 // Units cut among groups: each row's partial outputs, weighted by their sums, become the
-// output.  A CTA takes one row of the unit that starts in CTA blockIdx.y of the first kernel
-// and ends in another group; a thread takes four columns of every part, eight parts in flight.
-constexpr int JOIN_THREADS = 128;
+// output.  blockIdx.y is the CTA of the first kernel in which the unit starts.  With few parts
+// a unit a warp takes a row; with many (WIDE) a CTA does, an eighth of the parts a warp, and
+// joins its warps' sums.
+constexpr int JOIN_THREADS = 256, JOIN_WARPS = JOIN_THREADS / 32;
 
-template <typename T>
+template <typename T, bool WIDE>
 __global__ void __launch_bounds__(JOIN_THREADS) k_latent_join(const Params p) {
-    __shared__ float weight[GRID];
+    __shared__ float sums[WIDE ? JOIN_WARPS : 1][WIDE ? 512 : 1];
     pdl_wait_primary();
     const int4 u = p.plan[blockIdx.y];
     // (what an aborted call left there is checked)
     if (u.x < 0 || u.x >= p.B || u.y < 0 || u.y >= p.mtiles || u.z < 0 || u.w >= p.groups) return;
-    const int r = blockIdx.x, m = u.y * TM + r, rows_all = p.T * p.Hq, parts = u.w - u.z + 1;
-    if (m >= rows_all || parts < 2) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = WIDE ? blockIdx.x : blockIdx.x * JOIN_WARPS + warp;
+    const int m = u.y * TM + r, rows_all = p.T * p.Hq, parts = u.w - u.z + 1;
+    if (r >= p.rows_cap || m >= rows_all || parts < 2) return;
     // a group's partial of this row: the second slot where the unit starts, else the first
-    const int lane_cta = u.y % p.gs;
-    const auto part_row = [&](int i) {
-        const int64_t cta = static_cast<int64_t>(u.z + i) * p.gs + lane_cta;
-        return (2 * cta + (i == 0)) * p.rows_cap + r;
-    };
+    const int64_t step = static_cast<int64_t>(2) * p.gs * p.rows_cap;
+    const int64_t row0 = (static_cast<int64_t>(u.z) * p.gs + u.y % p.gs) * 2 * p.rows_cap + r;
+    const auto part_row = [&](int i) { return row0 + i * step + (i == 0 ? p.rows_cap : 0); };
     // every warp finds the row's largest sum by itself
-    const int lane = threadIdx.x & 31;
     float top = -INFINITY, sum = 0.0f;
     for (int i = lane; i < parts; i += 32) top = fmaxf(top, p.part_lse[part_row(i)]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     const float ref = top == -INFINITY ? 0.0f : top;
-    for (int i = lane; i < parts; i += 32) {
-        const float w = exp2f(p.part_lse[part_row(i)] - ref);
+    // a lane's columns: four of every 128
+    float4 acc[4] = {};
+    const int first = WIDE ? warp : 0, hop = WIDE ? JOIN_WARPS : 1;
+#pragma unroll 2
+    for (int i = first; i < parts; i += hop) {
+        const int64_t row = part_row(i);
+        float4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k * 128 + lane * 4 < p.L)
+                v[k] = *reinterpret_cast<const float4 *>(p.part + row * p.L + k * 128 + lane * 4);
+        const float w = exp2f(p.part_lse[row] - ref);
         sum += w;
-        if (threadIdx.x < 32) weight[i] = w;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k * 128 + lane * 4 < p.L) {
+                acc[k].x += w * v[k].x;
+                acc[k].y += w * v[k].y;
+                acc[k].z += w * v[k].z;
+                acc[k].w += w * v[k].w;
+            }
     }
+    if (WIDE) {
+        __shared__ float warp_sum[JOIN_WARPS];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    __syncthreads();
-    const int col = threadIdx.x * 4;
-    if (col < p.L) {
-        const float *src = p.part + col;
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int i = 0; i < parts; i += 8) {
-            float4 v[8];
+        for (int k = 0; k < 4; ++k) *reinterpret_cast<float4 *>(&sums[warp][k * 128 + lane * 4]) = acc[k];
+        if (lane == 0) warp_sum[warp] = sum;
+        __syncthreads();
+        sum = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (i + k < parts) v[k] = *reinterpret_cast<const float4 *>(src + part_row(i + k) * p.L);
+        for (int w = 0; w < JOIN_WARPS; ++w) sum += warp_sum[w];
+        if (warp >= 4) return;
+        float4 s4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (i + k < parts) {
-                    const float w = weight[i + k];
-                    acc.x += w * v[k].x;
-                    acc.y += w * v[k].y;
-                    acc.z += w * v[k].z;
-                    acc.w += w * v[k].w;
-                }
+        for (int w = 0; w < JOIN_WARPS; ++w) {
+            const float4 x = *reinterpret_cast<const float4 *>(&sums[w][warp * 128 + lane * 4]);
+            s4.x += x.x;
+            s4.y += x.y;
+            s4.z += x.z;
+            s4.w += x.w;
         }
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-        const int t = m / p.Hq, h = m - t * p.Hq;
-        *reinterpret_cast<uint2 *>(p.out + u.x * p.out_row + t * p.out_tok + h * p.out_head + col) =
-            make_uint2(T::narrow2(acc.x * inv, acc.y * inv), T::narrow2(acc.z * inv, acc.w * inv));
+        acc[0] = s4;
     }
-    if (p.lse && threadIdx.x == 0)
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const int t = m / p.Hq, h = m - t * p.Hq;
+    uint16_t *dst = p.out + u.x * p.out_row + t * p.out_tok + h * p.out_head;
+#pragma unroll
+    for (int k = 0; k < (WIDE ? 1 : 4); ++k) {
+        const int col = (WIDE ? warp : k) * 128 + lane * 4;
+        if (col < p.L)
+            *reinterpret_cast<uint2 *>(dst + col) =
+                make_uint2(T::narrow2(acc[k].x * inv, acc[k].y * inv), T::narrow2(acc[k].z * inv, acc[k].w * inv));
+    }
+    if (p.lse && lane == 0 && (!WIDE || warp == 0))
         p.lse[static_cast<int64_t>(u.x) * rows_all + m] = sum > 0.0f ? (top + log2f(sum)) * LN2 : -INFINITY;
 }
 
@@ -736,11 +869,11 @@ Layout layout(int64_t rows, int32_t L) {
     return y;
 }
 
-template <typename T>
-cudaError_t launch(const CUtensorMap &map, const Params &p, cudaStream_t stream) {
-    const int smem = (1 + p.stages) * (p.L / 64 + 1) * CHUNK + CHUNK + SMEM_EXTRA;
+template <typename T, int NL>
+cudaError_t launch(const Maps &maps, const Params &p, cudaStream_t stream) {
+    constexpr int smem = Sizes<NL>::SMEM;
     static AttrCache attr;
-    cudaError_t e = ensure_attr(k_latent_attn<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem, attr);
+    cudaError_t e = ensure_attr(k_latent_attn<T, NL>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem, attr);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(GRID);
@@ -749,15 +882,32 @@ cudaError_t launch(const CUtensorMap &map, const Params &p, cudaStream_t stream)
     cfg.stream = stream;
     cfg.attrs = pdl_attr();  // set up beside the end of whatever the stream runs before
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, k_latent_attn<T>, map, p);
+    e = cudaLaunchKernelEx(&cfg, k_latent_attn<T, NL>, maps, p);
     if (e != cudaSuccess) return e;
     count_launches(1);
-    cfg.gridDim = dim3(p.rows_cap, p.groups * p.gs);
     cfg.blockDim = dim3(JOIN_THREADS);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, k_latent_join<T>, p);
+    // few units: cut into many parts each, and few rows in all
+    const bool wide = static_cast<int64_t>(p.B) * p.mgroups * 4 < p.groups;
+    cfg.gridDim = dim3(wide ? p.rows_cap : (p.rows_cap + JOIN_WARPS - 1) / JOIN_WARPS, p.groups * p.gs);
+    e = wide ? cudaLaunchKernelEx(&cfg, k_latent_join<T, true>, p)
+             : cudaLaunchKernelEx(&cfg, k_latent_join<T, false>, p);
     if (e == cudaSuccess) count_launches(1);
     return e;
+}
+
+template <typename T>
+cudaError_t pick(const Maps &maps, const Params &p, cudaStream_t stream) {
+    switch (p.L / 64) {
+    case 1: return launch<T, 1>(maps, p, stream);
+    case 2: return launch<T, 2>(maps, p, stream);
+    case 3: return launch<T, 3>(maps, p, stream);
+    case 4: return launch<T, 4>(maps, p, stream);
+    case 5: return launch<T, 5>(maps, p, stream);
+    case 6: return launch<T, 6>(maps, p, stream);
+    case 7: return launch<T, 7>(maps, p, stream);
+    default: return launch<T, 8>(maps, p, stream);
+    }
 }
 
 }  // namespace lat
@@ -773,16 +923,30 @@ cudaError_t run_latent_attn(const LatentAttnArgs &a, int dtype, cudaStream_t str
     // boxes of the largest power of two (up to a tile) that divides the page: a box never
     // leaves its page, and its rows start at a multiple of eight, the swizzle's period
     const int box = std::min(lat::TN, a.page_size & -a.page_size);
-    CUtensorMap map;
-    const cuuint64_t W = static_cast<cuuint64_t>(a.L + a.R);
-    cuuint64_t dims[3] = {W, static_cast<cuuint64_t>(a.page_size), static_cast<cuuint64_t>(a.num_pages)};
-    cuuint64_t strides[2] = {W * 2, static_cast<cuuint64_t>(a.page_stride) * 2};
-    cuuint32_t boxes[3] = {64, static_cast<cuuint32_t>(box), 1};
-    cuuint32_t es[3] = {1, 1, 1};
-    if (fn(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(a.cache), dims, strides,
-           boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    lat::Maps maps;
+    const cuuint64_t W = static_cast<cuuint64_t>(a.L + a.R), P = static_cast<cuuint64_t>(a.page_size);
+    const cuuint64_t pages = static_cast<cuuint64_t>(a.num_pages);
+    const cuuint64_t page_bytes = static_cast<cuuint64_t>(a.page_stride) * 2;
+    const cuuint32_t rows = static_cast<cuuint32_t>(box);
+    const auto encode = [&](CUtensorMap *m, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+                            const cuuint32_t *boxes) {
+        const cuuint32_t es[4] = {1, 1, 1, 1};
+        return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<uint16_t *>(a.cache), dims, strides,
+                  boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    const cuuint64_t chunks = static_cast<cuuint64_t>(a.L / 64);
+    const cuuint64_t cdims[4] = {64, P, chunks, pages}, cstrides[3] = {W * 2, 128, page_bytes};
+    const cuuint32_t wide[4] = {64, rows, static_cast<cuuint32_t>(std::min<cuuint64_t>(4, chunks)), 1};
+    const cuuint32_t one[4] = {64, rows, 1, 1}, rot[3] = {64, rows, 1};
+    const cuuint64_t rdims[3] = {W, P, pages}, rstrides[2] = {W * 2, page_bytes};
+    // (a call encodes the ones that it needs: each costs the host a microsecond)
+    const bool whole = box == lat::TN && a.L >= 256, single = !whole || a.L % 256 != 0;
+    if ((whole && !encode(&maps.wide, 4, cdims, cstrides, wide)) ||
+        (single && !encode(&maps.one, 4, cdims, cstrides, one)) || !encode(&maps.rot, 3, rdims, rstrides, rot))
         return cudaErrorInvalidValue;
+    if (!whole) maps.wide = maps.one;
+    if (!single) maps.one = maps.wide;
     const lat::Layout y = lat::layout(static_cast<int64_t>(a.T) * a.Hq, a.L);
     unsigned char *ws = static_cast<unsigned char *>(a.workspace);
     lat::Params p = {};
@@ -805,9 +969,6 @@ cudaError_t run_latent_attn(const LatentAttnArgs &a, int dtype, cudaStream_t str
     p.gs = y.gs;
     p.mgroups = y.mgroups;
     p.groups = lat::GRID / y.gs;
-    const int stage = (a.L / 64 + 1) * lat::CHUNK;
-    p.stages = std::min<int>(lat::MAX_STAGES,
-                             (lat::SMEM_MAX - stage - lat::CHUNK - lat::SMEM_EXTRA) / stage);
     p.scale2 = a.scale * lat::LOG2E;
     p.out = a.out;
     p.out_row = a.out_row;
@@ -819,7 +980,7 @@ cudaError_t run_latent_attn(const LatentAttnArgs &a, int dtype, cudaStream_t str
     p.part_lse = reinterpret_cast<float *>(ws + y.lse);
     p.rows_cap = y.rows_cap;
     p.status = a.status;
-    return dtype == MTPSPEC_BF16 ? lat::launch<Bf16>(map, p, stream) : lat::launch<F16>(map, p, stream);
+    return dtype == MTPSPEC_BF16 ? lat::pick<Bf16>(maps, p, stream) : lat::pick<F16>(maps, p, stream);
 }
 
 }  // namespace mtpspec
