@@ -139,6 +139,17 @@ __device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity)
     return false;
 }
 
+// The same for a wait that is mostly long: the thread is suspended instead of polling, which
+// leaves issue slots and shared memory to the others.
+__device__ __forceinline__ bool wait_long(Shared &sh, uint64_t *bar, uint32_t parity) {
+    for (uint32_t it = 0; it < WAIT_LIMIT; ++it) {
+        if (mbar_test(bar, parity)) return true;
+        if (sh.abort) return false;
+    }
+    sh.abort = 1;
+    return false;
+}
+
 // Of a CTA that leaves after an abort: the last of a barrier's `fills` lands, or the limit.
 __device__ __forceinline__ void wait_out(uint64_t *bar, int fills) {
     for (uint32_t it = 0; fills > 0 && it < WAIT_LIMIT; ++it)
@@ -580,7 +591,7 @@ k_latent_attn(const __grid_constant__ Maps maps, const Params p) {
             const int sure = w.len - (p.T - 1 - (w.imt * TM) / p.Hq);  // the least limit
             float m_ref = -INFINITY, l = 0.0f;
             for (int tile = w.i0; tile < w.i1; ++tile, ++g) {
-                wait(sh, &sh.s_full[g & 1], (g >> 1) & 1);
+                wait_long(sh, &sh.s_full[g & 1], (g >> 1) & 1);
                 tc_fence_after();
                 uint32_t x[32];
                 tmem_ld32(trow + Z::S_COL + (g & 1) * (TN / 2), x);

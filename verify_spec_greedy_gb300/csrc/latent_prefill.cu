@@ -61,6 +61,17 @@ __device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity)
     return false;
 }
 
+// The same for a wait that is mostly long: the thread is suspended instead of polling, which
+// leaves issue slots and shared memory to the others.
+__device__ __forceinline__ bool wait_long(Shared &sh, uint64_t *bar, uint32_t parity) {
+    for (uint32_t it = 0; it < WAIT_LIMIT; ++it) {
+        if (mbar_test(bar, parity)) return true;
+        if (sh.abort) return false;
+    }
+    sh.abort = 1;
+    return false;
+}
+
 // The bounded wait of a CTA that leaves, whatever the abort flag says.
 __device__ __forceinline__ void wait_out(uint64_t *bar, uint32_t parity) {
     for (uint32_t it = 0; it < WAIT_LIMIT; ++it)
@@ -400,7 +411,7 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         };
         float m_ref = -INFINITY, l = 0.0f;
         for (int j = 0; j < nt; ++j) {
-            wait(sh, &sh.s_full[t], j & 1);
+            wait_long(sh, &sh.s_full[t], j & 1);
             tc_fence_after();
             uint32_t x[2][32];
             tmem_ld32(s_t + half * 64, x[0]);
@@ -480,7 +491,7 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             mbar_arrive(&sh.p_ready[t]);
         }
         if (nt > 0) {
-            wait(sh, &sh.o_done[t], 0);
+            wait_long(sh, &sh.o_done[t], 0);
             tc_fence_after();
         }
         l += swap(l);
