@@ -45,8 +45,10 @@ struct Params {
     uint16_t *out;
     int64_t out_row, out_tok, out_head;
     float *lse;
-    int4 *plan;      // [GRID]: the unit that starts in a CTA and ends in another: row, row
-                     // tile, first and last group; row -1 if there is none
+    int4 *plan;      // what the joining kernel goes by: row, row tile, first and last group of
+                     // a unit; by units (wide_join), or by CTAs, the unit that starts in a CTA
+                     // and ends in another (row -1 if there is none)
+    int wide_join;
     float *part;     // [2 * GRID][rows][L] fp32, normalised partial outputs
     float *part_lse; // [2 * GRID][rows], base 2
     int rows_cap;    // rows of a partial: min(64, T * Hq)
@@ -583,7 +585,7 @@ k_latent_attn(const __grid_constant__ Maps maps, const Params p) {
                 for (int i = tid; i < rows_all; i += 128)
                     p.lse[static_cast<int64_t>(b) * rows_all + i] = -INFINITY;
         }
-        int4 cut_unit = make_int4(-1, 0, 0, 0);
+        bool cut_here = false;  // a unit starts here and ends in another group
         while (more) {
             w = nw;
             const int m = w.imt * TM + r;
@@ -706,9 +708,10 @@ k_latent_attn(const __grid_constant__ Maps maps, const Params p) {
                 else if (p.lse)
                     p.lse[static_cast<int64_t>(w.ib) * rows_all + m] = lse2 * LN2;
             }
-            if (w.i0 == 0 && !whole)  // the unit starts here and goes on in other groups
-                cut_unit = make_int4(w.ib, w.imt, group,
-                                     cut.owner(t1 - w.left - (w.i1 - w.i0) + w.int_ - 1));
+            if (tid == 0 && w.i0 == 0 && (!whole || p.wide_join))  // the unit starts here
+                p.plan[p.wide_join ? w.ib * p.mtiles + w.imt : cta] = make_int4(
+                    w.ib, w.imt, group, cut.owner(t1 - w.left - (w.i1 - w.i0) + w.int_ - 1));
+            cut_here |= w.i0 == 0 && !whole;
             // A row a thread: stores of 32 bytes, a whole sector each, where the rows allow it.
             // (The store unit takes a sector of each of 32 rows at a time, 6000 cycles for 64
             // rows; changing places among four lanes first, for whole lines, cost more in
@@ -760,7 +763,7 @@ k_latent_attn(const __grid_constant__ Maps maps, const Params p) {
             tc_fence_before();
             mbar_arrive(&sh.o_empty);
         }
-        if (tid == 0) p.plan[cta] = cut_unit;
+        if (!p.wide_join && tid == 0 && !cut_here) p.plan[cta] = make_int4(-1, 0, 0, 0);
     }
     tc_fence_before();
     __syncthreads();
@@ -776,9 +779,9 @@ k_latent_attn(const __grid_constant__ Maps maps, const Params p) {
 }
 
 // Units cut among groups: each row's partial outputs, weighted by their sums, become the
-// output.  blockIdx.y is the CTA of the first kernel in which the unit starts.  With few parts
-// a unit a warp takes a row; with many (WIDE) a CTA does, an eighth of the parts a warp, and
-// joins its warps' sums.
+// output.  With few parts a unit a warp takes a row, and blockIdx.y is the CTA of the first
+// kernel in which the unit starts; with many (WIDE), which means few units, a CTA takes a row,
+// an eighth of the parts a warp, and blockIdx.y is the unit.
 constexpr int JOIN_THREADS = 256, JOIN_WARPS = JOIN_THREADS / 32;
 
 template <typename T, bool WIDE>
@@ -786,6 +789,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_latent_join(const Params p) {
     __shared__ float sums[WIDE ? JOIN_WARPS : 1][WIDE ? 512 : 1];
     pdl_wait_primary();
     const int4 u = p.plan[blockIdx.y];
+    // a row without keys is no unit of the first kernel's
+    if (WIDE && row_len(p, blockIdx.y / p.mtiles) == 0) return;
     // (what an aborted call left there is checked)
     if (u.x < 0 || u.x >= p.B || u.y < 0 || u.y >= p.mtiles || u.z < 0 || u.w >= p.groups) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -874,7 +879,7 @@ Layout layout(int64_t rows, int32_t L) {
     y.gs = (y.mtiles + y.mgroups - 1) / y.mgroups;
     y.rows_cap = static_cast<int>(std::min<int64_t>(rows, TM));
     y.plan = 0;
-    y.part = align256(GRID * sizeof(int4));
+    y.part = align256(GRID * sizeof(int4));  // (a wide join has fewer units than GRID / 4)
     y.lse = y.part + align256(static_cast<size_t>(2 * GRID) * y.rows_cap * L * 4);
     y.total = y.lse + align256(static_cast<size_t>(2 * GRID) * y.rows_cap * 4);
     return y;
@@ -898,10 +903,9 @@ cudaError_t launch(const Maps &maps, const Params &p, cudaStream_t stream) {
     count_launches(1);
     cfg.blockDim = dim3(JOIN_THREADS);
     cfg.dynamicSmemBytes = 0;
-    // few units: cut into many parts each, and few rows in all
-    const bool wide = static_cast<int64_t>(p.B) * p.mgroups * 4 < p.groups;
-    cfg.gridDim = dim3(wide ? p.rows_cap : (p.rows_cap + JOIN_WARPS - 1) / JOIN_WARPS, p.groups * p.gs);
-    e = wide ? cudaLaunchKernelEx(&cfg, k_latent_join<T, true>, p)
+    cfg.gridDim = p.wide_join ? dim3(p.rows_cap, p.B * p.mtiles)
+                              : dim3((p.rows_cap + JOIN_WARPS - 1) / JOIN_WARPS, p.groups * p.gs);
+    e = p.wide_join ? cudaLaunchKernelEx(&cfg, k_latent_join<T, true>, p)
              : cudaLaunchKernelEx(&cfg, k_latent_join<T, false>, p);
     if (e == cudaSuccess) count_launches(1);
     return e;
@@ -980,6 +984,8 @@ cudaError_t run_latent_attn(const LatentAttnArgs &a, int dtype, cudaStream_t str
     p.gs = y.gs;
     p.mgroups = y.mgroups;
     p.groups = lat::GRID / y.gs;
+    // few units: cut into many parts each, and few rows in all
+    p.wide_join = static_cast<int64_t>(p.B) * p.mgroups * 4 < p.groups;
     p.scale2 = a.scale * lat::LOG2E;
     p.out = a.out;
     p.out_row = a.out_row;
