@@ -182,3 +182,16 @@ def test_both_forms_agree():
     # both round weights, keys, values or latents to bf16 a few times: some 2^-8 of values of
     # size one each, averaged over the keys
     assert (got - out[0].double()).abs().max() < 8 * 2.0 ** -8
+
+
+@pytest.mark.parametrize("heads,B,longest,V", [(16, 40, 300, 128), (48, 9, 520, 64), (152, 3, 257, 128), (7, 33, 600, 128)])
+def test_more_pairs_than_multiprocessors(heads, B, longest, V):
+    # queries that see nothing, sequences without keys or queries among them
+    nq = [(37 * i + 11) % longest + 1 for i in range(B)]
+    nk = [n + (53 * i) % 150 for i, n in enumerate(nq)]
+    nq[1], nk[2], nk[B - 1] = 0, 0, max(1, nq[B - 1] - 140)
+    x = make(nq, nk, heads, 128, 64, V, BF, seed=B)
+    out, lse = run(x)
+    verify(x, out, lse)
+    again, _ = run(x)
+    assert torch.equal(out, again)

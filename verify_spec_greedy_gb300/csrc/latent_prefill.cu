@@ -22,18 +22,17 @@ using namespace tg;
 constexpr int TM = 128;            // queries of a tile
 constexpr int TN = 128;            // keys of a tile
 constexpr int CHUNK = TN * 128;    // bytes of 128 rows x 64 columns of 16 bits
-constexpr int NTHREADS = 640;      // warp 0 TMA, 1 MMA, 2 prefetch, 3 TMEM; 4-11, 12-19 softmax
+constexpr int NTHREADS = 640;      // warp 0 TMA, 1 MMA, 2 next work, 3 TMEM; 4-11, 12-19 softmax
 constexpr int SMEM_MAX = 232448;   // 227 KB a CTA
 constexpr float LAZY = 8.0f;       // the running maximum may lag by a factor of 2^8
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr unsigned WAVE = 152;     // SMs of a GB300, one CTA each
 constexpr int S_COL = 0, O_COL = 256;  // tile t: + 128 t
 constexpr uint32_t POLL_LIMIT = 1u << 25;  // polls of some 20 ns: ~1 s
 
 struct Params {
     const int32_t *cu_q, *cu_k;
-    int B, Tq, Tk, Hq, N, R, V, slots;
+    int B, Tq, Tk, Hq, N, R, V;
     int ranks;      // query tiles (pairs) a head has at most
     float scale2;   // scale * log2(e), above 0
     uint16_t *out;
@@ -42,10 +41,27 @@ struct Params {
     int32_t *status;
 };
 
+// A pair of query tiles of one head: its sequence, and its place there; pair -1: none.
+struct Work {
+    int q0, nq, k0, nk, pair, head;
+};
+// The same as the CTA's roles get it: with the key tiles before it, the ring's slot that it
+// starts in, and the pairs before it in which either tile of queries had keys to meet, and
+// the key tiles that it met (as far as parities go).
+struct Item {
+    Work w;
+    uint32_t g0;
+    int slot0;
+    uint32_t outputs[2], met[2];
+};
+
 struct __align__(16) Shared {
+    uint4 taken;  // the answer to a request for another CTA's work
     // a tile's keys (rotated part included) and its values, by the tile's number mod 2
     uint64_t k_full[2], v_full[2], k_free[2], v_free[2];
-    uint64_t q_full, s_full[2], p_ready[2], o_done[2], v_clean, drained;
+    uint64_t q_full[2], q_free[2], s_full[2], p_ready[2], o_done[2], v_clean, drained;
+    uint64_t near_end, answer, item_full[2], item_free[2];
+    Item item[2];
     uint32_t tmem;
     volatile int abort;
     float other[2][2][TM];  // what the two threads of a row tell each other, by tile and half
@@ -65,6 +81,16 @@ __device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity)
 // leaves issue slots and shared memory to the others.
 __device__ __forceinline__ bool wait_long(Shared &sh, uint64_t *bar, uint32_t parity) {
     for (uint32_t it = 0; it < WAIT_LIMIT; ++it) {
+        if (mbar_test(bar, parity)) return true;
+        if (sh.abort) return false;
+    }
+    sh.abort = 1;
+    return false;
+}
+
+// And for one that may take as long as a whole pair, on others whose own waits are bounded.
+__device__ __forceinline__ bool wait_far(Shared &sh, uint64_t *bar, uint32_t parity) {
+    for (uint32_t it = 0; it < 16 * WAIT_LIMIT; ++it) {
         if (mbar_test(bar, parity)) return true;
         if (sh.abort) return false;
     }
@@ -116,15 +142,12 @@ __host__ __device__ constexpr uint32_t idesc_of(int n, bool b_rows_k) {
 
 __device__ __forceinline__ int pairs_of(int2 q) { return (q.y - q.x + 2 * TM - 1) / (2 * TM); }
 
-// A CTA's sequence and the pair of query tiles in it; pair -1: none.
-struct Work {
-    int q0, nq, k0, nk, pair;
-};
 // The pair of number `rank`, for a warp whose lanes hold sequences b0 .. b1 - 1, with `at`
 // pairs before them and `sum` of their own.  Up to 32 sequences (one a lane), pairs go by
 // their place in their sequence, the furthest first; beyond, sequence by sequence.
-__device__ __forceinline__ Work find_work(const Params &p, int b0, int b1, int at, int sum, int rank) {
-    Work w = {0, 0, 0, 0, -1};
+__device__ __forceinline__ Work find_work(const Params &p, int b0, int b1, int at, int sum, int rank,
+                                          int head) {
+    Work w = {0, 0, 0, 0, -1, head};
     bool mine = at <= rank && rank < at + sum;
     int pair = at + sum - 1 - rank;
     if (p.B > 1 && p.B <= 32) {
@@ -150,7 +173,7 @@ __device__ __forceinline__ Work find_work(const Params &p, int b0, int b1, int a
             const int n = pairs_of(q);
             if (p.B <= 32 || rank < at + n) {
                 const int2 k = bounds(p.cu_k, b, p.Tk, bad);
-                w = {q.x, q.y - q.x, k.x, k.y - k.x, p.B <= 32 ? pair : n - 1 - (rank - at)};
+                w = {q.x, q.y - q.x, k.x, k.y - k.x, p.B <= 32 ? pair : n - 1 - (rank - at), head};
                 break;
             }
             at += n;
@@ -166,10 +189,62 @@ __device__ __forceinline__ Work find_work(const Params &p, int b0, int b1, int a
     return w;
 }
 
-// The slot `n` behind slot s of the ring.
-__device__ __forceinline__ int slot_behind(int s, int n, int slots) {
-    return s + n >= slots ? s + n - slots : s + n;
+// The request for the work of a CTA that has not started (which then never does), and what it
+// gave: that CTA's number, or -1 when there is none left.  After a -1 no more may be asked.
+__device__ __forceinline__ void ask_for_work(uint4 *dst, uint64_t *bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+            smem_addr(dst)),
+        "r"(smem_addr(bar))
+        : "memory");
 }
+__device__ __forceinline__ int work_given(const uint4 *src) {
+    int cta;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 h, [%1];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "mov.b32 %0, -1;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n\t}"
+        : "=r"(cta)
+        : "r"(smem_addr(src))
+        : "memory");
+    return cta;
+}
+
+// How far a pair of query tiles reaches: its first query's place in the sequence, and the key
+// tiles that either tile meets (a tile's last query sees the most).
+struct Extent {
+    int row0, n0, n1, n, nk;
+    __device__ __forceinline__ Extent(const Work &w) : row0(w.pair * 2 * TM), nk(w.nk) {
+        n0 = met(w, 0);
+        n1 = met(w, 1);
+        n = max(n0, n1);
+    }
+    __device__ __forceinline__ int met(const Work &w, int t) const {
+        const int first = row0 + t * TM, end = min(first + TM, w.nq);
+        const int seen = end + w.nk - w.nq;
+        return first >= w.nq || seen <= 0 ? 0 : (seen + TN - 1) / TN;
+    }
+    __device__ __forceinline__ int tiles(int t) const { return t ? n1 : n0; }
+    // the tile of queries that uses every chunk last
+    __device__ __forceinline__ int last() const { return n1 >= n0 ? 1 : 0; }
+    // the tile that the sequence's keys end in, if the pair meets it and it is not a whole one
+    __device__ __forceinline__ int tail() const { return nk % TN != 0 && nk / TN < n ? nk / TN : -1; }
+};
+
+// What follows from the chunks of a key tile and of a value tile.
+template <int KC, int VC>
+struct Sizes {
+    static constexpr int LEFT = (SMEM_MAX - SMEM_EXTRA) / CHUNK - 2 * KC;
+    static constexpr int TILE = KC + VC, SLOTS = LEFT < 2 * TILE ? LEFT : 2 * TILE;
+    static constexpr int SMEM = (2 * KC + SLOTS) * CHUNK + SMEM_EXTRA;
+    static_assert(SLOTS > TILE, "a tile and the start of the next");
+    // the slot `n` behind slot s of the ring
+    static __device__ __forceinline__ int behind(int s, int n) {
+        return s + n >= SLOTS ? s + n - SLOTS : s + n;
+    }
+};
 
 // KC, VC: the 64-column chunks of a key tile (N / 64 + 1 with the rotated one) and of a value
 // tile (V / 64).
@@ -178,56 +253,43 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkv,
                  const __grid_constant__ CUtensorMap mrot, const Params p) {
     extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's period
+    using Z = Sizes<KC, VC>;
     const uint32_t q_s = smem_addr(smem), ring = q_s + 2 * KC * CHUNK;
-    Shared &sh = *reinterpret_cast<Shared *>(smem + (2 * KC + p.slots) * CHUNK);
+    Shared &sh = *reinterpret_cast<Shared *>(smem + Z::SMEM - SMEM_EXTRA);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // heads side by side, the longest pairs of all of them first: what is left at the end is
-    // short, and CTAs that share a head's keys walk them at the same time
-    const int rank = blockIdx.x / p.Hq, head = blockIdx.x - rank * p.Hq;
 
-    // ---- which pair of tiles.  Every warp finds it by itself, from a scan of the sequences'
-    // pairs with a run of sequences a lane.
-    Work my;
-    {
+    // ---- warp 2 finds work, from a scan of the sequences' pairs with a run of sequences a lane.
+    // Work goes by rank: heads side by side, the longest pairs of all of them first, so that
+    // what is left at the end is short, and CTAs that share a head's keys walk them at the
+    // same time.
+    int b0 = 0, b1 = 0, sum = 0, at = 0;
+    const auto work_of = [&](int cta) {
+        return find_work(p, b0, b1, at, sum, cta / p.Hq, cta % p.Hq);
+    };
+    if (warp == 2) {
         const int per = (p.B + 31) / 32;
-        const int b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
+        b0 = min(p.B, lane * per);
+        b1 = min(p.B, b0 + per);
         bool bad = false;
-        int sum = 0;
         for (int b = b0; b < b1; ++b) sum += pairs_of(bounds(p.cu_q, b, p.Tq, bad));
-        int at = sum;
+        at = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xFFFFFFFFu, at, o);
             if (lane >= o) at += v;
         }
         at -= sum;
-        my = find_work(p, b0, b1, at, sum, rank);
-        if (blockIdx.x == 0 && p.status && warp == 0) {
+        const Work w = work_of(blockIdx.x);
+        if (lane == 0) sh.item[0] = Item{w, 0, 0, {0, 0}, {0, 0}};
+        if (blockIdx.x == 0 && p.status) {
             for (int b = b0; b < b1; ++b) bounds(p.cu_k, b, p.Tk, bad);
             if (bad) atomicOr(p.status, MTPSPEC_STATUS_BAD_PARAM);
         }
-        if (my.pair < 0) return;  // the grid has a CTA for every pair that there might be
-        if (warp == 2) {
-            // The CTA that comes one wave later begins with its queries and first keys: they
-            // go to L2 now, so that it does not begin with the way from HBM.
-            const unsigned next = blockIdx.x + WAVE;
-            if (next < gridDim.x) {
-                const int nr = next / p.Hq, h = next - nr * p.Hq;
-                const Work w = find_work(p, b0, b1, at, sum, nr);
-                if (w.pair >= 0 && elect_one()) {
-                    for (int t = 0; t < 2; ++t)
-                        for (int c = 0; c < KC; ++c)
-                            tma_prefetch_3d(&mq, c * 64, h, w.q0 + (w.pair * 2 + t) * TM);
-                    for (int c = 0; c < KC + VC; ++c)
-                        if (c != KC - 1)
-                            tma_prefetch_3d(&mkv, c < KC ? c * 64 : p.N + (c - KC) * 64, h, w.k0);
-                }
-            }
-        }
     }
     if (threadIdx.x == 0) {
-        mbar_init(&sh.q_full, 1);
         for (int t = 0; t < 2; ++t) {
+            mbar_init(&sh.q_full[t], 1);
+            mbar_init(&sh.q_free[t], 1);
             mbar_init(&sh.k_full[t], 1);
             mbar_init(&sh.v_full[t], 1);
             mbar_init(&sh.k_free[t], 1);
@@ -238,6 +300,12 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         }
         mbar_init(&sh.v_clean, 256);
         mbar_init(&sh.drained, 1);
+        mbar_init(&sh.near_end, 1);
+        mbar_init(&sh.answer, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.item_full[i], 1);
+            mbar_init(&sh.item_free[i], 18);  // the producer, the issuer, sixteen softmax warps
+        }
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(&mq);
@@ -255,67 +323,81 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    const int nq = my.nq, nk = my.nk, row0 = my.pair * 2 * TM;
-    // key tiles that a tile of queries meets; its last query sees the most
-    const auto key_tiles = [&](int t) {
-        const int first = row0 + t * TM, last = min(first + TM, nq) - 1;
-        const int seen = last + nk - nq + 1;
-        return first >= nq || seen <= 0 ? 0 : (seen + TN - 1) / TN;
+    // Every role goes through the CTA's items; the one after number `item` (false: none).
+    const auto next_item = [&](uint32_t item, bool one_thread) {
+        if (one_thread || lane == 0) mbar_arrive(&sh.item_free[item & 1]);
+        ++item;
+        return wait_long(sh, &sh.item_full[item & 1], ((item - 1) >> 1) & 1) && sh.item[item & 1].w.pair >= 0;
     };
-    const int n0 = key_tiles(0), n1 = key_tiles(1), n = max(n0, n1);
-    const int last = n1 >= n0 ? 1 : 0;  // the tile of queries that uses every chunk last
-    const int tail = nk % TN != 0 && nk / TN < n ? nk / TN : -1;  // the tile that keys end in
 
-    if (warp < 4) {
+    if (sh.item[0].w.pair < 0) {
+        // nothing: the grid has a CTA for every pair that there might be
+    } else if (warp < 4) {
         if (warp == 0) {
             if (elect_one()) {
                 // ---- producer
-                if (n > 0) {
-                    mbar_expect_tx(&sh.q_full, ((n0 > 0) + (n1 > 0)) * KC * CHUNK);
-                    for (int t = 0; t < 2; ++t)
-                        if ((t ? n1 : n0) > 0)
-                            for (int c = 0; c < KC; ++c)
-                                tma_load_3d(q_s + (t * KC + c) * CHUNK, &mq, c * 64, head,
-                                            my.q0 + row0 + t * TM, &sh.q_full);
-                }
                 // The ring holds at most two tiles' chunks, so a slot's last use was in one of
                 // the two tiles before; what was waited for once is not waited for again.
-                int slot = 0, k_done = -1, v_done = -1;
-                int j = 0;
-                for (; j < n && !sh.abort; ++j) {
+                // Tiles are numbered through all pairs of the CTA.
+                int64_t j = 0, k_done = -1, v_done = -1;
+                int slot = 0, q_uses[2] = {0, 0};
+                for (uint32_t item = 0;; ++item) {
+                    const Work my = sh.item[item & 1].w;
+                    const Extent x(my);
 #pragma unroll
-                    for (int c = 0; c < KC + VC; ++c) {
-                        const int was = j * (KC + VC) + c - p.slots;  // the chunk there before
-                        if (was >= 0) {
-                            const int wj = was < (j - 1) * (KC + VC) ? j - 2 : was < j * (KC + VC) ? j - 1 : j;
-                            const bool keys = was - wj * (KC + VC) < KC;
-                            int &done = keys ? k_done : v_done;
-                            if (wj > done) {
-                                if (!wait(sh, keys ? &sh.k_free[wj & 1] : &sh.v_free[wj & 1], (wj >> 1) & 1))
-                                    break;
-                                done = wj;
-                            }
+                    for (int t = 0; t < 2; ++t)
+                        if (x.tiles(t) > 0) {
+                            if (q_uses[t] > 0 && !wait(sh, &sh.q_free[t], (q_uses[t] - 1) & 1)) break;
+                            ++q_uses[t];
+                            mbar_expect_tx(&sh.q_full[t], KC * CHUNK);
+                            for (int c = 0; c < KC; ++c)
+                                tma_load_3d(q_s + (t * KC + c) * CHUNK, &mq, c * 64, my.head,
+                                            my.q0 + x.row0 + t * TM, &sh.q_full[t]);
                         }
-                        uint64_t *bar = c < KC ? &sh.k_full[j & 1] : &sh.v_full[j & 1];
-                        if (c == 0) mbar_expect_tx(bar, KC * CHUNK);
-                        if (c == KC) mbar_expect_tx(bar, VC * CHUNK);
-                        const uint32_t dst = ring + slot * CHUNK;
-                        if (c == KC - 1)
-                            tma_load_3d(dst, &mrot, 0, 0, my.k0 + j * TN, bar);
-                        else
-                            tma_load_3d(dst, &mkv, c < KC ? c * 64 : p.N + (c - KC) * 64, head,
-                                        my.k0 + j * TN, bar);
-                        slot = slot_behind(slot, 1, p.slots);
+                    for (int i = 0; i < x.n && !sh.abort; ++i, ++j) {
+#pragma unroll
+                        for (int c = 0; c < Z::TILE; ++c) {
+                            constexpr int TILE = Z::TILE;
+                            // the chunk there before, and how many tiles ago
+                            const int was = c - Z::SLOTS + 2 * TILE;
+                            const int64_t wj = j - (was < TILE ? 2 : was < 2 * TILE ? 1 : 0);
+                            if (wj >= 0) {
+                                const bool keys = was % TILE < KC;
+                                int64_t &done = keys ? k_done : v_done;
+                                if (wj > done) {
+                                    if (!wait(sh, keys ? &sh.k_free[wj & 1] : &sh.v_free[wj & 1], (wj >> 1) & 1))
+                                        break;
+                                    done = wj;
+                                }
+                            }
+                            uint64_t *bar = c < KC ? &sh.k_full[j & 1] : &sh.v_full[j & 1];
+                            if (c == 0) mbar_expect_tx(bar, KC * CHUNK);
+                            if (c == KC) mbar_expect_tx(bar, VC * CHUNK);
+                            const uint32_t dst = ring + slot * CHUNK;
+                            if (c == KC - 1)
+                                tma_load_3d(dst, &mrot, 0, 0, my.k0 + i * TN, bar);
+                            else
+                                tma_load_3d(dst, &mkv, c < KC ? c * 64 : p.N + (c - KC) * 64, my.head,
+                                            my.k0 + i * TN, bar);
+                            slot = Z::behind(slot, 1);
+                        }
                     }
+                    // All that this pair needs is on its way, a tile or two before it is used:
+                    // the time to ask for more.  (One, two or five tiles earlier, when work may
+                    // go to a CTA that will be free later than another: 8 x 800 tokens x 32
+                    // heads 93 -> 94.5, 96, 98; by the issuer at its last tile, 99 us.)
+                    mbar_arrive(&sh.near_end);
+                    if (sh.abort || !next_item(item, true)) break;
                 }
                 if (sh.abort) {
                     // let the copies in flight land: the last two tiles' and the queries' (a
                     // fill that was cut off never completes: its wait runs to the limit)
-                    for (int i = max(0, j - 2); i < j; ++i) {
+                    for (int64_t i = j > 2 ? j - 2 : 0; i < j; ++i) {
                         wait_out(&sh.k_full[i & 1], (i >> 1) & 1);
                         wait_out(&sh.v_full[i & 1], (i >> 1) & 1);
                     }
-                    if (n > 0) wait_out(&sh.q_full, 0);
+                    for (int t = 0; t < 2; ++t)
+                        if (q_uses[t] > 0) wait_out(&sh.q_full[t], (q_uses[t] - 1) & 1);
                 }
             }
         } else if (warp == 1) {
@@ -330,7 +412,7 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                     const uint64_t a = qd + t * (KC * (CHUNK >> 4));
 #pragma unroll
                     for (int c = 0; c < KC; ++c) {
-                        const uint64_t b = kd + slot_behind(slot, c, p.slots) * (CHUNK >> 4);
+                        const uint64_t b = kd + Z::behind(slot, c) * (CHUNK >> 4);
                         if (c < KC - 1 || p.R == 64) {
 #pragma unroll
                             for (int u = 0; u < 4; ++u)
@@ -345,7 +427,7 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 const auto products = [&](int slot, int t, int j) {
                     const uint32_t a = tmem + S_COL + t * 128, d = tmem + O_COL + t * 128;
                     const uint64_t b = vd + slot * (CHUNK >> 4);
-                    if (VC == 1 || slot + 1 < p.slots) {
+                    if (VC == 1 || slot + 1 < Z::SLOTS) {
 #pragma unroll
                         for (int u = 0; u < 8; ++u)
                             mma_ts(d, a + 8 * u, b + u * (2048 >> 4), id_o, (j | u) != 0);
@@ -357,38 +439,116 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                         }
                     }
                 };
-                int k = 0;  // the slot of the next tile's keys
-                if (n > 0 && wait(sh, &sh.q_full, 0) && wait(sh, &sh.k_full[0], 0)) {
-                    tc_fence_after();
-                    if (n0 > 0) scores(k, 0);
-                    if (n1 > 0) scores(k, 1);
-                    mma_commit(&sh.k_free[0]);
-                }
-                for (int j = 0; j < n && !sh.abort; ++j) {
-                    const int v = slot_behind(k, KC, p.slots);
-                    k = slot_behind(v, VC, p.slots);
-                    if (!wait(sh, &sh.v_full[j & 1], (j >> 1) & 1)) break;
-                    bool keys = false;  // tile j + 1's have been waited for
-                    if (j == tail && !wait(sh, &sh.v_clean, 0)) break;
+                // the slot of the next tile's keys; the tile's number through all pairs, and the
+                // numbers of tiles, pairs and cleared tails so far, as far as parities go
+                int k = 0;
+                uint32_t g = 0, q_uses[2] = {0, 0}, p_uses[2] = {0, 0}, tails = 0;
+                for (uint32_t item = 0;; ++item) {
+                    const Work my = sh.item[item & 1].w;
+                    const Extent x(my);
+                    const int last = x.last(), tail = x.tail();
+                    if (x.n > 0) {
+                        if (!wait(sh, &sh.k_full[g & 1], (g >> 1) & 1)) break;
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const int nt = t ? n1 : n0;
-                        if (j >= nt) continue;
-                        if (!wait(sh, &sh.p_ready[t], j & 1)) break;
-                        tc_fence_after();
-                        products(v, t, j);
-                        if (t == last) mma_commit(&sh.v_free[j & 1]);
-                        if (j + 1 == nt) mma_commit(&sh.o_done[t]);
-                        if (j + 1 < nt) {
-                            if (!keys && !wait(sh, &sh.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1)) break;
-                            keys = true;
-                            scores(k, t);
-                            if (t == last) mma_commit(&sh.k_free[(j + 1) & 1]);
+                        for (int t = 0; t < 2; ++t)
+                            if (x.tiles(t) > 0) {
+                                if (!wait(sh, &sh.q_full[t], q_uses[t] & 1)) break;
+                                ++q_uses[t];
+                                tc_fence_after();
+                                scores(k, t);
+                                if (x.tiles(t) == 1) mma_commit(&sh.q_free[t]);
+                            }
+                        mma_commit(&sh.k_free[g & 1]);
+                    }
+                    for (int j = 0; j < x.n && !sh.abort; ++j, ++g) {
+                        const int v = Z::behind(k, KC);
+                        k = Z::behind(v, VC);
+                        if (!wait(sh, &sh.v_full[g & 1], (g >> 1) & 1)) break;
+                        bool keys = false;  // tile j + 1's have been waited for
+                        if (j == tail && !wait(sh, &sh.v_clean, tails++ & 1)) break;
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const int nt = x.tiles(t);
+                            if (j >= nt) continue;
+                            if (!wait(sh, &sh.p_ready[t], p_uses[t]++ & 1)) break;
+                            tc_fence_after();
+                            products(v, t, j);
+                            if (t == last) mma_commit(&sh.v_free[g & 1]);
+                            if (j + 1 == nt) mma_commit(&sh.o_done[t]);
+                            if (j + 1 < nt) {
+                                if (!keys && !wait(sh, &sh.k_full[(g + 1) & 1], ((g + 1) >> 1) & 1)) break;
+                                keys = true;
+                                scores(k, t);
+                                if (j + 2 == nt) mma_commit(&sh.q_free[t]);
+                                if (t == last) mma_commit(&sh.k_free[(g + 1) & 1]);
+                            }
                         }
                     }
+                    if (sh.abort || !next_item(item, true)) break;
                 }
                 mma_commit(&sh.drained);
                 wait_out(&sh.drained, 0);
+            }
+        } else if (warp == 2) {
+            // ---- the next work: that of a CTA which has not started yet, so that its queries
+            // and keys are on their way while this CTA finishes what it has.  (A CTA a pair
+            // spent some 11,000 cycles on its start and its end; so 8 x 800 tokens x 32 heads
+            // took 126 us, not 93, and 8192 x 32 heads 472, not 442.)
+            Item it = sh.item[0];
+            for (uint32_t item = 0;; ++item) {
+                if (!wait_far(sh, &sh.near_end, item & 1)) break;
+                if (lane == 0) {
+                    mbar_expect_tx(&sh.answer, sizeof(uint4));
+                    ask_for_work(&sh.taken, &sh.answer);
+                }
+                __syncwarp();
+                if (!wait_long(sh, &sh.answer, item & 1)) {
+                    wait_out(&sh.answer, item & 1);
+                    break;
+                }
+                const int cta = work_given(&sh.taken);
+                fence_async_smem();  // read before the next answer overwrites it
+                const Extent was(it.w);
+                it.g0 += was.n;
+                it.slot0 = (it.slot0 + (was.n % Z::SLOTS) * Z::TILE) % Z::SLOTS;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    it.met[t] += was.tiles(t);
+                    it.outputs[t] += was.tiles(t) > 0;
+                }
+                it.w.pair = -1;
+                if (cta >= 0) it.w = work_of(cta);
+                // the item before this slot's last is left behind by all
+                if (item > 0 && !wait_long(sh, &sh.item_free[(item - 1) & 1], ((item - 1) >> 1) & 1)) break;
+                if (lane == 0) {
+                    sh.item[(item + 1) & 1] = it;
+                    mbar_arrive(&sh.item_full[(item + 1) & 1]);
+                }
+                const Work w = it.w;
+                if (w.pair < 0) {
+                    // whatever has not started by now has no work either
+                    for (uint32_t more = item + 1; cta >= 0; ++more) {
+                        if (lane == 0) {
+                            mbar_expect_tx(&sh.answer, sizeof(uint4));
+                            ask_for_work(&sh.taken, &sh.answer);
+                        }
+                        __syncwarp();
+                        if (!wait_long(sh, &sh.answer, more & 1)) wait_out(&sh.answer, more & 1);
+                        if (sh.abort || work_given(&sh.taken) < 0) break;
+                        fence_async_smem();
+                    }
+                    break;
+                }
+                if (elect_one()) {
+                    const Extent x(w);
+                    for (int t = 0; t < 2; ++t)
+                        for (int c = 0; c < KC && x.tiles(t) > 0; ++c)
+                            tma_prefetch_3d(&mq, c * 64, w.head, w.q0 + x.row0 + t * TM);
+                    for (int c = 0; c < KC + VC && x.n > 0; ++c)
+                        if (c != KC - 1)
+                            tma_prefetch_3d(&mkv, c < KC ? c * 64 : p.N + (c - KC) * 64, w.head, w.k0);
+                }
+                __syncwarp();
             }
         }
     } else {
@@ -396,10 +556,6 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         // the chain scores - weights - products of a tile took longer than the tensor cores
         // need for both tiles.)
         const int t = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, r = (warp & 3) * 32 + lane;
-        const int nt = t ? n1 : n0;
-        const int row = row0 + t * TM + r;
-        const int limit = row + nk - nq + 1;           // keys that this row sees
-        const int sure = row0 + t * TM + nk - nq + 1;  // that every row of the tile sees
         const uint32_t lane_bits = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_t = tmem + lane_bits + S_COL + t * 128, o_t = tmem + lane_bits + O_COL + t * 128;
         const int pair_bar = 1 + t * 4 + (warp & 3);
@@ -409,116 +565,130 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
             return sh.other[t][half ^ 1][r];
         };
-        float m_ref = -INFINITY, l = 0.0f;
-        for (int j = 0; j < nt; ++j) {
-            wait_long(sh, &sh.s_full[t], j & 1);
-            tc_fence_after();
-            uint32_t x[2][32];
-            tmem_ld32(s_t + half * 64, x[0]);
-            tmem_ld32(s_t + half * 64 + 32, x[1]);
-            if (__builtin_expect(j == tail && t == last, 0)) {
-                // value rows behind the sequence's last key: whatever follows there must not
-                // meet the zero weights.  (The barrier's fill before this one is used up by
-                // now, so the phase is this fill's.)
-                wait(sh, &sh.v_full[tail & 1], (tail >> 1) & 1);
-                const int z0 = nk - tail * TN;
-#pragma unroll
-                for (int c = KC; c < KC + VC; ++c) {
-                    const uint32_t v = ring + ((tail * (KC + VC) + c) % p.slots) * CHUNK + z0 * 128;
-                    for (int i = half * 128 + r; i < (TN - z0) * 8; i += 256)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + i * 16), "r"(0)
-                                     : "memory");
-                }
-                fence_async_smem();
-                mbar_arrive(&sh.v_clean);
+        for (uint32_t item = 0;; ++item) {
+            // (what only the pair's end needs stays in shared memory meanwhile)
+            const volatile Item &my = sh.item[item & 1];
+            int nt, tail, limit;  // limit: keys that this row sees
+            {
+                const Work w = {0, my.w.nq, 0, my.w.nk, my.w.pair, 0};
+                const Extent e(w);
+                nt = e.tiles(t);
+                tail = e.last() == t ? e.tail() : -1;  // the tile whose values are to be cleared
+                limit = e.row0 + t * TM + r + w.nk - w.nq + 1;
             }
-            tmem_wait_ld();
-            if (__builtin_expect(j * TN + TN > sure, 0)) {
-                const int seen = limit - j * TN - half * 64;
+            uint32_t parity = my.met[t] & 1;
+            float m_ref = -INFINITY, l = 0.0f;
+            for (int j = 0; j < nt; ++j) {
+                wait_long(sh, &sh.s_full[t], parity);
+                parity ^= 1;
+                tc_fence_after();
+                uint32_t x[2][32];
+                tmem_ld32(s_t + half * 64, x[0]);
+                tmem_ld32(s_t + half * 64 + 32, x[1]);
+                if (__builtin_expect(j == tail, 0)) {
+                    // value rows behind the sequence's last key: whatever follows there must not
+                    // meet the zero weights.  (The barrier's fill before this one is used up by
+                    // now, so the phase is this fill's.)
+                    const uint32_t g = my.g0 + tail;
+                    wait(sh, &sh.v_full[g & 1], (g >> 1) & 1);
+                    const int z0 = my.w.nk - tail * TN, first = my.slot0 + (tail % Z::SLOTS) * Z::TILE;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    if (i >= seen) x[0][i] = 0xFF800000u;
-                    if (i + 32 >= seen) x[1][i] = 0xFF800000u;
+                    for (int c = KC; c < KC + VC; ++c) {
+                        const uint32_t v = ring + (first + c) % Z::SLOTS * CHUNK + z0 * 128;
+                        for (int i = half * 128 + r; i < (TN - z0) * 8; i += 256)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + i * 16), "r"(0)
+                                         : "memory");
+                    }
+                    fence_async_smem();
+                    mbar_arrive(&sh.v_clean);
                 }
+                tmem_wait_ld();
+                if (__builtin_expect(j * TN + TN > limit - r, 0)) {  // more than every row sees
+                    const int seen = limit - j * TN - half * 64;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        if (i >= seen) x[0][i] = 0xFF800000u;
+                        if (i + 32 >= seen) x[1][i] = 0xFF800000u;
+                    }
+                }
+                float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    top4[i & 3] = max3(top4[i & 3], __uint_as_float(x[0][i]), __uint_as_float(x[1][i]));
+                const float mine = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
+                // (the second barrier of a tile is p_ready: nobody writes the next value before
+                // the products have taken both threads' weights)
+                const float top = fmaxf(mine, swap(mine)) * p.scale2;
+                const bool raise = top > m_ref + LAZY;
+                if (__builtin_expect(j > 0 && __any_sync(0xFFFFFFFFu, raise), 0)) {
+                    // the scores came after the products of the tile before: the output is free
+                    const float f = raise ? ex2(m_ref - top) : 1.0f;
+                    l *= f;
+#pragma unroll
+                    for (int c = half * (VC * 32); c < (half + 1) * (VC * 32); c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(o_t + c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st16(o_t + c, o);
+                    }
+                }
+                if (raise) m_ref = top;
+                const float m_use = m_ref == -INFINITY ? 0.0f : m_ref;
+                const uint64_t scale_2 = pack2(p.scale2, p.scale2), minus_m = pack2(-m_use, -m_use);
+                uint64_t part[2] = {0, 0};  // two pairs of sums
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float e0, e1;
+                        unpack2(fma2(pack2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])),
+                                     scale_2, minus_m), e0, e1);
+                        e0 = ex2(e0);
+                        e1 = ex2(e1);
+                        part[i & 1] = add2(part[i & 1], pack2(e0, e1));
+                        w[i] = T::narrow2(e0, e1);
+                    }
+                    tmem_st16(s_t + half * 32 + 16 * c, w);
+                }
+                tmem_wait_st();
+                float l0, l1;
+                unpack2(add2(part[0], part[1]), l0, l1);
+                l += l0 + l1;
+                tc_fence_before();
+                mbar_arrive(&sh.p_ready[t]);
             }
-            float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            if (nt > 0) {
+                wait_long(sh, &sh.o_done[t], my.outputs[t] & 1);
+                tc_fence_after();
+            }
+            l += swap(l);
+            const int row = my.w.pair * 2 * TM + t * TM + r, head = my.w.head;
+            const bool real = row < my.w.nq;
+            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            const int64_t tok = my.w.q0 + row;
+            if (real && half == 0 && p.lse)
+                p.lse[tok * p.Hq + head] = l > 0.0f ? (m_ref + log2f(l)) * LN2 : -INFINITY;
+            uint16_t *dst = p.out + tok * p.out_tok + head * p.out_head + half * (VC * 32);
+            // 32 bytes a store, a whole sector, where the rows allow it
+            const bool sectors = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                top4[i & 3] = max3(top4[i & 3], __uint_as_float(x[0][i]), __uint_as_float(x[1][i]));
-            const float mine = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
-            // (the second barrier of a tile is p_ready: nobody writes the next value before
-            // the products have taken both threads' weights)
-            const float top = fmaxf(mine, swap(mine)) * p.scale2;
-            const bool raise = top > m_ref + LAZY;
-            if (__builtin_expect(j > 0 && __any_sync(0xFFFFFFFFu, raise), 0)) {
-                // the scores came after the products of the tile before: the output is free
-                const float f = raise ? ex2(m_ref - top) : 1.0f;
-                l *= f;
-#pragma unroll
-                for (int c = half * (VC * 32); c < (half + 1) * (VC * 32); c += 16) {
-                    uint32_t o[16];
-                    tmem_ld16(o_t + c, o);
+            for (int c = 0; c < VC; ++c) {
+                uint32_t o[32] = {};
+                if (nt > 0) {
+                    tmem_ld32(o_t + half * (VC * 32) + 32 * c, o);
                     tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                    tmem_st16(o_t + c, o);
                 }
-            }
-            if (raise) m_ref = top;
-            const float m_use = m_ref == -INFINITY ? 0.0f : m_ref;
-            const uint64_t scale_2 = pack2(p.scale2, p.scale2), minus_m = pack2(-m_use, -m_use);
-            uint64_t part[2] = {0, 0};  // two pairs of sums
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t w[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float e0, e1;
-                    unpack2(fma2(pack2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])),
-                                 scale_2, minus_m), e0, e1);
-                    e0 = ex2(e0);
-                    e1 = ex2(e1);
-                    part[i & 1] = add2(part[i & 1], pack2(e0, e1));
-                    w[i] = T::narrow2(e0, e1);
-                }
-                tmem_st16(s_t + half * 32 + 16 * c, w);
-            }
-            tmem_wait_st();
-            float l0, l1;
-            unpack2(add2(part[0], part[1]), l0, l1);
-            l += l0 + l1;
-            tc_fence_before();
-            mbar_arrive(&sh.p_ready[t]);
-        }
-        if (nt > 0) {
-            wait_long(sh, &sh.o_done[t], 0);
-            tc_fence_after();
-        }
-        l += swap(l);
-        const bool real = row < nq;
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-        const int64_t tok = my.q0 + row;
-        if (real && half == 0 && p.lse)
-            p.lse[tok * p.Hq + head] = l > 0.0f ? (m_ref + log2f(l)) * LN2 : -INFINITY;
-        uint16_t *dst = p.out + tok * p.out_tok + head * p.out_head + half * (VC * 32);
-        // 32 bytes a store, a whole sector, where the rows allow it
-        const bool sectors = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
-        uint32_t o[VC][32];
-        if (nt > 0) {
-#pragma unroll
-            for (int c = 0; c < VC; ++c) tmem_ld32(o_t + half * (VC * 32) + 32 * c, o[c]);
-            tmem_wait_ld();
-        }
-        if (real) {
-#pragma unroll
-            for (int c = 0; c < VC; ++c)
+                if (!real) continue;
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
                     uint32_t y[8];
 #pragma unroll
                     for (int u = 0; u < 8; ++u)
-                        y[u] = nt > 0 ? T::narrow2(__uint_as_float(o[c][16 * v + 2 * u]) * inv,
-                                                   __uint_as_float(o[c][16 * v + 2 * u + 1]) * inv)
+                        y[u] = nt > 0 ? T::narrow2(__uint_as_float(o[16 * v + 2 * u]) * inv,
+                                                   __uint_as_float(o[16 * v + 2 * u + 1]) * inv)
                                       : 0u;
                     uint16_t *d = dst + c * 32 + v * 16;
                     if (sectors) {
@@ -528,6 +698,12 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                         *reinterpret_cast<uint4 *>(d + 8) = make_uint4(y[4], y[5], y[6], y[7]);
                     }
                 }
+            }
+            // The next pair's products overwrite this output once its first weights are there,
+            // which come after these reads.  Both threads of a row have read each other's sum.
+            tc_fence_before();
+            asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+            if (!next_item(item, false)) break;
         }
     }
     tc_fence_before();
@@ -544,7 +720,7 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
 template <typename T, int KC, int VC>
 cudaError_t launch(const CUtensorMap &mq, const CUtensorMap &mkv, const CUtensorMap &mrot,
                    const Params &p, cudaStream_t stream) {
-    const int smem = (2 * KC + p.slots) * CHUNK + SMEM_EXTRA;
+    constexpr int smem = Sizes<KC, VC>::SMEM;
     static AttrCache attr;
     cudaError_t e = ensure_attr(k_latent_prefill<T, KC, VC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem, attr);
     if (e != cudaSuccess) return e;
@@ -600,9 +776,6 @@ cudaError_t run_latent_prefill(const LatentPrefillArgs &a, int dtype, cudaStream
     p.N = a.N;
     p.R = a.R;
     p.V = a.V;
-    const int q_bytes = 2 * (a.N / 64 + 1) * lpf::CHUNK;
-    p.slots = std::min<int>(2 * (a.N / 64 + 1 + a.V / 64),
-                            (lpf::SMEM_MAX - lpf::SMEM_EXTRA - q_bytes) / lpf::CHUNK);
     p.ranks = static_cast<int>((a.Tq + 2 * lpf::TM - 1) / (2 * lpf::TM) + a.B - 1);
     p.scale2 = a.scale * lpf::LOG2E;
     p.out = a.out;
