@@ -3,11 +3,18 @@
 // rotated by the same angles, in one launch.
 //
 // The work is bytes: every value is read once and written once, and a rotation is four
-// products a pair.  Two kinds of CTA share the grid.  The first blocks take the queries, 16
-// elements a thread (two 16-byte loads and stores): eight neighbouring pairs, or eight pairs
-// of the two halves, so that one thread's cosines and sines are two runs of 32 bytes either
-// way.  The blocks behind them take a token a warp: the latent stays in registers between
-// the sum of squares and the scaling (at most 512 values, two vectors a lane).
+// products a pair.  Two kinds of CTA share the grid.  The first blocks take the queries, in
+// units of 16 elements (two 16-byte loads and stores): eight neighbouring pairs, or eight pairs
+// of the two halves, so that a unit's cosines and sines are two runs of 32 bytes either way.
+// The blocks behind them take a token a warp: the latent stays in registers between the sum of
+// squares and the scaling (at most 512 values, two vectors a lane).
+//
+// Few calls are long enough to be bound by HBM: the bound is the chain position - angles -
+// stores of a block times the blocks that an SM goes through, so a thread loads two units
+// before it needs their positions.  12k tokens x 32 heads (126 MB, in a graph): 24.5 us, 5.1
+// TB/s, against 28.6 with one unit a thread and 27.5 with four (80 registers, fewer threads);
+// 1024 tokens x 128 heads: 8.9 us against 9.4 and 9.5; from 4 to 64 tokens the same or better.
+// One token: 3.1 us, the launch.
 #include "common.cuh"
 #include "kernels.h"
 #include "half_types.cuh"
@@ -17,6 +24,7 @@ namespace la {
 
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
+constexpr int UNITS = 2;  // units of sixteen query elements a thread takes, THREADS apart
 
 // Where a token's row goes: `angle` says whether its row and position are good, `page`
 // is its page or -1 (a padding token, or one that is not written).
@@ -51,21 +59,30 @@ __device__ __forceinline__ Slot find_slot(const LatentAppendArgs &a, int64_t t) 
     return s;
 }
 
-// Pairs i0 .. i0 + 7 of one vector of R values: the rotation of x (read) into y (written).
+// Sixteen elements of one vector of R values, the pairs i0 .. i0 + 7.
+struct Sixteen {
+    uint4 lo, hi;
+};
+template <bool PAIRS>
+__device__ __forceinline__ int lo_of(int i0) { return PAIRS ? 2 * i0 : i0; }
+template <bool PAIRS>
+__device__ __forceinline__ int hi_of(int i0, int R) { return PAIRS ? 2 * i0 + 8 : R / 2 + i0; }
+template <bool PAIRS>
+__device__ __forceinline__ Sixteen load16(const uint16_t *x, int R, int i0) {
+    return {*reinterpret_cast<const uint4 *>(x + lo_of<PAIRS>(i0)),
+            *reinterpret_cast<const uint4 *>(x + hi_of<PAIRS>(i0, R))};
+}
 template <typename T, bool PAIRS>
-__device__ __forceinline__ void rotate16(const uint16_t *__restrict__ x, uint16_t *__restrict__ y,
-                                         const float *__restrict__ angles, int R, int i0) {
-    const int lo = PAIRS ? 2 * i0 : i0, hi = PAIRS ? 2 * i0 + 8 : R / 2 + i0;
-    const uint4 v0 = *reinterpret_cast<const uint4 *>(x + lo);
-    const uint4 v1 = *reinterpret_cast<const uint4 *>(x + hi);
+__device__ __forceinline__ void rotate16(const Sixteen &x, uint16_t *y, const float *__restrict__ angles,
+                                         int R, int i0) {
     float c[8], s[8], a[8], b[8];
 #pragma unroll
     for (int u = 0; u < 8; u += 4) {
         *reinterpret_cast<float4 *>(c + u) = *reinterpret_cast<const float4 *>(angles + i0 + u);
         *reinterpret_cast<float4 *>(s + u) = *reinterpret_cast<const float4 *>(angles + R / 2 + i0 + u);
     }
-    half8_to_float<T>(v0, a);
-    half8_to_float<T>(v1, b);
+    half8_to_float<T>(x.lo, a);
+    half8_to_float<T>(x.hi, b);
     float o0[8], o1[8];
     if (PAIRS) {
 #pragma unroll
@@ -82,26 +99,40 @@ __device__ __forceinline__ void rotate16(const uint16_t *__restrict__ x, uint16_
             o1[u] = a[u] * s[u] + b[u] * c[u];
         }
     }
-    *reinterpret_cast<uint4 *>(y + lo) = float_to_half8<T>(o0);
-    *reinterpret_cast<uint4 *>(y + hi) = float_to_half8<T>(o1);
+    *reinterpret_cast<uint4 *>(y + lo_of<PAIRS>(i0)) = float_to_half8<T>(o0);
+    *reinterpret_cast<uint4 *>(y + hi_of<PAIRS>(i0, R)) = float_to_half8<T>(o1);
 }
 
 template <typename T, bool PAIRS>
 __global__ void __launch_bounds__(THREADS)
 k_append(const LatentAppendArgs a, const unsigned q_blocks) {
-    const int units = a.R / 16;  // units of 16 elements in one vector of R
+    const uint32_t units = a.R / 16;  // units of 16 elements in one vector of R
     if (blockIdx.x < q_blocks) {
+        // (at most 2^20 tokens x 1024 heads x 4 units: the last index is 2^32 - 1)
         const uint32_t per_tok = static_cast<uint32_t>(a.Hq) * units;
-        const int64_t i = static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x;
-        const int64_t t = i / per_tok;
-        if (t >= a.T) return;
-        const uint32_t r = static_cast<uint32_t>(i - t * per_tok);
-        const int h = r / units, u = r - h * units;
-        const int row = a.tok_row[t], pos = a.positions[t];
-        if (row < 0 || row >= a.B || pos < 0 || pos >= a.pos_end) return;
-        rotate16<T, PAIRS>(a.q_rot + t * a.q_rot_tok + h * a.q_rot_head,
-                           a.q_out + t * a.q_out_tok + h * a.q_out_head,
-                           a.cos_sin + static_cast<int64_t>(pos) * a.R, a.R, 8 * u);
+        const uint32_t first = blockIdx.x * (THREADS * UNITS) + threadIdx.x;
+        // the values are loaded before the token's position is known: the two chains overlap
+        Sixteen x[UNITS];
+        int pos[UNITS];
+        uint16_t *y[UNITS];
+        uint32_t i0[UNITS];
+#pragma unroll
+        for (int k = 0; k < UNITS; ++k) {
+            const uint32_t i = first + k * THREADS, t = i / per_tok;
+            pos[k] = -1;
+            if (t >= a.T) continue;
+            const uint32_t r = i - t * per_tok, h = r / units;
+            i0[k] = 8 * (r - h * units);
+            x[k] = load16<PAIRS>(a.q_rot + t * a.q_rot_tok + h * a.q_rot_head, a.R, i0[k]);
+            y[k] = a.q_out + t * a.q_out_tok + h * a.q_out_head;
+            const int row = a.tok_row[t];
+            pos[k] = a.positions[t];
+            if (row < 0 || row >= a.B || pos[k] >= a.pos_end) pos[k] = -1;
+        }
+#pragma unroll
+        for (int k = 0; k < UNITS; ++k)
+            if (pos[k] >= 0)
+                rotate16<T, PAIRS>(x[k], y[k], a.cos_sin + static_cast<int64_t>(pos[k]) * a.R, a.R, i0[k]);
         return;
     }
     const int lane = threadIdx.x & 31;
@@ -114,12 +145,14 @@ k_append(const LatentAppendArgs a, const unsigned q_blocks) {
 #pragma unroll
     for (int k = 0; k < 2; ++k)
         if (lane + 32 * k < vecs) v[k] = ld_stream_16B(x + 8 * (lane + 32 * k));
+    Sixteen rot;
+    if (lane < units) rot = load16<PAIRS>(a.rot + t * a.rot_stride, a.R, 8 * lane);
     const Slot s = find_slot(a, t);
     if (s.bad && lane == 0 && a.status) atomicOr(a.status, MTPSPEC_STATUS_BAD_PARAM);
     if (s.page < 0) return;
     uint16_t *dst = a.cache + s.page * a.page_stride + static_cast<int64_t>(s.off) * (a.L + a.R);
     if (lane < units)
-        rotate16<T, PAIRS>(a.rot + t * a.rot_stride, dst + a.L,
+        rotate16<T, PAIRS>(rot, dst + a.L,
                            a.cos_sin + static_cast<int64_t>(s.pos) * a.R, a.R, 8 * lane);
     if (a.norm_w) {
         float sum = 0.0f;
@@ -153,7 +186,8 @@ k_append(const LatentAppendArgs a, const unsigned q_blocks) {
 template <typename T, bool PAIRS>
 cudaError_t launch(const LatentAppendArgs &a, cudaStream_t stream) {
     const int64_t q_units = a.q_rot ? a.T * a.Hq * (a.R / 16) : 0;
-    const unsigned q_blocks = static_cast<unsigned>((q_units + THREADS - 1) / THREADS);
+    const int64_t a_block = int64_t{THREADS} * UNITS;
+    const unsigned q_blocks = static_cast<unsigned>((q_units + a_block - 1) / a_block);
     const unsigned t_blocks = static_cast<unsigned>((a.T + WARPS - 1) / WARPS);
     k_append<T, PAIRS><<<q_blocks + t_blocks, THREADS, 0, stream>>>(a, q_blocks);
     const cudaError_t e = cudaGetLastError();
