@@ -271,6 +271,9 @@ k_latent_attn(const __grid_constant__ Maps maps, const Params p) {
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    // (tensor memory is taken only once the kernel before has ended: holding it would stop that
+    // kernel's blocks, if they were still to take theirs)
+    pdl_wait_primary();
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_addr(&sh.tmem)),
@@ -278,7 +281,6 @@ k_latent_attn(const __grid_constant__ Maps maps, const Params p) {
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    pdl_wait_primary();
     // ---- where this CTA starts.  Every warp finds it by itself, from a scan of the rows'
     // tiles with a run of rows a lane: no role waits for another's.
     const int per_lane = (p.B + 31) / 32;
