@@ -1,13 +1,31 @@
 // Attention over whole prompts in the expanded form: every head has its own N key values and
 // V values a token, and the heads share the R rotated key values of a token.
 //
-// One pass over the keys with the running maximum and sum of a softmax.  A CTA takes 256
-// queries of one head as two tiles of 128 rows: while the tensor cores work on one tile's
-// products, the other tile's softmax runs, eight warps a tile.  Tensor
-// memory holds both tiles' scores (128 columns each, whose first half becomes the weights,
-// the left operand of the second product) and outputs.  Keys and values stream through a
-// ring of 16 KB chunks (128 tokens x 64 columns) in the order in which they are used.  The
-// shared rotated part is read from its own array, so no key is ever put together in memory.
+// One pass over the keys with the running maximum m and sum l of a softmax: for a tile of keys
+//     S = Q K^T,  p = 2^(s - m),  l += sum p,  O += p V,  and O, l scaled by 2^(m - m') when m
+// changes (s, m in powers of two, scale * log2 e folded in; m follows a row's maximum only when
+// that has grown by more than 2^8).  Weights are rounded to 16 bits for the second product; l
+// sums the unrounded ones in fp32.  Keys that no query of a tile sees are never read.
+//
+// A pair of query tiles, 256 queries of one head, is a CTA's unit of work: while the tensor
+// cores work on one tile's products, the other tile's softmax runs, eight warps a tile, two
+// threads a row.  Tensor memory holds both tiles' scores (128 columns each, whose first half
+// becomes the weights, the left operand of the second product) and outputs: all of its 512
+// columns.  Keys and values stream through a ring of 16 KB chunks (128 tokens x 64 columns) in
+// the order in which they are used.  The shared rotated part is read from its own array, so no
+// key is ever put together in memory.  The grid has a CTA a pair, and one that has nothing left
+// to load takes over a pair whose CTA has not started.
+//
+// What bounds it (bf16, N = V = 128, R = 64; products 1938 TFLOP/s measured): 8192 tokens x 32
+// heads, 687 GFLOP: 442 us, 1.55 PFLOP/s, 0.80; counters: tensor pipe 65 %, shared memory of the
+// products 52 %, exponentials 27 %, DRAM 18 %.  A round of both tiles takes some 3,500 cycles
+// for 2,560 of products: the chain scores - softmax - products of a tile is longer than the
+// other tile's products, and a third tile has no tensor memory.  Splitting the chain (first
+// half of the weights handed over early) cost more in barriers than it gave: 439 -> 476 us.
+// 8 prompts of 77-1500 tokens x 32 heads, 61 GFLOP: 85 us, 0.71 PFLOP/s: the last softmax and
+// the output of a pair are not covered by anything (tensor pipe 36 %).  Two chunks of 900 and
+// 1000 queries x 16 heads behind 7001 keys: 130 us, 1.14 PFLOP/s: 128 pairs, 24 of the 152
+// multiprocessors have none.  300 tokens x 16 heads: 12.3 us, the way from launch to output.
 #include <algorithm>
 
 #include "half_types.cuh"
