@@ -87,7 +87,7 @@ int mtp_latent_append(const void *latent, int64_t latent_stride, const void *rot
  *   out   [B, T, Hq, L] with row, token and head strides      lse float [B, T, Hq] or NULL
  *   cache, block_table, page_size, page_stride, num_pages, max_pages as above; entries of
  *         the table that no visible position needs are not read
- *   kv_len int32 [B] in [0, max_pages * page_size]
+ *   kv_len int32 [B] in [0, min(max_pages * page_size, 2^31 - 256)]
  *   workspace  >= mtp_latent_attn_workspace_bytes(B, T, Hq, L, R) bytes, 256-byte aligned
  *   status int32 [1] or NULL: MTPSPEC_STATUS_BAD_PARAM is OR-ed in for a length out of range
  *         (taken as the nearest in range) or a page id out of range (its positions are read

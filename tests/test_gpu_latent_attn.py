@@ -229,3 +229,28 @@ def test_short_workspace_is_refused():
         lib.mtp_latent_attn(x["q"], x["cache"], x["table"], x["kv_len"], out, 0.1, workspace=ws[:-1])
     with pytest.raises(lib.MtpSpecError):
         lib.mtp_latent_attn(x["q"], x["cache"], x["table"], x["kv_len"], out, 0.1)
+
+
+@pytest.mark.parametrize("length", [2 ** 31 - 256, 2 ** 31 - 1])
+def test_the_longest_text(length):
+    # one page, repeated: position n has the scores of n % 4096; a longer length is reported
+    # and taken as the longest
+    P, L, R = 4096, 64, 16
+    longest = 2 ** 31 - 256
+    x = make([P], 1, 2, L, R, P, BF, seed=12)
+    page = int(x["table"][0, 0])
+    x["table"] = torch.full((1, 2 ** 31 // P), page, dtype=torch.int32, device=DEV)
+    x["kv_len"] = torch.tensor([length], dtype=torch.int32, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out, lse = run(x, status=status)
+    assert int(status) == (0 if length == longest else lib.STATUS_BAD_PARAM)
+    keys = x["cache"][page].double()
+    times = torch.full((P,), longest // P, device=DEV).double()
+    times[:longest % P] += 1
+    s = x["q"][0, 0].double() @ keys.T * x["scale"] + times.log()
+    want, A = s.softmax(1) @ keys[:, :L], s.softmax(1) @ keys[:, :L].abs()
+    # four additions a tile of a CTA's share, none off by more than 2^-22 of the sum so far
+    steps = 4 * (longest // 64 // 152 + 1) + 16 + 152
+    tol = (steps + 2 * 80) * 2.0 ** -22 + 2.0 ** -8
+    assert ((out[0, 0].double() - want).abs() <= tol * A + 2.0 ** -8 * want.abs()).all()
+    assert ((lse[0, 0].double() - s.logsumexp(1)).abs() <= tol).all()

@@ -24,7 +24,7 @@
 //   64 rows a sequence (256 x 500-4000 keys, 725 MB): 148 us, 4.9 TB/s, 0.73 of the copy rate.
 //     Counters: DRAM 65 %, tensor pipe 24 %, shared memory of the products 39 %.  The rest is
 //     the ends of units, 6,000 cycles each for outputs of 64 rows x 512, and start and join.
-//   256 rows a sequence (64 x 1000-8000 keys, 170 GFLOP): 217 us, 0.78 PFLOP/s, 0.41.  A tile
+//   256 rows a sequence (64 x 1000-8000 keys, 170 GFLOP): 220 us, 0.77 PFLOP/s, 0.40.  A tile
 //     takes 2,700-2,950 cycles, 1,792 of them products at the rate of 64-row accumulators,
 //     which is set by shared memory (every 16-column step reads 2 KB of queries or weights
 //     beside the keys); the keys' arrival and the softmax between the two products take the
@@ -63,6 +63,7 @@ struct Params {
     int64_t q_row, q_tok, q_head;
     const int32_t *block_table, *kv_len;
     int64_t max_pages;
+    int max_len;         // the table's positions, as far as tiles beyond them have 32-bit numbers
     int num_pages, page_size, box_rows;
     int B, T, Hq, L, R;
     int mtiles;          // row tiles of a sequence
@@ -83,9 +84,7 @@ struct Params {
 };
 
 __device__ __forceinline__ int row_len(const Params &p, int b) {
-    const int64_t cap = p.max_pages * p.page_size;
-    const int n = p.kv_len[b];
-    return n < 0 ? 0 : static_cast<int>(n < cap ? n : cap);
+    return min(max(p.kv_len[b], 0), p.max_len);
 }
 __device__ __forceinline__ int tiles_of(int len) { return (len + TN - 1) / TN; }
 
@@ -338,7 +337,7 @@ k_latent_attn(const __grid_constant__ Maps maps, const Params p) {
     w.lane = cta - group * p.gs;
     {
         const bool mine = t0 < t1 && at <= t0 && t0 < at + sum;
-        int b = r0, n = 0, in = 0;
+        int b = r0, n = 0;
         if (mine) {
             bool found = false;
 #pragma unroll
@@ -362,18 +361,15 @@ k_latent_attn(const __grid_constant__ Maps maps, const Params p) {
                 }
             }
         }
-        in = static_cast<int>(t0 - at);  // fewer than 2^31 tiles a row
+        const int64_t in = t0 - at;  // the row's tiles before it, over all its units
         const unsigned who = __ballot_sync(0xFFFFFFFFu, mine);
         const int src = who ? __ffs(who) - 1 : 0;
         w.b = __shfl_sync(0xFFFFFFFFu, b, src);
         w.len = __shfl_sync(0xFFFFFFFFu, n, src);
-        w.off = __shfl_sync(0xFFFFFFFFu, in, src);
+        const int64_t off = __shfl_sync(0xFFFFFFFFu, in, src);
         w.nt = tiles_of(w.len);
-        w.mg = 0;
-        if (p.mgroups > 1 && w.nt > 0) {
-            w.mg = w.off / w.nt;
-            w.off -= w.mg * w.nt;
-        }
+        w.mg = p.mgroups > 1 && w.nt > 0 ? static_cast<int>(off / w.nt) : 0;
+        w.off = static_cast<int>(off - static_cast<int64_t>(w.mg) * w.nt);
     }
     tc_fence_before();
     __syncthreads();
@@ -601,7 +597,7 @@ k_latent_attn(const __grid_constant__ Maps maps, const Params p) {
         // ---- rows without keys, and lengths out of range, while the first keys are on their way
         for (int b = cta; b < p.B; b += GRID) {
             const int n = p.kv_len[b];
-            if (tid == 0 && p.status && (n < 0 || n > p.max_pages * p.page_size))
+            if (tid == 0 && p.status && (n < 0 || n > p.max_len))
                 atomicOr(p.status, MTPSPEC_STATUS_BAD_PARAM);
             if (row_len(p, b) > 0) continue;
             const int row_vecs = Z::L / 8;
@@ -1002,6 +998,7 @@ cudaError_t run_latent_attn(const LatentAttnArgs &a, int dtype, cudaStream_t str
     p.block_table = a.block_table;
     p.kv_len = a.kv_len;
     p.max_pages = a.max_pages;
+    p.max_len = static_cast<int>(std::min<int64_t>(a.max_pages * a.page_size, (int64_t{1} << 31) - 256));
     p.num_pages = static_cast<int>(a.num_pages);
     p.page_size = a.page_size;
     p.box_rows = box;
