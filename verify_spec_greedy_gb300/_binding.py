@@ -384,23 +384,31 @@ def _half_codes():
 def _view(t, name, shape, like=None):
     """(pointer, strides in elements) of a 16-bit tensor of `shape` on the GPU whose last axis
     is contiguous; `like` gives the type it has to have.  An axis of one has stride 0."""
-    if t is None:
-        raise ValueError(f"{name} is required")
-    if not isinstance(t, _kinds()["tensor"]):
-        raise TypeError(f"{name} must be a torch tensor")
-    codes = _HALF_CODES or _half_codes()
-    if (t.dtype is not like) if like is not None else (t.dtype not in codes):
-        raise TypeError(f"{name} must hold {like or 'bfloat16 or float16'} values, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must live on a CUDA device")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    try:  # what is as it should be takes few questions: a call's host time is some 10 us
+        good = (t.is_cuda and t.shape == shape and
+                (t.dtype is like if like is not None else t.dtype in (_HALF_CODES or _half_codes())))
+    except AttributeError:
+        good = False
+    if not good:
+        _refuse_view(t, name, shape, like)
     st = t.stride()
     if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}'s last axis must be contiguous")
     if 1 in shape:
         st = [0 if n == 1 else s for n, s in zip(shape, st)]
     return t.data_ptr(), st
+
+
+def _refuse_view(t, name, shape, like):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not isinstance(t, _kinds()["tensor"]):
+        raise TypeError(f"{name} must be a torch tensor")
+    if (t.dtype is not like) if like is not None else (t.dtype not in (_HALF_CODES or _half_codes())):
+        raise TypeError(f"{name} must hold {like or 'bfloat16 or float16'} values, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _vec(t, name, dtype, kind, numel=0):
@@ -450,7 +458,7 @@ def mtp_latent_append(latent, rot, cos_sin, tok_row, positions, block_table, cac
     if norm_w is not None and norm_w.dtype != dt:
         raise TypeError(f"norm_w must hold {dt} values, got {norm_w.dtype}")
     _call("mtp_latent_append", lp, ls[0], rp, rs[0],
-          _arg(norm_w, "norm_w", _HALF, L, optional=True), float(eps),
+          None if norm_w is None else _vec(norm_w, "norm_w", dt, _HALF, L), float(eps),
           _vec(cos_sin, "cos_sin", _FLOAT, _F32), cos_sin.shape[0], 1 if interleaved else 0,
           _vec(tok_row, "tok_row", _INT, _I32, T), _vec(positions, "positions", _INT, _I32, T), T, L,
           R, _vec(block_table, "block_table", _INT, _I32), B, max_pages, cp, pages, P, page_stride,
