@@ -254,3 +254,11 @@ def test_the_longest_text(length):
     tol = (steps + 2 * 80) * 2.0 ** -22 + 2.0 ** -8
     assert ((out[0, 0].double() - want).abs() <= tol * A + 2.0 ** -8 * want.abs()).all()
     assert ((lse[0, 0].double() - s.logsumexp(1)).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("page", [8, 16, 24, 32, 40, 64, 192])
+@pytest.mark.parametrize("L,R", [(512, 64), (448, 16), (320, 32), (256, 48), (192, 64)])
+def test_pages_of_every_height(L, R, page):
+    x = make([page, 333, 129, 1], 2, 5, L, R, page, BF, seed=page, spare=1)
+    out, lse = run(x)
+    verify(x, out, lse)

@@ -24,12 +24,12 @@
 //   64 rows a sequence (256 x 500-4000 keys, 725 MB): 148 us, 4.9 TB/s, 0.73 of the copy rate.
 //     Counters: DRAM 65 %, tensor pipe 24 %, shared memory of the products 39 %.  The rest is
 //     the ends of units, 6,000 cycles each for outputs of 64 rows x 512, and start and join.
-//   256 rows a sequence (64 x 1000-8000 keys, 170 GFLOP): 220 us, 0.77 PFLOP/s, 0.40.  A tile
-//     takes 2,700-2,950 cycles, 1,792 of them products at the rate of 64-row accumulators,
+//   256 rows a sequence (64 x 1000-8000 keys, 170 GFLOP): 213 us, 0.80 PFLOP/s, 0.41.  A tile
+//     takes some 2,750 cycles, 1,792 of them products at the rate of 64-row accumulators,
 //     which is set by shared memory (every 16-column step reads 2 KB of queries or weights
 //     beside the keys); the keys' arrival and the softmax between the two products take the
 //     rest, since a third tile does not fit.
-//   168 rows, 100k keys, one sequence: 66 us; as the last, and each row has 50 parts to join.
+//   168 rows, 100k keys, one sequence: 63 us; as the last, and each row has 50 parts to join.
 //   One row of 600 keys: 11.6 us; 8 x 2k keys, 64 rows: 18 us: two launches and one tile's way
 //     from page table to output.
 #include <algorithm>
@@ -195,13 +195,13 @@ __device__ __forceinline__ void mma_ws(uint32_t d, uint64_t a, uint64_t b, uint3
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// The descriptor of a tile whose 64-column chunks lie CHUNK bytes apart and whose rows are
-// the products' K axis (the "MN-major" form): 8-row groups every 1024 bytes.
-__device__ __forceinline__ uint64_t smem_desc_rows_k(uint32_t addr) {
+// The descriptor of a tile whose rows are the products' K axis (the "MN-major" form): its
+// 64-column chunks and its groups of 8 rows lie this many bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_rows_k(uint32_t addr, uint32_t chunk_step, uint32_t group_step) {
     uint64_t d = 0;
     d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(CHUNK >> 4) << 16;
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(chunk_step >> 4) << 16;
+    d |= static_cast<uint64_t>(group_step >> 4) << 32;
     d |= static_cast<uint64_t>(1) << 46;
     d |= static_cast<uint64_t>(2) << 61;
     return d;
@@ -225,6 +225,11 @@ struct Sizes {
     static __host__ __device__ constexpr int width(int k) {  // its chunks
         return k < (NL >> 2) ? 4 : (k == (NL >> 2) && ((NL >> 1) & 1) ? 2 : 1);
     }
+    // Pieces of four chunks lie group by group of 8 rows, the chunks of a group side by side,
+    // so that a box of any number of groups is one copy; narrower ones chunk by chunk.
+    static __host__ __device__ constexpr int chunk_step(int k) { return width(k) == 4 ? 1024 : CHUNK; }
+    static __host__ __device__ constexpr int group_step(int k) { return width(k) == 4 ? 4096 : 1024; }
+    static constexpr int COPIES = (NL >> 2) + (NL & 3) + 1;  // of a box of rows, the rotated one too
     static constexpr int UNIT = width(0);
     static constexpr int ROT_SLOTS = NL < 7 ? 4 : 2;
     static constexpr int LEFT = SMEM_MAX - SMEM_EXTRA - (CHUNKS + 1 + ROT_SLOTS) * CHUNK;
@@ -235,29 +240,28 @@ struct Sizes {
     static_assert(SLOTS > PIECES, "a tile and the start of the next");
 };
 
-// The cache's maps.  `wide` and `one` see a row's latents as L / 64 chunks of 64 values, so
-// that one copy brings four chunks (or one) of a box's rows, chunk by chunk, as the products
-// want them; `rot` brings the 64 columns from L on, zeros beyond the row's end.
+// The cache's maps.  `wide` sees a page as groups of 8 rows and a row's latents as chunks of 64
+// values, and brings four chunks of a box's groups; `one` brings a chunk of a box's rows; `rot`
+// the 64 columns from L on, zeros beyond the row's end.
 struct Maps {
     CUtensorMap wide, one, rot;
 };
 template <typename Z>
 __device__ __forceinline__ void piece_load(const Maps &m, int k, uint32_t dst, int box, int box_rows,
                                            int row, int page, uint64_t *bar) {
-    if (Z::width(k) == 4 && box_rows == TN) {
-        tma_load_4d(dst, &m.wide, 0, row, Z::first(k), page, bar);
+    if (Z::width(k) == 4) {
+        tma_load_5d(dst + box * box_rows * 512, &m.wide, 0, 0, Z::first(k), row >> 3, page, bar);
     } else {
-        // (a box of fewer rows than a tile would put its chunks too close together)
 #pragma unroll
         for (int c = 0; c < Z::width(k); ++c)
             tma_load_4d(dst + c * CHUNK + box * box_rows * 128, &m.one, 0, row, Z::first(k) + c, page, bar);
     }
 }
-// The same to L2, for boxes as high as a tile.
+// The same to L2.
 template <typename Z>
 __device__ __forceinline__ void piece_prefetch(const Maps &m, int k, int row, int page) {
     if (Z::width(k) == 4) {
-        tma_prefetch_4d(&m.wide, 0, row, Z::first(k), page);
+        tma_prefetch_5d(&m.wide, 0, 0, Z::first(k), row >> 3, page);
     } else {
 #pragma unroll
         for (int c = 0; c < Z::width(k); ++c) tma_prefetch_4d(&m.one, 0, row, Z::first(k) + c, page);
@@ -448,9 +452,11 @@ k_latent_attn(const __grid_constant__ Maps maps, const Params p) {
                     // The next tile goes to L2 as soon as this one's pieces are under way: what
                     // its slots wait for is then the way from L2, which leaves them sooner to
                     // the tile after.  (64 rows x 8k keys x 256 query rows 241 -> 217 us; two
-                    // or four tiles ahead 221; in boxes smaller than a tile, four times the
-                    // copies, it costs more than it gives: 150 -> 161 us.)
-                    if (p.box_rows == TN && f < w.i1) settle(true);
+                    // or four tiles ahead 221.)  Pages shorter than a tile multiply the copies:
+                    // with 12 a tile it still pays (L = 512, pages of 16, 64 query rows 156 ->
+                    // 152 us), with 16 and more it costs (L = 192, pages of 16: 111 -> 115;
+                    // L = 512, pages of 8: 156 -> 163).
+                    if (boxes * Z::COPIES <= 12 && f < w.i1) settle(true);
                     if (sh.abort || !wait(sh, &sh.rot_empty[rs], rph)) break;
                     mbar_expect_tx(&sh.rot_full[rs], CHUNK);
                     ++rot_filled;
@@ -484,7 +490,6 @@ k_latent_attn(const __grid_constant__ Maps maps, const Params p) {
             constexpr uint32_t id_qk = idesc_of<T>(TN, false);
             const uint64_t qd = smem_desc_sw128(q_s), pd = smem_desc_sw128(p_s);
             const uint64_t kd = smem_desc_sw128(kv_s), rd = smem_desc_sw128(rot_s);
-            const uint64_t vd = smem_desc_rows_k(kv_s);
             int item = 0;
             int sa = 0, sb = 0, ra = 0;            // the next slots of tiles a and b
             uint32_t pa = 0, pra = 0, par = 0;     // their phases; parity of tile a's number
@@ -501,10 +506,12 @@ k_latent_attn(const __grid_constant__ Maps maps, const Params p) {
 #pragma unroll
                 for (int k = 0; k < Z::PIECES; ++k) {
                     const uint32_t id = idesc_of<T>(Z::width(k) * 64, true);
-                    const uint64_t v = vd + sb * (Z::SLOT_BYTES >> 4);
+                    const uint64_t v = smem_desc_rows_k(kv_s, Z::chunk_step(k), Z::group_step(k)) +
+                                       sb * (Z::SLOT_BYTES >> 4);
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
-                        mma_ws(tmem + Z::first(k) * 32, pd + 2 * u, v + u * (2048 >> 4), id, !first || u > 0);
+                        mma_ws(tmem + Z::first(k) * 32, pd + 2 * u, v + u * (2 * Z::group_step(k) >> 4), id,
+                               !first || u > 0);
                     mma_commit(&sh.empty[sb]);
                     if (++sb == Z::SLOTS) sb = 0;
                 }
@@ -539,9 +546,11 @@ k_latent_attn(const __grid_constant__ Maps maps, const Params p) {
 #pragma unroll
                     for (int k = 0; k < Z::PIECES; ++k) {
                         if (!filled(&sh.full[sa], pa)) break;
-                        const uint64_t key = kd + sa * (Z::SLOT_BYTES >> 4);
+                        // (kd's groups of rows are 1024 bytes apart)
+                        const uint64_t key = kd + (static_cast<uint64_t>((Z::group_step(k) - 1024) >> 4) << 32) +
+                                             sa * (Z::SLOT_BYTES >> 4);
 #pragma unroll
-                        for (int i = 0; i < Z::width(k); ++i) scores(Z::first(k) + i, key + i * (CHUNK >> 4));
+                        for (int i = 0; i < Z::width(k); ++i) scores(Z::first(k) + i, key + i * (Z::chunk_step(k) >> 4));
                         if (++sa == Z::SLOTS) {
                             sa = 0;
                             pa ^= 1;
@@ -694,13 +703,15 @@ k_latent_attn(const __grid_constant__ Maps maps, const Params p) {
                     // must not meet the zero weights
                     const int z0 = w.len - tile * TN, vec = (TN - z0) * 8;
                     int at = piece_slot;
-#pragma unroll 1
+#pragma unroll
                     for (int k = 0; k < Z::PIECES; ++k) {
-                        const uint32_t v = kv_s + at * Z::SLOT_BYTES + z0 * 128;
+                        const uint32_t v = kv_s + at * Z::SLOT_BYTES;
+#pragma unroll 1
                         for (int i = tid; i < vec * Z::width(k); i += 128) {
-                            const int c = i / vec;
+                            const int c = i / vec, in = i - c * vec, z = z0 + (in >> 3);
                             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                             v + c * CHUNK + (i - c * vec) * 16),
+                                             v + c * Z::chunk_step(k) + (z >> 3) * Z::group_step(k) +
+                                             (z & 7) * 128 + (in & 7) * 16),
                                          "r"(0)
                                          : "memory");
                         }
@@ -971,23 +982,23 @@ cudaError_t run_latent_attn(const LatentAttnArgs &a, int dtype, cudaStream_t str
     const cuuint32_t rows = static_cast<cuuint32_t>(box);
     const auto encode = [&](CUtensorMap *m, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
                             const cuuint32_t *boxes) {
-        const cuuint32_t es[4] = {1, 1, 1, 1};
+        const cuuint32_t es[5] = {1, 1, 1, 1, 1};
         return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<uint16_t *>(a.cache), dims, strides,
                   boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
     const cuuint64_t chunks = static_cast<cuuint64_t>(a.L / 64);
+    const cuuint64_t wdims[5] = {64, 8, chunks, P / 8, pages}, wstrides[4] = {W * 2, 128, W * 16, page_bytes};
     const cuuint64_t cdims[4] = {64, P, chunks, pages}, cstrides[3] = {W * 2, 128, page_bytes};
-    const cuuint32_t wide[4] = {64, rows, static_cast<cuuint32_t>(std::min<cuuint64_t>(4, chunks)), 1};
-    const cuuint32_t one[4] = {64, rows, 1, 1}, rot[3] = {64, rows, 1};
     const cuuint64_t rdims[3] = {W, P, pages}, rstrides[2] = {W * 2, page_bytes};
+    const cuuint32_t wide[5] = {64, 8, 4, rows / 8, 1}, one[4] = {64, rows, 1, 1}, rot[3] = {64, rows, 1};
     // (a call encodes the ones that it needs: each costs the host a microsecond)
-    const bool whole = box == lat::TN && a.L >= 256, single = !whole || a.L % 256 != 0;
-    if ((whole && !encode(&maps.wide, 4, cdims, cstrides, wide)) ||
-        (single && !encode(&maps.one, 4, cdims, cstrides, one)) || !encode(&maps.rot, 3, rdims, rstrides, rot))
+    const bool quads = a.L >= 256, singles = a.L % 256 != 0;
+    if ((quads && !encode(&maps.wide, 5, wdims, wstrides, wide)) ||
+        (singles && !encode(&maps.one, 4, cdims, cstrides, one)) || !encode(&maps.rot, 3, rdims, rstrides, rot))
         return cudaErrorInvalidValue;
-    if (!whole) maps.wide = maps.one;
-    if (!single) maps.one = maps.wide;
+    if (!quads) maps.wide = maps.one;
+    if (!singles) maps.one = maps.wide;
     const lat::Layout y = lat::layout(static_cast<int64_t>(a.T) * a.Hq, a.L);
     unsigned char *ws = static_cast<unsigned char *>(a.workspace);
     lat::Params p = {};
