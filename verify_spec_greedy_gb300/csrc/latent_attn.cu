@@ -22,7 +22,7 @@
 //
 // What bounds it (bf16, L = 512, R = 64; HBM copy 6.7 TB/s, products 1938 TFLOP/s measured):
 //   64 rows a sequence (256 x 500-4000 keys, 725 MB): 148 us, 4.9 TB/s, 0.73 of the copy rate.
-//     Counters: DRAM 65 %, tensor pipe 24 %, shared memory of the products 39 %.  The rest is
+//     Counters: DRAM 67 %, tensor pipe 24 %, shared memory of the products 40 %.  The rest is
 //     the ends of units, 6,000 cycles each for outputs of 64 rows x 512, and start and join.
 //   256 rows a sequence (64 x 1000-8000 keys, 170 GFLOP): 213 us, 0.80 PFLOP/s, 0.41.  A tile
 //     takes some 2,750 cycles, 1,792 of them products at the rate of 64-row accumulators,
