@@ -513,19 +513,28 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             // spent some 11,000 cycles on its start and its end; so 8 x 800 tokens x 32 heads
             // took 126 us, not 93, and 8192 x 32 heads 472, not 442.)
             Item it = sh.item[0];
-            for (uint32_t item = 0;; ++item) {
-                if (!wait_far(sh, &sh.near_end, item & 1)) break;
+            // Request number n: the CTA given, or -1; false if the answer did not come.  The warp
+            // decides together, since what follows has full-warp operations; and all lanes have
+            // read an answer before the next request lets another be written over it.
+            const auto ask = [&](uint32_t n, int &cta) {
                 if (lane == 0) {
                     mbar_expect_tx(&sh.answer, sizeof(uint4));
                     ask_for_work(&sh.taken, &sh.answer);
                 }
                 __syncwarp();
-                if (!wait_long(sh, &sh.answer, item & 1)) {
-                    wait_out(&sh.answer, item & 1);
-                    break;
+                if (!__all_sync(0xFFFFFFFFu, wait_long(sh, &sh.answer, n & 1))) {
+                    wait_out(&sh.answer, n & 1);
+                    return false;
                 }
-                const int cta = work_given(&sh.taken);
-                fence_async_smem();  // read before the next answer overwrites it
+                cta = work_given(&sh.taken);
+                fence_async_smem();
+                __syncwarp();
+                return true;
+            };
+            for (uint32_t item = 0;; ++item) {
+                if (!__all_sync(0xFFFFFFFFu, wait_far(sh, &sh.near_end, item & 1))) break;
+                int cta;
+                if (!ask(item, cta)) break;
                 const Extent was(it.w);
                 it.g0 += was.n;
                 it.slot0 = (it.slot0 + (was.n % Z::SLOTS) * Z::TILE) % Z::SLOTS;
@@ -537,7 +546,9 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 it.w.pair = -1;
                 if (cta >= 0) it.w = work_of(cta);
                 // the item before this slot's last is left behind by all
-                if (item > 0 && !wait_long(sh, &sh.item_free[(item - 1) & 1], ((item - 1) >> 1) & 1)) break;
+                if (item > 0 && !__all_sync(0xFFFFFFFFu, wait_long(sh, &sh.item_free[(item - 1) & 1],
+                                                                   ((item - 1) >> 1) & 1)))
+                    break;
                 if (lane == 0) {
                     sh.item[(item + 1) & 1] = it;
                     mbar_arrive(&sh.item_full[(item + 1) & 1]);
@@ -545,15 +556,7 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 const Work w = it.w;
                 if (w.pair < 0) {
                     // whatever has not started by now has no work either
-                    for (uint32_t more = item + 1; cta >= 0; ++more) {
-                        if (lane == 0) {
-                            mbar_expect_tx(&sh.answer, sizeof(uint4));
-                            ask_for_work(&sh.taken, &sh.answer);
-                        }
-                        __syncwarp();
-                        if (!wait_long(sh, &sh.answer, more & 1)) wait_out(&sh.answer, more & 1);
-                        if (sh.abort || work_given(&sh.taken) < 0) break;
-                        fence_async_smem();
+                    for (uint32_t more = item + 1; cta >= 0 && ask(more, cta); ++more) {
                     }
                     break;
                 }
