@@ -1,6 +1,7 @@
 """mtp_latent_prefill's work: a multiprocessor takes over pairs of query tiles whose CTAs have not
 started.  The grid has a CTA for every pair that the lengths might give, so ragged calls leave
-thousands of CTAs without work among those that have some.  Calls repeat bit for bit."""
+thousands of CTAs without work among those that have some.  Every pair is done, and calls repeat
+bit for bit."""
 import pytest
 import torch
 
@@ -27,3 +28,16 @@ def test_thousands_of_ctas_without_work(B, heads, long):
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
     assert int(status.item()) == 0
     verify(x, want, want_lse, heads=[0, heads // 2, heads - 1])
+
+
+@pytest.mark.parametrize("B,heads", [(4, 64), (90, 12)])
+def test_long_sequences_behind_empty_ones(B, heads):
+    # more pairs than multiprocessors, and more CTAs without work than pairs
+    nq = [0] * B
+    nq[B // 3], nq[-1] = 700, 1100
+    x = make(nq, nq, heads, 128, 64, 128, F16, seed=B)
+    want, want_lse = run(x)
+    verify(x, want, want_lse, heads=[0, heads - 1])
+    for _ in range(10):
+        out, lse = run(x)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)

@@ -106,7 +106,8 @@ __device__ __forceinline__ bool wait_long(Shared &sh, uint64_t *bar, uint32_t pa
     return false;
 }
 
-// And for one that may take as long as a whole pair, on others whose own waits are bounded.
+// And for one that may take as long as a whole pair, or as the last CTAs' number gives requests, on
+// others whose own waits are bounded.
 __device__ __forceinline__ bool wait_far(Shared &sh, uint64_t *bar, uint32_t parity) {
     for (uint32_t it = 0; it < 16 * WAIT_LIMIT; ++it) {
         if (mbar_test(bar, parity)) return true;
@@ -280,9 +281,10 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     // Work goes by rank: heads side by side, the longest pairs of all of them first, so that
     // what is left at the end is short, and CTAs that share a head's keys walk them at the
     // same time.
-    int b0 = 0, b1 = 0, sum = 0, at = 0;
+    int b0 = 0, b1 = 0, sum = 0, at = 0, pairs = 0;
     const auto work_of = [&](int cta) {
-        return find_work(p, b0, b1, at, sum, cta / p.Hq, cta % p.Hq);
+        const int rank = cta / p.Hq;
+        return rank < pairs ? find_work(p, b0, b1, at, sum, rank, cta % p.Hq) : Work{0, 0, 0, 0, -1, 0};
     };
     if (warp == 2) {
         const int per = (p.B + 31) / 32;
@@ -296,6 +298,7 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             const int v = __shfl_up_sync(0xFFFFFFFFu, at, o);
             if (lane >= o) at += v;
         }
+        pairs = __shfl_sync(0xFFFFFFFFu, at, 31);
         at -= sum;
         const Work w = work_of(blockIdx.x);
         if (lane == 0) sh.item[0] = Item{w, 0, 0, {0, 0}, {0, 0}};
@@ -345,7 +348,7 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     const auto next_item = [&](uint32_t item, bool one_thread) {
         if (one_thread || lane == 0) mbar_arrive(&sh.item_free[item & 1]);
         ++item;
-        return wait_long(sh, &sh.item_full[item & 1], ((item - 1) >> 1) & 1) && sh.item[item & 1].w.pair >= 0;
+        return wait_far(sh, &sh.item_full[item & 1], ((item - 1) >> 1) & 1) && sh.item[item & 1].w.pair >= 0;
     };
 
     if (sh.item[0].w.pair < 0) {
@@ -531,10 +534,9 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 __syncwarp();
                 return true;
             };
+            uint32_t asked = 0;
             for (uint32_t item = 0;; ++item) {
                 if (!__all_sync(0xFFFFFFFFu, wait_far(sh, &sh.near_end, item & 1))) break;
-                int cta;
-                if (!ask(item, cta)) break;
                 const Extent was(it.w);
                 it.g0 += was.n;
                 it.slot0 = (it.slot0 + (was.n % Z::SLOTS) * Z::TILE) % Z::SLOTS;
@@ -543,8 +545,16 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                     it.met[t] += was.tiles(t);
                     it.outputs[t] += was.tiles(t) > 0;
                 }
+                // CTAs without work are among those that have not started (nothing says in which
+                // order they are handed out): the next one with work, or the end of them all
                 it.w.pair = -1;
-                if (cta >= 0) it.w = work_of(cta);
+                bool there;
+                int cta = 0;
+                while ((there = ask(asked++, cta)) && cta >= 0) {
+                    it.w = work_of(cta);
+                    if (it.w.pair >= 0) break;
+                }
+                if (!there) break;
                 // the item before this slot's last is left behind by all
                 if (item > 0 && !__all_sync(0xFFFFFFFFu, wait_long(sh, &sh.item_free[(item - 1) & 1],
                                                                    ((item - 1) >> 1) & 1)))
@@ -554,12 +564,7 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                     mbar_arrive(&sh.item_full[(item + 1) & 1]);
                 }
                 const Work w = it.w;
-                if (w.pair < 0) {
-                    // whatever has not started by now has no work either
-                    for (uint32_t more = item + 1; cta >= 0 && ask(more, cta); ++more) {
-                    }
-                    break;
-                }
+                if (w.pair < 0) break;
                 if (elect_one()) {
                     const Extent x(w);
                     for (int t = 0; t < 2; ++t)
