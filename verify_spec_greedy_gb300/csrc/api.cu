@@ -73,6 +73,8 @@ MTPSPEC_API int mtpspec_selftest_wait_timeout(int which, uint32_t limit, int32_t
     cudaError_t e = which == 0 ? mtpspec::run_wait_selftest_clusters(limit, status, s)
                     : which == 1 ? mtpspec::run_wait_selftest_chunks(limit, status, s)
                                  : mtpspec::run_wait_selftest_gemm(limit, status, s);
+    if (which == 2 && e == cudaSuccess) e = mtpspec::run_wait_selftest_latent_attn(limit, status, s);
+    if (which == 2 && e == cudaSuccess) e = mtpspec::run_wait_selftest_latent_prefill(limit, status, s);
     return launched(e);
 }
 

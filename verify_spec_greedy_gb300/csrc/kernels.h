@@ -108,6 +108,10 @@ cudaError_t run_verify_chunks(const VerifySampleArgs &a, cudaStream_t stream);
 cudaError_t run_wait_selftest_clusters(uint32_t limit, int32_t *status, cudaStream_t stream);
 cudaError_t run_wait_selftest_chunks(uint32_t limit, int32_t *status, cudaStream_t stream);
 cudaError_t run_wait_selftest_gemm(uint32_t limit, int32_t *status, cudaStream_t stream);
+// These two take the timeout that a wait of the GEMM has set out of `status` when one of theirs
+// does not give up.
+cudaError_t run_wait_selftest_latent_attn(uint32_t limit, int32_t *status, cudaStream_t stream);
+cudaError_t run_wait_selftest_latent_prefill(uint32_t limit, int32_t *status, cudaStream_t stream);
 
 // The fixed-scratch variant: per-unit records in the library's static device array
 // (a.workspace is ignored).  Units B * (D + 1) must not exceed kStaticVerifyUnits.

@@ -158,8 +158,9 @@ constexpr int SMEM_EXTRA = static_cast<int>(sizeof(Shared));
 
 // A bounded wait; once any wait of the CTA has given up, the others return at once, and the
 // roles run to their ends without touching what they could not wait for.
-__device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity) {
-    for (uint32_t it = 0; it < POLL_LIMIT; ++it) {
+__device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity,
+                                    uint32_t limit = POLL_LIMIT) {
+    for (uint32_t it = 0; it < limit; ++it) {
         if (mbar_poll(bar, parity)) return true;
         if (sh.abort) return false;
     }
@@ -169,8 +170,9 @@ __device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity)
 
 // The same for a wait that is mostly long: the thread is suspended instead of polling, which
 // leaves issue slots and shared memory to the others.
-__device__ __forceinline__ bool wait_long(Shared &sh, uint64_t *bar, uint32_t parity) {
-    for (uint32_t it = 0; it < WAIT_LIMIT; ++it) {
+__device__ __forceinline__ bool wait_long(Shared &sh, uint64_t *bar, uint32_t parity,
+                                         uint32_t limit = WAIT_LIMIT) {
+    for (uint32_t it = 0; it < limit; ++it) {
         if (mbar_test(bar, parity)) return true;
         if (sh.abort) return false;
     }
@@ -901,6 +903,24 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_latent_join(const Params p) {
         p.lse[static_cast<int64_t>(u.x) * rows_all + m] = sum > 0.0f ? (top + log2f(sum)) * LN2 : -INFINITY;
 }
 
+// Diagnostic of the bounded waits, as the other kernels': on a barrier of two arrivals that got
+// one, both forms must give up after `limit` polls and raise the abort flag; if not, the timeout
+// is taken out of the status word.
+__global__ void k_wait_selftest(uint32_t limit, int32_t *status) {
+    __shared__ Shared sh;
+    if (threadIdx.x != 0) return;
+    mbar_init(&sh.drained, 2);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    mbar_arrive(&sh.drained);
+    bool ok = true;
+    for (int form = 0; form < 2; ++form) {
+        sh.abort = 0;
+        const bool got = form == 0 ? wait(sh, &sh.drained, 0, limit) : wait_long(sh, &sh.drained, 0, limit);
+        ok &= !got && sh.abort;
+    }
+    if (!ok) atomicAnd(status, ~MTPSPEC_STATUS_TIMEOUT);
+}
+
 size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 struct Layout {
@@ -967,6 +987,13 @@ cudaError_t pick(const Maps &maps, const Params &p, cudaStream_t stream) {
 size_t latent_attn_workspace_bytes(int64_t B, int32_t T, int32_t Hq, int32_t L) {
     (void)B;
     return lat::layout(static_cast<int64_t>(T) * Hq, L).total;
+}
+
+cudaError_t run_wait_selftest_latent_attn(uint32_t limit, int32_t *status, cudaStream_t stream) {
+    lat::k_wait_selftest<<<1, 32, 0, stream>>>(limit, status);
+    const cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) count_launches(1);
+    return e;
 }
 
 cudaError_t run_latent_attn(const LatentAttnArgs &a, int dtype, cudaStream_t stream) {

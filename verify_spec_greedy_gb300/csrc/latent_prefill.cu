@@ -83,11 +83,13 @@ struct __align__(16) Shared {
     uint32_t tmem;
     volatile int abort;
     float other[2][2][TM];  // what the two threads of a row tell each other, by tile and half
+    volatile int go[2][4][2];  // and their warps, by tile, rows and half: is there a next item?
 };
 constexpr int SMEM_EXTRA = static_cast<int>(sizeof(Shared));
 
-__device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity) {
-    for (uint32_t it = 0; it < POLL_LIMIT; ++it) {
+__device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity,
+                                    uint32_t limit = POLL_LIMIT) {
+    for (uint32_t it = 0; it < limit; ++it) {
         if (mbar_poll(bar, parity)) return true;
         if (sh.abort) return false;
     }
@@ -97,8 +99,9 @@ __device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity)
 
 // The same for a wait that is mostly long: the thread is suspended instead of polling, which
 // leaves issue slots and shared memory to the others.
-__device__ __forceinline__ bool wait_long(Shared &sh, uint64_t *bar, uint32_t parity) {
-    for (uint32_t it = 0; it < WAIT_LIMIT; ++it) {
+__device__ __forceinline__ bool wait_long(Shared &sh, uint64_t *bar, uint32_t parity,
+                                         uint32_t limit = WAIT_LIMIT) {
+    for (uint32_t it = 0; it < limit; ++it) {
         if (mbar_test(bar, parity)) return true;
         if (sh.abort) return false;
     }
@@ -108,13 +111,23 @@ __device__ __forceinline__ bool wait_long(Shared &sh, uint64_t *bar, uint32_t pa
 
 // And for one that may take as long as a whole pair, or as the last CTAs' number gives requests, on
 // others whose own waits are bounded.
-__device__ __forceinline__ bool wait_far(Shared &sh, uint64_t *bar, uint32_t parity) {
-    for (uint32_t it = 0; it < 16 * WAIT_LIMIT; ++it) {
+__device__ __forceinline__ bool wait_far(Shared &sh, uint64_t *bar, uint32_t parity,
+                                        uint32_t limit = 16 * WAIT_LIMIT) {
+    for (uint32_t it = 0; it < limit; ++it) {
         if (mbar_test(bar, parity)) return true;
         if (sh.abort) return false;
     }
     sh.abort = 1;
     return false;
+}
+
+// Whether both warps of a row's halves say yes.  They meet at barrier `bar` in everything they
+// do, so that after a wait that gave up neither may go on without the other; and they meet there
+// once more before the next question.
+__device__ __forceinline__ bool both(volatile int (&said)[2], int half, bool yes, int bar) {
+    if ((threadIdx.x & 31) == 0) said[half] = yes;
+    asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
+    return said[0] && said[1];
 }
 
 // The bounded wait of a CTA that leaves, whatever the abort flag says.
@@ -344,9 +357,8 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    // Every role goes through the CTA's items; the one after number `item` (false: none).
-    const auto next_item = [&](uint32_t item, bool one_thread) {
-        if (one_thread || lane == 0) mbar_arrive(&sh.item_free[item & 1]);
+    // Every role goes through the CTA's items: is there one after number `item`, and no abort?
+    const auto next_item = [&](uint32_t item) {
         ++item;
         return wait_far(sh, &sh.item_full[item & 1], ((item - 1) >> 1) & 1) && sh.item[item & 1].w.pair >= 0;
     };
@@ -408,7 +420,8 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                     // go to a CTA that will be free later than another: 8 x 800 tokens x 32
                     // heads 93 -> 94.5, 96, 98; by the issuer at its last tile, 99 us.)
                     mbar_arrive(&sh.near_end);
-                    if (sh.abort || !next_item(item, true)) break;
+                    mbar_arrive(&sh.item_free[item & 1]);
+                    if (sh.abort || !next_item(item)) break;
                 }
                 if (sh.abort) {
                     // let the copies in flight land: the last two tiles' and the queries' (a
@@ -505,7 +518,8 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                             }
                         }
                     }
-                    if (sh.abort || !next_item(item, true)) break;
+                    mbar_arrive(&sh.item_free[item & 1]);
+                    if (sh.abort || !next_item(item)) break;
                 }
                 mma_commit(&sh.drained);
                 wait_out(&sh.drained, 0);
@@ -559,6 +573,7 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 if (item > 0 && !__all_sync(0xFFFFFFFFu, wait_long(sh, &sh.item_free[(item - 1) & 1],
                                                                    ((item - 1) >> 1) & 1)))
                     break;
+                if (__any_sync(0xFFFFFFFFu, sh.abort)) break;  // no more work for a CTA that leaves
                 if (lane == 0) {
                     sh.item[(item + 1) & 1] = it;
                     mbar_arrive(&sh.item_full[(item + 1) & 1]);
@@ -726,10 +741,12 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 }
             }
             // The next pair's products overwrite this output once its first weights are there,
-            // which come after these reads.  Both threads of a row have read each other's sum.
+            // which come after these reads.
             tc_fence_before();
-            asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
-            if (!next_item(item, false)) break;
+            __syncwarp();  // the whole warp is done with the item
+            if (lane == 0) mbar_arrive(&sh.item_free[item & 1]);
+            const bool more = __all_sync(0xFFFFFFFFu, next_item(item));
+            if (!both(sh.go[t][warp & 3], half, more, pair_bar)) break;
         }
     }
     tc_fence_before();
@@ -741,6 +758,40 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                      "r"(TMEM_COLS)
                      : "memory");
     }
+}
+
+// Diagnostic of the bounded waits: on a barrier of two arrivals that got one, each form must give
+// up after `limit` polls and raise the abort flag; and of two warps of which one's wait completed,
+// neither goes on.  If any does otherwise, the timeout is taken out of the status word.
+__global__ void k_wait_selftest(uint32_t limit, int32_t *status) {
+    __shared__ Shared sh;
+    uint64_t *never = &sh.item_full[0], *done = &sh.item_full[1];
+    if (threadIdx.x == 0) {
+        mbar_init(never, 2);
+        mbar_init(done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        mbar_arrive(never);
+        mbar_arrive(done);
+    }
+    bool ok = true;
+    for (int form = 0; form < 4; ++form) {
+        __syncthreads();
+        if (threadIdx.x == 0) sh.abort = 0;
+        __syncthreads();
+        bool got;
+        if (form == 3) {  // one warp's next item is there, the other's is not
+            const int half = threadIdx.x >> 5;
+            const bool there = wait_far(sh, half ? never : done, 0, limit);
+            ok &= there == (half == 0);
+            got = both(sh.go[0][0], half, __all_sync(0xFFFFFFFFu, there), 1);
+        } else {
+            got = form == 0 ? wait(sh, never, 0, limit)
+                  : form == 1 ? wait_long(sh, never, 0, limit) : wait_far(sh, never, 0, limit);
+        }
+        __syncthreads();
+        ok &= !got && sh.abort;
+    }
+    if (!ok) atomicAnd(status, ~MTPSPEC_STATUS_TIMEOUT);
 }
 
 template <typename T, int KC, int VC>
@@ -785,6 +836,13 @@ bool token_map(CUtensorMap *m, const uint16_t *ptr, int64_t tokens, int64_t head
 }
 
 }  // namespace lpf
+
+cudaError_t run_wait_selftest_latent_prefill(uint32_t limit, int32_t *status, cudaStream_t stream) {
+    lpf::k_wait_selftest<<<1, 64, 0, stream>>>(limit, status);
+    const cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) count_launches(1);
+    return e;
+}
 
 cudaError_t run_latent_prefill(const LatentPrefillArgs &a, int dtype, cudaStream_t stream) {
     CUtensorMap mq, mkv, mrot;
