@@ -124,8 +124,8 @@ size_t mtp_latent_attn_workspace_bytes(int64_t B, int32_t T, int32_t Hq, int32_t
  *   cu_q, cu_k int32 [B + 1], not decreasing, from 0 to Tq and Tk
  *   out  [Tq, Hq, V] with token and head strides       lse float [Tq, Hq] or NULL
  *   status int32 [1] or NULL: MTPSPEC_STATUS_BAD_PARAM is OR-ed in for a bound out of range
- *        or out of order (taken as the nearest good one); MTPSPEC_STATUS_TIMEOUT if a wait
- *        gave up.
+ *        or out of order (taken as the nearest good one: in range, and not below the bounds
+ *        before it); MTPSPEC_STATUS_TIMEOUT if a wait gave up.
  * N and V are 64 or 128; 16 <= R <= 64 with R % 16 == 0; 0 <= Tq, Tk <= 2^24 (Tk >= 1 when
  * Tq > 0), 1 <= B <= 65536, 1 <= Hq <= 1024, scale finite and above
  * 0.  Queries outside every sequence

@@ -136,12 +136,10 @@ __device__ __forceinline__ void wait_out(uint64_t *bar, uint32_t parity) {
         if (mbar_test(bar, parity)) return;
 }
 
-// A sequence's bounds in [0, n], in order.
-__device__ __forceinline__ int2 bounds(const int32_t *cu, int b, int n, bool &bad) {
-    const int c0 = cu[b], c1 = cu[b + 1];
-    const int a = min(max(c0, 0), n), e = min(max(c1, a), n);
-    bad |= a != c0 || e != c1;
-    return make_int2(a, e);
+// Bound i of `cu` as it is taken: in [0, n], and not below the ones before it (as taken, `before`,
+// at least 0), so that sequences never overlap and have no more pairs than the grid has CTAs.
+__device__ __forceinline__ int bound(const int32_t *cu, int i, int n, int before) {
+    return max(min(cu[i], n), before);
 }
 
 // D[128, n] (+)= A[128, 16] B[16, n], A from tensor memory.  (Descriptors stay 64-bit values
@@ -172,14 +170,21 @@ __host__ __device__ constexpr uint32_t idesc_of(int n, bool b_rows_k) {
            (static_cast<uint32_t>(TM >> 4) << 24);
 }
 
-__device__ __forceinline__ int pairs_of(int2 q) { return (q.y - q.x + 2 * TM - 1) / (2 * TM); }
+__device__ __forceinline__ int pairs_of(int queries) { return (queries + 2 * TM - 1) / (2 * TM); }
 
-// The pair of number `rank`, for a warp whose lanes hold sequences b0 .. b1 - 1, with `at`
-// pairs before them and `sum` of their own.  Up to 32 sequences (one a lane), pairs go by
-// their place in their sequence, the furthest first; beyond, sequence by sequence.
-__device__ __forceinline__ Work find_work(const Params &p, int b0, int b1, int at, int sum, int rank,
-                                          int head) {
+// A lane's run of sequences b0 .. b1 - 1: the largest bounds before its first, the pairs before
+// it and its own.
+struct Run {
+    int b0, b1, q_before, k_before, at, sum;
+};
+
+// The pair of number `rank`, for a warp whose lanes hold the runs.  Up to 32 sequences (one a
+// lane), pairs go by their place in their sequence, the furthest first; beyond, sequence by
+// sequence.
+__device__ __forceinline__ Work find_work(const Params &p, const Run &run, int rank, int head) {
     Work w = {0, 0, 0, 0, -1, head};
+    const int sum = run.sum;
+    int at = run.at;
     bool mine = at <= rank && rank < at + sum;
     int pair = at + sum - 1 - rank;
     if (p.B > 1 && p.B <= 32) {
@@ -199,16 +204,17 @@ __device__ __forceinline__ Work find_work(const Params &p, int b0, int b1, int a
         }
     }
     if (mine) {
-        bool bad = false;
-        for (int b = b0; b < b1; ++b) {
-            const int2 q = bounds(p.cu_q, b, p.Tq, bad);
-            const int n = pairs_of(q);
+        int q0 = bound(p.cu_q, run.b0, p.Tq, run.q_before), k0 = bound(p.cu_k, run.b0, p.Tk, run.k_before);
+        for (int b = run.b0; b < run.b1; ++b) {
+            const int q1 = bound(p.cu_q, b + 1, p.Tq, q0), k1 = bound(p.cu_k, b + 1, p.Tk, k0);
+            const int n = pairs_of(q1 - q0);
             if (p.B <= 32 || rank < at + n) {
-                const int2 k = bounds(p.cu_k, b, p.Tk, bad);
-                w = {q.x, q.y - q.x, k.x, k.y - k.x, p.B <= 32 ? pair : n - 1 - (rank - at), head};
+                w = {q0, q1 - q0, k0, k1 - k0, p.B <= 32 ? pair : n - 1 - (rank - at), head};
                 break;
             }
             at += n;
+            q0 = q1;
+            k0 = k1;
         }
     }
     const unsigned who = __ballot_sync(0xFFFFFFFFu, mine);
@@ -294,29 +300,57 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     // Work goes by rank: heads side by side, the longest pairs of all of them first, so that
     // what is left at the end is short, and CTAs that share a head's keys walk them at the
     // same time.
-    int b0 = 0, b1 = 0, sum = 0, at = 0, pairs = 0;
+    Run run = {};
+    int pairs = 0;
     const auto work_of = [&](int cta) {
         const int rank = cta / p.Hq;
-        return rank < pairs ? find_work(p, b0, b1, at, sum, rank, cta % p.Hq) : Work{0, 0, 0, 0, -1, 0};
+        return rank < pairs ? find_work(p, run, rank, cta % p.Hq) : Work{0, 0, 0, 0, -1, 0};
     };
     if (warp == 2) {
         const int per = (p.B + 31) / 32;
-        b0 = min(p.B, lane * per);
-        b1 = min(p.B, b0 + per);
-        bool bad = false;
-        for (int b = b0; b < b1; ++b) sum += pairs_of(bounds(p.cu_q, b, p.Tq, bad));
-        at = sum;
+        run.b0 = min(p.B, lane * per);
+        run.b1 = min(p.B, run.b0 + per);
+        int q = 0, k = 0;  // the largest bounds up to and with this run's
+        for (int b = run.b0; b < run.b1; ++b) {
+            q = bound(p.cu_q, b, p.Tq, q);
+            k = bound(p.cu_k, b, p.Tk, k);
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {  // (lanes without one to their left get their own)
+            q = max(q, __shfl_up_sync(0xFFFFFFFFu, q, o));
+            k = max(k, __shfl_up_sync(0xFFFFFFFFu, k, o));
+        }
+        q = __shfl_up_sync(0xFFFFFFFFu, q, 1);
+        k = __shfl_up_sync(0xFFFFFFFFu, k, 1);
+        run.q_before = lane > 0 ? q : 0;
+        run.k_before = lane > 0 ? k : 0;
+        if (run.b0 < run.b1) {
+            int q0 = bound(p.cu_q, run.b0, p.Tq, run.q_before);
+            for (int b = run.b0; b < run.b1; ++b) {
+                const int q1 = bound(p.cu_q, b + 1, p.Tq, q0);
+                run.sum += pairs_of(q1 - q0);
+                q0 = q1;
+            }
+        }
+        run.at = run.sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xFFFFFFFFu, at, o);
-            if (lane >= o) at += v;
+            const int v = __shfl_up_sync(0xFFFFFFFFu, run.at, o);
+            if (lane >= o) run.at += v;
         }
-        pairs = __shfl_sync(0xFFFFFFFFu, at, 31);
-        at -= sum;
+        pairs = __shfl_sync(0xFFFFFFFFu, run.at, 31);
+        run.at -= run.sum;
         const Work w = work_of(blockIdx.x);
         if (lane == 0) sh.item[0] = Item{w, 0, 0, {0, 0}, {0, 0}};
         if (blockIdx.x == 0 && p.status) {
-            for (int b = b0; b < b1; ++b) bounds(p.cu_k, b, p.Tk, bad);
+            bool bad = false;
+            int q0 = run.q_before, k0 = run.k_before;
+            // (a run looks at its own bounds, and the last one at the end of all)
+            for (int b = run.b0; b < run.b1 + (run.b1 == p.B && run.b0 < run.b1); ++b) {
+                q0 = bound(p.cu_q, b, p.Tq, q0);
+                k0 = bound(p.cu_k, b, p.Tk, k0);
+                bad |= q0 != p.cu_q[b] || k0 != p.cu_k[b];
+            }
             if (bad) atomicOr(p.status, MTPSPEC_STATUS_BAD_PARAM);
         }
     }
