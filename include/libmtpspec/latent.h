@@ -79,7 +79,8 @@ int mtp_latent_append(const void *latent, int64_t latent_stride, const void *rot
  *     s_n = scale * q[b][t][h] . cache(b, n)          (L + R products, fp32)
  *     out[b][t][h] = sum_n softmax(s)_n cache(b, n)[0..L)
  *     lse[b][t][h] = ln sum_n e^(s_n)                 (when lse is not NULL)
- * A query that sees nothing has out = 0 and lse = -inf.  The weights are rounded to `dtype`
+ * A query that sees nothing has out = 0 and lse = -inf; one with a NaN among the scores that it
+ * sees has NaN in both, and changes no other.  The weights are rounded to `dtype`
  * before their products (as the tensor cores take them), all sums are fp32, and the output
  * is rounded once.
  *
@@ -116,7 +117,7 @@ size_t mtp_latent_attn_workspace_bytes(int64_t B, int32_t T, int32_t Hq, int32_t
  * (the sequence's last query sees every key; nk > nq is a chunk behind a cached prefix).
  *     s_j = scale * (q[i][h][0..N) . kv[j][h][0..N) + q[i][h][N..N+R) . rot[j])
  *     out[i][h] = sum_j softmax(s)_j kv[j][h][N..N+V),   lse[i][h] = ln sum_j e^(s_j)
- * A query that sees nothing has out = 0 and lse = -inf; precision as in mtp_latent_attn.
+ * A query that sees nothing has out = 0 and lse = -inf; NaN and precision as in mtp_latent_attn.
  *
  *   q    [Tq, Hq, N + R] with token and head strides
  *   kv   [Tk, Hq, N + V] with token and head strides (a token's key, then its value)

@@ -738,8 +738,9 @@ k_latent_attn(const __grid_constant__ Maps maps, const Params p) {
             tc_fence_after();
             const bool whole = w.i0 == 0 && w.i1 == w.int_;
             const bool real = m < rows_all;
-            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-            const float lse2 = l > 0.0f ? m_ref + log2f(l) : -INFINITY;
+            // (a sum of zero: nothing was seen; one that is NaN stays so)
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const float lse2 = l == 0.0f ? -INFINITY : m_ref + log2f(l);
             if (real && half == 0) {
                 if (!whole)
                     p.part_lse[(2 * cta + (w.i0 > 0 ? 0 : 1)) * static_cast<int64_t>(p.rows_cap) + r] =
@@ -889,7 +890,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_latent_join(const Params p) {
         }
         acc[0] = s4;
     }
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const int t = m / p.Hq, h = m - t * p.Hq;
     uint16_t *dst = p.out + u.x * p.out_row + t * p.out_tok + h * p.out_head;
 #pragma unroll
@@ -900,7 +901,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_latent_join(const Params p) {
                 make_uint2(T::narrow2(acc[k].x * inv, acc[k].y * inv), T::narrow2(acc[k].z * inv, acc[k].w * inv));
     }
     if (p.lse && lane == 0 && (!WIDE || warp == 0))
-        p.lse[static_cast<int64_t>(u.x) * rows_all + m] = sum > 0.0f ? (top + log2f(sum)) * LN2 : -INFINITY;
+        p.lse[static_cast<int64_t>(u.x) * rows_all + m] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * LN2;
 }
 
 // Diagnostic of the bounded waits, as the other kernels': on a barrier of two arrivals that got

@@ -742,10 +742,10 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             l += swap(l);
             const int row = my.w.pair * 2 * TM + t * TM + r, head = my.w.head;
             const bool real = row < my.w.nq;
-            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // (zero: nothing was seen; NaN stays)
             const int64_t tok = my.w.q0 + row;
             if (real && half == 0 && p.lse)
-                p.lse[tok * p.Hq + head] = l > 0.0f ? (m_ref + log2f(l)) * LN2 : -INFINITY;
+                p.lse[tok * p.Hq + head] = l == 0.0f ? -INFINITY : (m_ref + log2f(l)) * LN2;
             uint16_t *dst = p.out + tok * p.out_tok + head * p.out_head + half * (VC * 32);
             // 32 bytes a store, a whole sector, where the rows allow it
             const bool sectors = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
