@@ -82,7 +82,8 @@ int mtp_latent_append(const void *latent, int64_t latent_stride, const void *rot
  * A query that sees nothing has out = 0 and lse = -inf; one with a NaN among the scores that it
  * sees has NaN in both, and changes no other.  The weights are rounded to `dtype`
  * before their products (as the tensor cores take them), all sums are fp32, and the output
- * is rounded once.
+ * is rounded once.  In float16 a weight below 2^-21 of the largest one so far has fewer bits
+ * than the type's 11, and one below 2^-32 counts for nothing in out (lse has it all the same).
  *
  *   q     [B, T, Hq, L + R] with row, token and head strides
  *   out   [B, T, Hq, L] with row, token and head strides      lse float [B, T, Hq] or NULL

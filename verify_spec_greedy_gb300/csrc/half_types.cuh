@@ -10,6 +10,9 @@ namespace mtpspec {
 
 struct Bf16 {
     static constexpr uint32_t mma_format = 1;  // operand format field of kind::f16
+    // A softmax's first weight, in powers of two, when it is rounded to this type: bf16 has the
+    // exponents of fp32, and its smallest weights are worth as many bits as the largest.
+    static constexpr float first_weight = 0.0f;
     static __device__ __forceinline__ float2 widen2(uint32_t v) {
         return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
     }
@@ -21,6 +24,11 @@ struct Bf16 {
 
 struct F16 {
     static constexpr uint32_t mma_format = 0;
+    // fp16's normal values end at 2^-14 and its largest is just below 2^16.  Weights start at 2^7
+    // and, while the maximum they refer to lags by up to 2^8, stay within 2^15; so those down to
+    // 2^-21 of the first keep all their bits, those down to 2^-32 some.  (From 1, keys 2^-18 below
+    // an early high one were off by up to 2^-7: a fair part of the output when they are many.)
+    static constexpr float first_weight = 7.0f;
     static __device__ __forceinline__ float2 widen2(uint32_t v) {
         return __half22float2(*reinterpret_cast<const __half2 *>(&v));
     }

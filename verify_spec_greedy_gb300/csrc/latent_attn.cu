@@ -6,9 +6,10 @@
 //     S = Q K^T,  p = 2^(s - m),  l += sum p,  O += p V,  and O, l scaled by 2^(m - m') when m
 // changes (s, m in powers of two, scale * log2 e folded in).  V is the first L columns of K, so
 // a tile is brought to shared memory once and used for both products.  m follows a row's
-// maximum only when that has grown by more than 2^8: weights stay below 2^8, which 16 bits and
-// the fp32 sums take without loss, and O is rarely rescaled.  Weights are rounded to 16 bits
-// for the second product; l sums the unrounded ones in fp32.
+// maximum only when that has grown by more than 2^8, so O is rarely rescaled.  Weights are rounded
+// to 16 bits for the second product; l sums the unrounded ones in fp32.  In fp16, m lies 2^7 below
+// the maximum that it was taken from: weights start at 2^7, stay within 2^15, and keep seven more
+// powers of two above the subnormal ones; O, l and m carry the factor, and out and lse do not.
 //
 // Rows: a sequence's T * Hq (token, head) pairs in tiles of 64, which with L <= 512 output
 // columns in fp32 take half of the tensor memory (the accumulator of 64 rows is folded into
@@ -650,9 +651,9 @@ k_latent_attn(const __grid_constant__ Maps maps, const Params p) {
                 asm volatile("bar.sync %0, 64;" ::"r"(1 + (wq & 1)) : "memory");
                 top = fmaxf(top, sh.xm[slot][wq ^ 2][lane]) * p.scale2;
                 slot ^= 1;
-                const bool raise = top > m_ref + LAZY;
+                const bool raise = top > m_ref + (LAZY + T::first_weight);
                 const float m_old = m_ref;
-                if (raise) m_ref = top;
+                if (raise) m_ref = top - T::first_weight;
                 const float m_use = m_ref == -INFINITY ? 0.0f : m_ref;
                 const uint64_t scale_2 = pack2(p.scale2, p.scale2), minus_m = pack2(-m_use, -m_use);
                 uint64_t part[2] = {0, 0};  // two pairs of sums

@@ -5,7 +5,8 @@
 //     S = Q K^T,  p = 2^(s - m),  l += sum p,  O += p V,  and O, l scaled by 2^(m - m') when m
 // changes (s, m in powers of two, scale * log2 e folded in; m follows a row's maximum only when
 // that has grown by more than 2^8).  Weights are rounded to 16 bits for the second product; l
-// sums the unrounded ones in fp32.  Keys that no query of a tile sees are never read.
+// sums the unrounded ones in fp32.  (In fp16 m lies 2^7 below that maximum, so that fewer weights
+// are subnormal: half_types.cuh.)  Keys that no query of a tile sees are never read.
 //
 // A pair of query tiles, 256 queries of one head, is a CTA's unit of work: while the tensor
 // cores work on one tile's products, the other tile's softmax runs, eight warps a tile, two
@@ -694,10 +695,11 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 // (the second barrier of a tile is p_ready: nobody writes the next value before
                 // the products have taken both threads' weights)
                 const float top = fmaxf(mine, swap(mine)) * p.scale2;
-                const bool raise = top > m_ref + LAZY;
+                const bool raise = top > m_ref + (LAZY + T::first_weight);
+                const float m_new = top - T::first_weight;
                 if (__builtin_expect(j > 0 && __any_sync(0xFFFFFFFFu, raise), 0)) {
                     // the scores came after the products of the tile before: the output is free
-                    const float f = raise ? ex2(m_ref - top) : 1.0f;
+                    const float f = raise ? ex2(m_ref - m_new) : 1.0f;
                     l *= f;
 #pragma unroll
                     for (int c = half * (VC * 32); c < (half + 1) * (VC * 32); c += 16) {
@@ -709,7 +711,7 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                         tmem_st16(o_t + c, o);
                     }
                 }
-                if (raise) m_ref = top;
+                if (raise) m_ref = m_new;
                 const float m_use = m_ref == -INFINITY ? 0.0f : m_ref;
                 const uint64_t scale_2 = pack2(p.scale2, p.scale2), minus_m = pack2(-m_use, -m_use);
                 uint64_t part[2] = {0, 0};  // two pairs of sums
