@@ -381,6 +381,21 @@ def _half_codes():
     return _HALF_CODES
 
 
+def _axes(t, name, n):
+    """The sizes of a tensor of n axes."""
+    try:
+        s = t.shape
+        if len(s) == n:
+            return s
+    except (AttributeError, TypeError):
+        pass
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not isinstance(t, _kinds()["tensor"]):
+        raise TypeError(f"{name} must be a torch tensor")
+    raise ValueError(f"{name} must have {n} axes, got shape {tuple(t.shape)}")
+
+
 def _view(t, name, shape, like=None):
     """(pointer, strides in elements) of a 16-bit tensor of `shape` on the GPU whose last axis
     is contiguous; `like` gives the type it has to have.  An axis of one has stride 0."""
@@ -413,17 +428,17 @@ def _refuse_view(t, name, shape, like):
 
 def _vec(t, name, dtype, kind, numel=0):
     """As _arg, for a tensor of one type."""
-    if (t is not None and t.dtype is dtype and t.is_cuda and t.is_contiguous() and
-            t.numel() >= numel):
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() >= numel:
+            return t.data_ptr()
+    except AttributeError:
+        pass
     return _arg(t, name, kind, numel)
 
 
 def _cache_view(cache, like, W):
     """(pointer, pages, page size, page stride) of a paged cache [pages, page_size, W]."""
-    if cache is None or cache.dim() != 3:
-        raise ValueError("cache must be [pages, page_size, L + R]")
-    n, P, _ = cache.shape
+    n, P, _ = _axes(cache, "cache", 3)
     ptr, st = _view(cache, "cache", (n, P, W), like)
     if P > 1 and st[1] != W:
         raise ValueError("the rows of a cache page must be contiguous")
@@ -438,28 +453,29 @@ def mtp_latent_append(latent, rot, cos_sin, tok_row, positions, block_table, cac
     include/libmtpspec/latent.h).  Row strides, and token and head strides, may be any
     multiple of 8 elements."""
     codes = _HALF_CODES or _half_codes()
-    T, L = latent.shape
-    R = rot.shape[1]
+    T, L = _axes(latent, "latent", 2)
+    R = _axes(rot, "rot", 2)[1]
     dt = latent.dtype
-    B, max_pages = block_table.shape
+    B, max_pages = _axes(block_table, "block_table", 2)
     lp, ls = _view(latent, "latent", (T, L))
     rp, rs = _view(rot, "rot", (T, R), dt)
     cp, pages, P, page_stride = _cache_view(cache, dt, L + R)
-    if cos_sin.dim() != 2 or cos_sin.shape[1] != R:
+    max_pos, angles = _axes(cos_sin, "cos_sin", 2)
+    if angles != R:
         raise ValueError(f"cos_sin must be [max_pos, {R}]")
     queries = (None, 0, 0, None, 0, 0, 0)
     if q_rot is not None or q_out is not None:
         if q_rot is None or q_out is None:
             raise ValueError("q_rot and q_out go together")
-        Hq = q_rot.shape[1]
+        Hq = _axes(q_rot, "q_rot", 3)[1]
         qp, qs = _view(q_rot, "q_rot", (T, Hq, R), dt)
         op, os_ = _view(q_out, "q_out", (T, Hq, R), dt)
         queries = (qp, qs[0], qs[1], op, os_[0], os_[1], Hq)
-    if norm_w is not None and norm_w.dtype != dt:
+    if norm_w is not None and getattr(norm_w, "dtype", dt) != dt:
         raise TypeError(f"norm_w must hold {dt} values, got {norm_w.dtype}")
     _call("mtp_latent_append", lp, ls[0], rp, rs[0],
           None if norm_w is None else _vec(norm_w, "norm_w", dt, _HALF, L), float(eps),
-          _vec(cos_sin, "cos_sin", _FLOAT, _F32), cos_sin.shape[0], 1 if interleaved else 0,
+          _vec(cos_sin, "cos_sin", _FLOAT, _F32), max_pos, 1 if interleaved else 0,
           _vec(tok_row, "tok_row", _INT, _I32, T), _vec(positions, "positions", _INT, _I32, T), T, L,
           R, _vec(block_table, "block_table", _INT, _I32), B, max_pages, cp, pages, P, page_stride,
           *queries, codes[dt], _arg(status, "status", _I32, 1, optional=True),
@@ -476,17 +492,18 @@ def mtp_latent_attn(q, cache, block_table, kv_len, out, scale: float, lse=None, 
     """out[B, T, Hq, L]: attention of q[B, T, Hq, L + R] over the paged cache, query t of row b
     seeing positions below kv_len[b] - (T - 1 - t) (see include/libmtpspec/latent.h)."""
     codes = _HALF_CODES or _half_codes()
-    B, T, Hq, W = q.shape
-    L = out.shape[-1]
+    B, T, Hq, W = _axes(q, "q", 4)
+    L = _axes(out, "out", 4)[3]
     dt = q.dtype
     qp, qs = _view(q, "q", (B, T, Hq, W))
     op, os_ = _view(out, "out", (B, T, Hq, L), dt)
     cp, pages, P, page_stride = _cache_view(cache, dt, W)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
+    rows, max_pages = _axes(block_table, "block_table", 2)
+    if rows != B:
         raise ValueError(f"block_table must be [{B}, max_pages]")
     wp, ws = _ws(workspace)
     _call("mtp_latent_attn", qp, qs[0], qs[1], qs[2], cp, pages, P, page_stride,
-          _vec(block_table, "block_table", _INT, _I32), block_table.shape[1],
+          _vec(block_table, "block_table", _INT, _I32), max_pages,
           _vec(kv_len, "kv_len", _INT, _I32, B), B, T, Hq, L, W - L, float(scale), op, os_[0], os_[1],
           os_[2], lse if lse is None else _vec(lse, "lse", _FLOAT, _F32, B * T * Hq), codes[dt], wp, ws,
           _arg(status, "status", _I32, 1, optional=True), _stream(stream))
@@ -499,18 +516,19 @@ def mtp_latent_prefill(q, kv, rot, cu_q, cu_k, out, scale: float, lse=None, stat
     the heads' shared rot[Tk, R], sequences bounded by cu_q and cu_k [B + 1] (see
     include/libmtpspec/latent.h)."""
     codes = _HALF_CODES or _half_codes()
-    Tq, Hq, D = q.shape
-    Tk, R = rot.shape
-    V = out.shape[-1]
+    Tq, Hq, D = _axes(q, "q", 3)
+    Tk, R = _axes(rot, "rot", 2)
+    V = _axes(out, "out", 3)[2]
     N = D - R
     dt = q.dtype
     qp, qs = _view(q, "q", (Tq, Hq, D))
     kp, ks = _view(kv, "kv", (Tk, Hq, N + V), dt)
     rp, rs = _view(rot, "rot", (Tk, R), dt)
     op, os_ = _view(out, "out", (Tq, Hq, V), dt)
+    cq = _vec(cu_q, "cu_q", _INT, _I32)
     B = cu_q.numel() - 1
     _call("mtp_latent_prefill", qp, qs[0], qs[1], kp, ks[0], ks[1], rp, rs[0],
-          _vec(cu_q, "cu_q", _INT, _I32, B + 1), _vec(cu_k, "cu_k", _INT, _I32, B + 1), B, Tq, Tk, Hq,
-          N, R, V, float(scale), op, os_[0], os_[1],
-          lse if lse is None else _vec(lse, "lse", _FLOAT, _F32, Tq * Hq), codes[dt], _arg(status, "status", _I32, 1, optional=True), _stream(stream))
+          cq, _vec(cu_k, "cu_k", _INT, _I32, B + 1), B, Tq, Tk, Hq, N, R, V, float(scale), op, os_[0],
+          os_[1], lse if lse is None else _vec(lse, "lse", _FLOAT, _F32, Tq * Hq), codes[dt],
+          _arg(status, "status", _I32, 1, optional=True), _stream(stream))
     return out
