@@ -13,7 +13,9 @@
  * R % 16 == 0; page_size a multiple of 8, up to 2^24.
  *
  * Strides are in elements, multiples of 8, and the last axis is contiguous; 16-bit arrays
- * are 16-byte aligned, whole numbers and floats 4-byte aligned.
+ * are 16-byte aligned, whole numbers and floats 4-byte aligned.  An output's axes may come in any
+ * order, but none of its elements may lie in two places: each stride is at least what the axes
+ * of smaller strides span.
  *
  * Cache entries and prompt tokens below a row's length are finite; whatever lies at or
  * beyond it (an unwritten part of a page, NaN and infinities among it) has no effect.

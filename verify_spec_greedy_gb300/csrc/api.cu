@@ -457,9 +457,25 @@ bool cache_sizes(int64_t num_pages, int32_t page_size, int64_t page_stride, int6
            page_stride >= static_cast<int64_t>(page_size) * row && page_stride <= kMaxStride &&
            page_stride % 8 == 0;
 }
-// A stride over `n` items of `item` elements each: 16-byte steps, and no overlap.
+// A stride over `n` items of `item` elements each: 16-byte steps, and no overlap along this axis.
 bool stride_ok(int64_t stride, int64_t n, int64_t item) {
     return stride % 8 == 0 && stride <= kMaxStride && (n <= 1 ? stride >= 0 : stride >= item);
+}
+// An output whose items of `item` elements lie along three axes: no item overlaps another, since
+// every axis steps over all that the axes of smaller strides span.  (Two writers of one element
+// would leave either's value.)
+bool apart(int64_t item, int64_t s0, int64_t n0, int64_t s1, int64_t n1, int64_t s2 = 0, int64_t n2 = 1) {
+    int64_t s[3] = {s0, s1, s2}, n[3] = {n0, n1, n2}, span = item;
+    for (int done = 0; done < 3; ++done) {
+        int k = -1;
+        for (int i = 0; i < 3; ++i)
+            if (n[i] > 1 && (k < 0 || s[i] < s[k])) k = i;
+        if (k < 0) break;
+        if (s[k] < span) return false;
+        span += s[k] * (n[k] - 1);
+        n[k] = 1;
+    }
+    return true;
 }
 
 }  // namespace
@@ -482,7 +498,8 @@ MTPSPEC_API int mtp_latent_append(
         if (!q_rot || !q_out) return MTPSPEC_ERR_ARG;
         if (Hq < 1 || Hq > kMaxHeads || !stride_ok(q_rot_head_stride, Hq, R) ||
             !stride_ok(q_out_head_stride, Hq, R) || !stride_ok(q_rot_tok_stride, T, R) ||
-            !stride_ok(q_out_tok_stride, T, R))
+            !stride_ok(q_out_tok_stride, T, R) ||
+            !apart(R, q_out_tok_stride, T, q_out_head_stride, Hq))
             return MTPSPEC_ERR_SHAPE;
     }
     if (!(eps >= 0.0f)) return MTPSPEC_ERR_ARG;
@@ -560,7 +577,8 @@ MTPSPEC_API int mtp_latent_attn(const void *q, int64_t q_row_stride, int64_t q_t
         return MTPSPEC_ERR_SHAPE;
     if (!stride_ok(q_row_stride, B, L + R) || !stride_ok(q_tok_stride, T, L + R) ||
         !stride_ok(q_head_stride, Hq, L + R) || !stride_ok(out_row_stride, B, L) ||
-        !stride_ok(out_tok_stride, T, L) || !stride_ok(out_head_stride, Hq, L))
+        !stride_ok(out_tok_stride, T, L) || !stride_ok(out_head_stride, Hq, L) ||
+        !apart(L, out_row_stride, B, out_tok_stride, T, out_head_stride, Hq))
         return MTPSPEC_ERR_SHAPE;
     if (!good_scale(scale)) return MTPSPEC_ERR_ARG;
     if (B == 0) return MTPSPEC_OK;
@@ -617,7 +635,7 @@ MTPSPEC_API int mtp_latent_prefill(const void *q, int64_t q_tok_stride, int64_t 
     if (!stride_ok(q_tok_stride, Tq, N + R) || !stride_ok(q_head_stride, Hq, N + R) ||
         !stride_ok(kv_tok_stride, Tk, N + V) || !stride_ok(kv_head_stride, Hq, N + V) ||
         !stride_ok(rot_stride, Tk, R) || !stride_ok(out_tok_stride, Tq, V) ||
-        !stride_ok(out_head_stride, Hq, V))
+        !stride_ok(out_head_stride, Hq, V) || !apart(V, out_tok_stride, Tq, out_head_stride, Hq))
         return MTPSPEC_ERR_SHAPE;
     if (!good_scale(scale)) return MTPSPEC_ERR_ARG;
     if (Tq == 0) return MTPSPEC_OK;
