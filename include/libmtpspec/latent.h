@@ -10,12 +10,13 @@
  * Rows are kept in pages: position n of row b is at block_table[b][n / page_size], offset
  * n % page_size.  Elements are 16 bits wide, bfloat16 or float16 (`dtype`), and every array
  * of a call has the same type.  64 <= L <= 512 with L % 64 == 0; 16 <= R <= 64 with
- * R % 16 == 0; page_size a multiple of 8, up to 2^24.
+ * R % 16 == 0; page_size a multiple of 8, up to 2^24; num_pages, max_pages and max_pos from 1
+ * to 2^31 - 1.
  *
- * Strides are in elements, multiples of 8, and the last axis is contiguous; 16-bit arrays
- * are 16-byte aligned, whole numbers and floats 4-byte aligned.  An output's axes may come in any
- * order, but none of its elements may lie in two places: each stride is at least what the axes
- * of smaller strides span.
+ * Strides are in elements, multiples of 8, below 2^39, and the last axis is contiguous; 16-bit
+ * arrays are 16-byte aligned, whole numbers and floats 4-byte aligned.  An output's axes may
+ * come in any order, but no two of its elements may share a place: each stride is at least what
+ * the axes of smaller strides span.
  *
  * Cache entries and prompt tokens below a row's length are finite; whatever lies at or
  * beyond it (an unwritten part of a page, NaN and infinities among it) has no effect.
@@ -96,8 +97,8 @@ int mtp_latent_append(const void *latent, int64_t latent_stride, const void *rot
  *   status int32 [1] or NULL: MTPSPEC_STATUS_BAD_PARAM is OR-ed in for a length out of range
  *         (taken as the nearest in range) or a page id out of range (its positions are read
  *         as zeros); MTPSPEC_STATUS_TIMEOUT if a wait gave up.
- * 0 <= B <= 2^20, 1 <= T <= 256, 1 <= Hq <= 1024, T * Hq <= 65536, scale finite and above 0.  Two
- * launches; the results do not depend on timing.
+ * 0 <= B <= 2^20, 1 <= T <= 256, 1 <= Hq <= 1024, T * Hq <= 65536, B * T * Hq <= 2^31 - 1, scale
+ * finite and above 0.  Two launches; the results do not depend on timing.
  */
 int mtp_latent_attn(const void *q, int64_t q_row_stride, int64_t q_tok_stride,
                     int64_t q_head_stride, const void *cache, int64_t num_pages,
@@ -131,9 +132,8 @@ size_t mtp_latent_attn_workspace_bytes(int64_t B, int32_t T, int32_t Hq, int32_t
  *        or out of order (taken as the nearest good one: in range, and not below the bounds
  *        before it); MTPSPEC_STATUS_TIMEOUT if a wait gave up.
  * N and V are 64 or 128; 16 <= R <= 64 with R % 16 == 0; 0 <= Tq, Tk <= 2^24 (Tk >= 1 when
- * Tq > 0), 1 <= B <= 65536, 1 <= Hq <= 1024, scale finite and above
- * 0.  Queries outside every sequence
- * are not written.  One launch.
+ * Tq > 0), 1 <= B <= 65536, 1 <= Hq <= 1024, scale finite and above 0.  Queries outside every
+ * sequence are not written.  One launch.
  */
 int mtp_latent_prefill(const void *q, int64_t q_tok_stride, int64_t q_head_stride,
                        const void *kv, int64_t kv_tok_stride, int64_t kv_head_stride,
