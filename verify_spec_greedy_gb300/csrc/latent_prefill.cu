@@ -400,7 +400,167 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
 
     if (sh.item[0].w.pair < 0) {
         // nothing: the grid has a CTA for every pair that there might be
-    } else if (warp < 4) {
+    } else if (warp >= 4) {
+        // (Sixteen of twenty warps run this, so it comes before the other roles in the code: behind
+        // them 900 and 1000 queries x 16 heads behind 7001 keys took 139 us, not 133.6, and 8192 x 32
+        // heads 490, not 477, whenever the roles before it had grown.)
+        // ---- softmax: two threads a row, 64 of a tile's 128 keys each.  (With one thread a row
+        // the chain scores - weights - products of a tile took longer than the tensor cores
+        // need for both tiles.)
+        const int t = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, r = (warp & 3) * 32 + lane;
+        const uint32_t lane_bits = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t s_t = tmem + lane_bits + S_COL + t * 128, o_t = tmem + lane_bits + O_COL + t * 128;
+        const int pair_bar = 1 + t * 4 + (warp & 3);
+        // this thread's value for the row's other thread, and the other's
+        const auto swap = [&](float v) {
+            sh.other[t][half][r] = v;
+            asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+            return sh.other[t][half ^ 1][r];
+        };
+        for (uint32_t item = 0;; ++item) {
+            // (what only the pair's end needs stays in shared memory meanwhile)
+            const volatile Item &my = sh.item[item & 1];
+            int nt, tail, limit;  // limit: keys that this row sees
+            {
+                const Work w = {0, my.w.nq, 0, my.w.nk, my.w.pair, 0};
+                const Extent e(w);
+                nt = e.tiles(t);
+                tail = e.last() == t ? e.tail() : -1;  // the tile whose values are to be cleared
+                limit = e.row0 + t * TM + r + w.nk - w.nq + 1;
+            }
+            uint32_t parity = my.met[t] & 1;
+            float m_ref = -INFINITY, l = 0.0f;
+            for (int j = 0; j < nt; ++j) {
+                wait_long(sh, &sh.s_full[t], parity);
+                parity ^= 1;
+                tc_fence_after();
+                uint32_t x[2][32];
+                tmem_ld32(s_t + half * 64, x[0]);
+                tmem_ld32(s_t + half * 64 + 32, x[1]);
+                if (__builtin_expect(j == tail, 0)) {
+                    // value rows behind the sequence's last key: whatever follows there must not
+                    // meet the zero weights.  (The barrier's fill before this one is used up by
+                    // now, so the phase is this fill's.)
+                    const uint32_t g = my.g0 + tail;
+                    wait(sh, &sh.v_full[g & 1], (g >> 1) & 1);
+                    const int z0 = my.w.nk - tail * TN, first = my.slot0 + (tail % Z::SLOTS) * Z::TILE;
+#pragma unroll
+                    for (int c = KC; c < KC + VC; ++c) {
+                        const uint32_t v = ring + (first + c) % Z::SLOTS * CHUNK + z0 * 128;
+                        for (int i = half * 128 + r; i < (TN - z0) * 8; i += 256)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + i * 16), "r"(0)
+                                         : "memory");
+                    }
+                    fence_async_smem();
+                    mbar_arrive(&sh.v_clean);
+                }
+                tmem_wait_ld();
+                if (__builtin_expect(j * TN + TN > limit - r, 0)) {  // more than every row sees
+                    const int seen = limit - j * TN - half * 64;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        if (i >= seen) x[0][i] = 0xFF800000u;
+                        if (i + 32 >= seen) x[1][i] = 0xFF800000u;
+                    }
+                }
+                float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    top4[i & 3] = max3(top4[i & 3], __uint_as_float(x[0][i]), __uint_as_float(x[1][i]));
+                const float mine = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
+                // (the second barrier of a tile is p_ready: nobody writes the next value before
+                // the products have taken both threads' weights)
+                const float top = fmaxf(mine, swap(mine)) * p.scale2;
+                const bool raise = top > m_ref + (LAZY + T::first_weight);
+                const float m_new = top - T::first_weight;
+                if (__builtin_expect(j > 0 && __any_sync(0xFFFFFFFFu, raise), 0)) {
+                    // the scores came after the products of the tile before: the output is free
+                    const float f = raise ? ex2(m_ref - m_new) : 1.0f;
+                    l *= f;
+#pragma unroll
+                    for (int c = half * (VC * 32); c < (half + 1) * (VC * 32); c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(o_t + c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st16(o_t + c, o);
+                    }
+                }
+                if (raise) m_ref = m_new;
+                const float m_use = m_ref == -INFINITY ? 0.0f : m_ref;
+                const uint64_t scale_2 = pack2(p.scale2, p.scale2), minus_m = pack2(-m_use, -m_use);
+                uint64_t part[2] = {0, 0};  // two pairs of sums
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float e0, e1;
+                        unpack2(fma2(pack2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])),
+                                     scale_2, minus_m), e0, e1);
+                        e0 = ex2(e0);
+                        e1 = ex2(e1);
+                        part[i & 1] = add2(part[i & 1], pack2(e0, e1));
+                        w[i] = T::narrow2(e0, e1);
+                    }
+                    tmem_st16(s_t + half * 32 + 16 * c, w);
+                }
+                tmem_wait_st();
+                float l0, l1;
+                unpack2(add2(part[0], part[1]), l0, l1);
+                l += l0 + l1;
+                tc_fence_before();
+                mbar_arrive(&sh.p_ready[t]);
+            }
+            if (nt > 0) {
+                wait_long(sh, &sh.o_done[t], my.outputs[t] & 1);
+                tc_fence_after();
+            }
+            l += swap(l);
+            const int row = my.w.pair * 2 * TM + t * TM + r, head = my.w.head;
+            const bool real = row < my.w.nq;
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // (zero: nothing was seen; NaN stays)
+            const int64_t tok = my.w.q0 + row;
+            if (real && half == 0 && p.lse)
+                p.lse[tok * p.Hq + head] = l == 0.0f ? -INFINITY : (m_ref + log2f(l)) * LN2;
+            uint16_t *dst = p.out + tok * p.out_tok + head * p.out_head + half * (VC * 32);
+            // 32 bytes a store, a whole sector, where the rows allow it
+            const bool sectors = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
+#pragma unroll
+            for (int c = 0; c < VC; ++c) {
+                uint32_t o[32] = {};
+                if (nt > 0) {
+                    tmem_ld32(o_t + half * (VC * 32) + 32 * c, o);
+                    tmem_wait_ld();
+                }
+                if (!real) continue;
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    uint32_t y[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        y[u] = nt > 0 ? T::narrow2(__uint_as_float(o[16 * v + 2 * u]) * inv,
+                                                   __uint_as_float(o[16 * v + 2 * u + 1]) * inv)
+                                      : 0u;
+                    uint16_t *d = dst + c * 32 + v * 16;
+                    if (sectors) {
+                        st_global_32B(d, y);
+                    } else {
+                        *reinterpret_cast<uint4 *>(d) = make_uint4(y[0], y[1], y[2], y[3]);
+                        *reinterpret_cast<uint4 *>(d + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+                    }
+                }
+            }
+            // The next pair's products overwrite this output once its first weights are there,
+            // which come after these reads.
+            tc_fence_before();
+            __syncwarp();  // the whole warp is done with the item
+            if (lane == 0) mbar_arrive(&sh.item_free[item & 1]);
+            const bool more = __all_sync(0xFFFFFFFFu, next_item(item));
+            if (!both(sh.go[t][warp & 3], half, more, pair_bar)) break;
+        }
+    } else {
         if (warp == 0) {
             if (elect_one()) {
                 // ---- producer
@@ -626,163 +786,6 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 }
                 __syncwarp();
             }
-        }
-    } else {
-        // ---- softmax: two threads a row, 64 of a tile's 128 keys each.  (With one thread a row
-        // the chain scores - weights - products of a tile took longer than the tensor cores
-        // need for both tiles.)
-        const int t = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, r = (warp & 3) * 32 + lane;
-        const uint32_t lane_bits = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t s_t = tmem + lane_bits + S_COL + t * 128, o_t = tmem + lane_bits + O_COL + t * 128;
-        const int pair_bar = 1 + t * 4 + (warp & 3);
-        // this thread's value for the row's other thread, and the other's
-        const auto swap = [&](float v) {
-            sh.other[t][half][r] = v;
-            asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
-            return sh.other[t][half ^ 1][r];
-        };
-        for (uint32_t item = 0;; ++item) {
-            // (what only the pair's end needs stays in shared memory meanwhile)
-            const volatile Item &my = sh.item[item & 1];
-            int nt, tail, limit;  // limit: keys that this row sees
-            {
-                const Work w = {0, my.w.nq, 0, my.w.nk, my.w.pair, 0};
-                const Extent e(w);
-                nt = e.tiles(t);
-                tail = e.last() == t ? e.tail() : -1;  // the tile whose values are to be cleared
-                limit = e.row0 + t * TM + r + w.nk - w.nq + 1;
-            }
-            uint32_t parity = my.met[t] & 1;
-            float m_ref = -INFINITY, l = 0.0f;
-            for (int j = 0; j < nt; ++j) {
-                wait_long(sh, &sh.s_full[t], parity);
-                parity ^= 1;
-                tc_fence_after();
-                uint32_t x[2][32];
-                tmem_ld32(s_t + half * 64, x[0]);
-                tmem_ld32(s_t + half * 64 + 32, x[1]);
-                if (__builtin_expect(j == tail, 0)) {
-                    // value rows behind the sequence's last key: whatever follows there must not
-                    // meet the zero weights.  (The barrier's fill before this one is used up by
-                    // now, so the phase is this fill's.)
-                    const uint32_t g = my.g0 + tail;
-                    wait(sh, &sh.v_full[g & 1], (g >> 1) & 1);
-                    const int z0 = my.w.nk - tail * TN, first = my.slot0 + (tail % Z::SLOTS) * Z::TILE;
-#pragma unroll
-                    for (int c = KC; c < KC + VC; ++c) {
-                        const uint32_t v = ring + (first + c) % Z::SLOTS * CHUNK + z0 * 128;
-                        for (int i = half * 128 + r; i < (TN - z0) * 8; i += 256)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + i * 16), "r"(0)
-                                         : "memory");
-                    }
-                    fence_async_smem();
-                    mbar_arrive(&sh.v_clean);
-                }
-                tmem_wait_ld();
-                if (__builtin_expect(j * TN + TN > limit - r, 0)) {  // more than every row sees
-                    const int seen = limit - j * TN - half * 64;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        if (i >= seen) x[0][i] = 0xFF800000u;
-                        if (i + 32 >= seen) x[1][i] = 0xFF800000u;
-                    }
-                }
-                float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    top4[i & 3] = max3(top4[i & 3], __uint_as_float(x[0][i]), __uint_as_float(x[1][i]));
-                const float mine = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
-                // (the second barrier of a tile is p_ready: nobody writes the next value before
-                // the products have taken both threads' weights)
-                const float top = fmaxf(mine, swap(mine)) * p.scale2;
-                const bool raise = top > m_ref + (LAZY + T::first_weight);
-                const float m_new = top - T::first_weight;
-                if (__builtin_expect(j > 0 && __any_sync(0xFFFFFFFFu, raise), 0)) {
-                    // the scores came after the products of the tile before: the output is free
-                    const float f = raise ? ex2(m_ref - m_new) : 1.0f;
-                    l *= f;
-#pragma unroll
-                    for (int c = half * (VC * 32); c < (half + 1) * (VC * 32); c += 16) {
-                        uint32_t o[16];
-                        tmem_ld16(o_t + c, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        tmem_st16(o_t + c, o);
-                    }
-                }
-                if (raise) m_ref = m_new;
-                const float m_use = m_ref == -INFINITY ? 0.0f : m_ref;
-                const uint64_t scale_2 = pack2(p.scale2, p.scale2), minus_m = pack2(-m_use, -m_use);
-                uint64_t part[2] = {0, 0};  // two pairs of sums
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float e0, e1;
-                        unpack2(fma2(pack2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])),
-                                     scale_2, minus_m), e0, e1);
-                        e0 = ex2(e0);
-                        e1 = ex2(e1);
-                        part[i & 1] = add2(part[i & 1], pack2(e0, e1));
-                        w[i] = T::narrow2(e0, e1);
-                    }
-                    tmem_st16(s_t + half * 32 + 16 * c, w);
-                }
-                tmem_wait_st();
-                float l0, l1;
-                unpack2(add2(part[0], part[1]), l0, l1);
-                l += l0 + l1;
-                tc_fence_before();
-                mbar_arrive(&sh.p_ready[t]);
-            }
-            if (nt > 0) {
-                wait_long(sh, &sh.o_done[t], my.outputs[t] & 1);
-                tc_fence_after();
-            }
-            l += swap(l);
-            const int row = my.w.pair * 2 * TM + t * TM + r, head = my.w.head;
-            const bool real = row < my.w.nq;
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // (zero: nothing was seen; NaN stays)
-            const int64_t tok = my.w.q0 + row;
-            if (real && half == 0 && p.lse)
-                p.lse[tok * p.Hq + head] = l == 0.0f ? -INFINITY : (m_ref + log2f(l)) * LN2;
-            uint16_t *dst = p.out + tok * p.out_tok + head * p.out_head + half * (VC * 32);
-            // 32 bytes a store, a whole sector, where the rows allow it
-            const bool sectors = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
-#pragma unroll
-            for (int c = 0; c < VC; ++c) {
-                uint32_t o[32] = {};
-                if (nt > 0) {
-                    tmem_ld32(o_t + half * (VC * 32) + 32 * c, o);
-                    tmem_wait_ld();
-                }
-                if (!real) continue;
-#pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    uint32_t y[8];
-#pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        y[u] = nt > 0 ? T::narrow2(__uint_as_float(o[16 * v + 2 * u]) * inv,
-                                                   __uint_as_float(o[16 * v + 2 * u + 1]) * inv)
-                                      : 0u;
-                    uint16_t *d = dst + c * 32 + v * 16;
-                    if (sectors) {
-                        st_global_32B(d, y);
-                    } else {
-                        *reinterpret_cast<uint4 *>(d) = make_uint4(y[0], y[1], y[2], y[3]);
-                        *reinterpret_cast<uint4 *>(d + 8) = make_uint4(y[4], y[5], y[6], y[7]);
-                    }
-                }
-            }
-            // The next pair's products overwrite this output once its first weights are there,
-            // which come after these reads.
-            tc_fence_before();
-            __syncwarp();  // the whole warp is done with the item
-            if (lane == 0) mbar_arrive(&sh.item_free[item & 1]);
-            const bool more = __all_sync(0xFFFFFFFFu, next_item(item));
-            if (!both(sh.go[t][warp & 3], half, more, pair_bar)) break;
         }
     }
     tc_fence_before();
