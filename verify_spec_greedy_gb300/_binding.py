@@ -381,19 +381,15 @@ def _half_codes():
     return _HALF_CODES
 
 
-def _axes(t, name, n):
-    """The sizes of a tensor of n axes."""
-    try:
-        s = t.shape
-        if len(s) == n:
-            return s
-    except (AttributeError, TypeError):
-        pass
-    if t is None:
-        raise ValueError(f"{name} is required")
-    if not isinstance(t, _kinds()["tensor"]):
-        raise TypeError(f"{name} must be a torch tensor")
-    raise ValueError(f"{name} must have {n} axes, got shape {tuple(t.shape)}")
+def _refuse_axes(**tensors):
+    """The message for the first of the (tensor, number of axes) that is not as it should be."""
+    for name, (t, n) in tensors.items():
+        if t is None:
+            raise ValueError(f"{name} is required")
+        if not isinstance(t, _kinds()["tensor"]):
+            raise TypeError(f"{name} must be a torch tensor")
+        if t.dim() != n:
+            raise ValueError(f"{name} must have {n} axes, got shape {tuple(t.shape)}")
 
 
 def _view(t, name, shape, like=None):
@@ -436,13 +432,12 @@ def _vec(t, name, dtype, kind, numel=0):
     return _arg(t, name, kind, numel)
 
 
-def _cache_view(cache, like, W):
-    """(pointer, pages, page size, page stride) of a paged cache [pages, page_size, W]."""
-    n, P, _ = _axes(cache, "cache", 3)
+def _cache_view(cache, n, P, like, W):
+    """(pointer, page stride) of a paged cache [n pages, page size P, W]."""
     ptr, st = _view(cache, "cache", (n, P, W), like)
     if P > 1 and st[1] != W:
         raise ValueError("the rows of a cache page must be contiguous")
-    return ptr, n, P, st[0] if n > 1 else P * W
+    return ptr, st[0] if n > 1 else P * W
 
 
 def mtp_latent_append(latent, rot, cos_sin, tok_row, positions, block_table, cache, norm_w=None,
@@ -453,21 +448,29 @@ def mtp_latent_append(latent, rot, cos_sin, tok_row, positions, block_table, cac
     include/libmtpspec/latent.h).  Row strides, and token and head strides, may be any
     multiple of 8 elements."""
     codes = _HALF_CODES or _half_codes()
-    T, L = _axes(latent, "latent", 2)
-    R = _axes(rot, "rot", 2)[1]
+    queries = (None, 0, 0, None, 0, 0, 0)
+    Hq = 0
+    try:
+        T, L = latent.shape
+        _, R = rot.shape
+        max_pos, angles = cos_sin.shape
+        B, max_pages = block_table.shape
+        pages, P, _ = cache.shape
+        if q_rot is not None:
+            _, Hq, _ = q_rot.shape
+    except (AttributeError, TypeError, ValueError):
+        _refuse_axes(latent=(latent, 2), rot=(rot, 2), cos_sin=(cos_sin, 2), block_table=(block_table, 2),
+                     cache=(cache, 3), q_rot=(q_rot, 3))
+        raise
     dt = latent.dtype
-    B, max_pages = _axes(block_table, "block_table", 2)
     lp, ls = _view(latent, "latent", (T, L))
     rp, rs = _view(rot, "rot", (T, R), dt)
-    cp, pages, P, page_stride = _cache_view(cache, dt, L + R)
-    max_pos, angles = _axes(cos_sin, "cos_sin", 2)
+    cp, page_stride = _cache_view(cache, pages, P, dt, L + R)
     if angles != R:
         raise ValueError(f"cos_sin must be [max_pos, {R}]")
-    queries = (None, 0, 0, None, 0, 0, 0)
     if q_rot is not None or q_out is not None:
         if q_rot is None or q_out is None:
             raise ValueError("q_rot and q_out go together")
-        Hq = _axes(q_rot, "q_rot", 3)[1]
         qp, qs = _view(q_rot, "q_rot", (T, Hq, R), dt)
         op, os_ = _view(q_out, "q_out", (T, Hq, R), dt)
         queries = (qp, qs[0], qs[1], op, os_[0], os_[1], Hq)
@@ -492,13 +495,18 @@ def mtp_latent_attn(q, cache, block_table, kv_len, out, scale: float, lse=None, 
     """out[B, T, Hq, L]: attention of q[B, T, Hq, L + R] over the paged cache, query t of row b
     seeing positions below kv_len[b] - (T - 1 - t) (see include/libmtpspec/latent.h)."""
     codes = _HALF_CODES or _half_codes()
-    B, T, Hq, W = _axes(q, "q", 4)
-    L = _axes(out, "out", 4)[3]
+    try:
+        B, T, Hq, W = q.shape
+        _, _, _, L = out.shape
+        pages, P, _ = cache.shape
+        rows, max_pages = block_table.shape
+    except (AttributeError, TypeError, ValueError):
+        _refuse_axes(q=(q, 4), cache=(cache, 3), block_table=(block_table, 2), out=(out, 4))
+        raise
     dt = q.dtype
     qp, qs = _view(q, "q", (B, T, Hq, W))
     op, os_ = _view(out, "out", (B, T, Hq, L), dt)
-    cp, pages, P, page_stride = _cache_view(cache, dt, W)
-    rows, max_pages = _axes(block_table, "block_table", 2)
+    cp, page_stride = _cache_view(cache, pages, P, dt, W)
     if rows != B:
         raise ValueError(f"block_table must be [{B}, max_pages]")
     wp, ws = _ws(workspace)
@@ -516,9 +524,13 @@ def mtp_latent_prefill(q, kv, rot, cu_q, cu_k, out, scale: float, lse=None, stat
     the heads' shared rot[Tk, R], sequences bounded by cu_q and cu_k [B + 1] (see
     include/libmtpspec/latent.h)."""
     codes = _HALF_CODES or _half_codes()
-    Tq, Hq, D = _axes(q, "q", 3)
-    Tk, R = _axes(rot, "rot", 2)
-    V = _axes(out, "out", 3)[2]
+    try:
+        Tq, Hq, D = q.shape
+        Tk, R = rot.shape
+        _, _, V = out.shape
+    except (AttributeError, TypeError, ValueError):
+        _refuse_axes(q=(q, 3), rot=(rot, 2), out=(out, 3))
+        raise
     N = D - R
     dt = q.dtype
     qp, qs = _view(q, "q", (Tq, Hq, D))
