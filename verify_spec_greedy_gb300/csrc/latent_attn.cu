@@ -25,13 +25,13 @@
 //   64 rows a sequence (256 x 500-4000 keys, 725 MB): 148 us, 4.9 TB/s, 0.73 of the copy rate.
 //     Counters: DRAM 67 %, tensor pipe 24 %, shared memory of the products 40 %.  The rest is
 //     the ends of units, 6,000 cycles each for outputs of 64 rows x 512, and start and join.
-//   256 rows a sequence (64 x 1000-8000 keys, 170 GFLOP): 213 us, 0.80 PFLOP/s, 0.41.  A tile
+//   256 rows a sequence (64 x 1000-8000 keys, 170 GFLOP): 216 us, 0.79 PFLOP/s, 0.41.  A tile
 //     takes some 2,750 cycles, 1,792 of them products at the rate of 64-row accumulators,
 //     which is set by shared memory (every 16-column step reads 2 KB of queries or weights
 //     beside the keys); the keys' arrival and the softmax between the two products take the
 //     rest, since a third tile does not fit.
-//   168 rows, 100k keys, one sequence: 63 us; as the last, and each row has 50 parts to join.
-//   One row of 600 keys: 11.6 us; 8 x 2k keys, 64 rows: 18 us: two launches and one tile's way
+//   168 rows, 100k keys, one sequence: 65 us; as the last, and each row has 50 parts to join.
+//   One row of 600 keys: 12 us; 8 x 2k keys, 64 rows: 21 us: two launches and one tile's way
 //     from page table to output.
 #include <algorithm>
 

@@ -18,15 +18,20 @@
 // to load takes over a pair whose CTA has not started.
 //
 // What bounds it (bf16, N = V = 128, R = 64; products 1938 TFLOP/s measured): 8192 tokens x 32
-// heads, 687 GFLOP: 442 us, 1.55 PFLOP/s, 0.80; counters: tensor pipe 65 %, shared memory of the
-// products 52 %, exponentials 27 %, DRAM 18 %.  A round of both tiles takes some 3,500 cycles
+// heads, 687 GFLOP: 477-490 us when called on and on, at the 1815 MHz that the power limit leaves
+// (1390 W of 1400), 1.42 PFLOP/s, 0.73; 444 us in the first milliseconds after a pause, at some
+// 1900-2070 MHz, 0.80.  Counters: tensor pipe 66 %, shared memory of the products 52 %,
+// exponentials 27 %, DRAM 18 %.  A round of both tiles takes some 3,500 cycles
 // for 2,560 of products: the chain scores - softmax - products of a tile is longer than the
 // other tile's products, and a third tile has no tensor memory.  Splitting the chain (first
 // half of the weights handed over early) cost more in barriers than it gave: 439 -> 476 us.
 // 8 prompts of 77-1500 tokens x 32 heads, 61 GFLOP: 85 us, 0.71 PFLOP/s: the last softmax and
-// the output of a pair are not covered by anything (tensor pipe 36 %).  Two chunks of 900 and
-// 1000 queries x 16 heads behind 7001 keys: 130 us, 1.14 PFLOP/s: 128 pairs, 24 of the 152
-// multiprocessors have none.  300 tokens x 16 heads: 12.3 us, the way from launch to output.
+// the output of a pair are not covered by anything (tensor pipe 34 %), and tiles on the diagonal
+// and at the ends are computed whole, 1.27 times the visible products.  Two chunks of 900 and
+// 1000 queries x 16 heads behind 7001 keys: 129-135 us, 1.11-1.14 PFLOP/s: 128 pairs, 24 of the 152
+// multiprocessors have none.  300 tokens x 16 heads: 12 us, the way from launch to output.
+//
+// Registers: 640 threads leave 96 a thread, and each instance spills 40 to 52 bytes a thread.
 #include <algorithm>
 
 #include "half_types.cuh"
@@ -110,8 +115,8 @@ __device__ __forceinline__ bool wait_long(Shared &sh, uint64_t *bar, uint32_t pa
     return false;
 }
 
-// And for one that may take as long as a whole pair, or as the last CTAs' number gives requests, on
-// others whose own waits are bounded.
+// And for one on others whose own waits are bounded, which may take as long as a whole pair, or as
+// the requests for all CTAs that have no work.
 __device__ __forceinline__ bool wait_far(Shared &sh, uint64_t *bar, uint32_t parity,
                                         uint32_t limit = 16 * WAIT_LIMIT) {
     for (uint32_t it = 0; it < limit; ++it) {
