@@ -178,8 +178,8 @@ __host__ __device__ constexpr uint32_t idesc_of(int n, bool b_rows_k) {
 
 __device__ __forceinline__ int pairs_of(int queries) { return (queries + 2 * TM - 1) / (2 * TM); }
 
-// A lane's run of sequences b0 .. b1 - 1: the largest bounds before its first, the pairs before
-// it and its own.
+// A lane's run of sequences b0 .. b1 - 1: the largest bounds before its first (0 when all bounds
+// are in range and in order, as they should be), the pairs before it and its own.
 struct Run {
     int b0, b1, q_before, k_before, at, sum;
 };
@@ -316,26 +316,36 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         const int per = (p.B + 31) / 32;
         run.b0 = min(p.B, lane * per);
         run.b1 = min(p.B, run.b0 + per);
-        int q = 0, k = 0;  // the largest bounds up to and with this run's
+        int q0 = p.cu_q[run.b0], k0 = p.cu_k[run.b0];
+        bool good = q0 >= 0 && k0 >= 0 && q0 <= p.Tq && k0 <= p.Tk;
         for (int b = run.b0; b < run.b1; ++b) {
-            q = bound(p.cu_q, b, p.Tq, q);
-            k = bound(p.cu_k, b, p.Tk, k);
+            const int q1 = p.cu_q[b + 1], k1 = p.cu_k[b + 1];
+            good &= q1 >= q0 && k1 >= k0 && q1 <= p.Tq && k1 <= p.Tk;
+            if (good) run.sum += pairs_of(q1 - q0);
+            q0 = q1;
+            k0 = k1;
         }
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {  // (lanes without one to their left get their own)
-            q = max(q, __shfl_up_sync(0xFFFFFFFFu, q, o));
-            k = max(k, __shfl_up_sync(0xFFFFFFFFu, k, o));
-        }
-        q = __shfl_up_sync(0xFFFFFFFFu, q, 1);
-        k = __shfl_up_sync(0xFFFFFFFFu, k, 1);
-        run.q_before = lane > 0 ? q : 0;
-        run.k_before = lane > 0 ? k : 0;
-        if (run.b0 < run.b1) {
-            int q0 = bound(p.cu_q, run.b0, p.Tq, run.q_before);
+        if (!__all_sync(0xFFFFFFFFu, good)) {  // each bound counts as the largest up to it
+            if (blockIdx.x == 0 && lane == 0 && p.status) atomicOr(p.status, MTPSPEC_STATUS_BAD_PARAM);
+            int q = 0, k = 0;
             for (int b = run.b0; b < run.b1; ++b) {
-                const int q1 = bound(p.cu_q, b + 1, p.Tq, q0);
-                run.sum += pairs_of(q1 - q0);
-                q0 = q1;
+                q = bound(p.cu_q, b, p.Tq, q);
+                k = bound(p.cu_k, b, p.Tk, k);
+            }
+            for (int o = 1; o < 32; o <<= 1) {  // (lanes without one to their left get their own)
+                q = max(q, __shfl_up_sync(0xFFFFFFFFu, q, o));
+                k = max(k, __shfl_up_sync(0xFFFFFFFFu, k, o));
+            }
+            q = __shfl_up_sync(0xFFFFFFFFu, q, 1);
+            k = __shfl_up_sync(0xFFFFFFFFu, k, 1);
+            run.q_before = lane > 0 ? q : 0;
+            run.k_before = lane > 0 ? k : 0;
+            run.sum = 0;
+            q = bound(p.cu_q, run.b0, p.Tq, run.q_before);
+            for (int b = run.b0; b < run.b1; ++b) {
+                const int q1 = bound(p.cu_q, b + 1, p.Tq, q);
+                run.sum += pairs_of(q1 - q);
+                q = q1;
             }
         }
         run.at = run.sum;
@@ -348,17 +358,6 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         run.at -= run.sum;
         const Work w = work_of(blockIdx.x);
         if (lane == 0) sh.item[0] = Item{w, 0, 0, {0, 0}, {0, 0}};
-        if (blockIdx.x == 0 && p.status) {
-            bool bad = false;
-            int q0 = run.q_before, k0 = run.k_before;
-            // (a run looks at its own bounds, and the last one at the end of all)
-            for (int b = run.b0; b < run.b1 + (run.b1 == p.B && run.b0 < run.b1); ++b) {
-                q0 = bound(p.cu_q, b, p.Tq, q0);
-                k0 = bound(p.cu_k, b, p.Tk, k0);
-                bad |= q0 != p.cu_q[b] || k0 != p.cu_k[b];
-            }
-            if (bad) atomicOr(p.status, MTPSPEC_STATUS_BAD_PARAM);
-        }
     }
     if (threadIdx.x == 0) {
         for (int t = 0; t < 2; ++t) {
