@@ -89,7 +89,6 @@ struct __align__(16) Shared {
     uint32_t tmem;
     volatile int abort;
     float other[2][2][TM];  // what the two threads of a row tell each other, by tile and half
-    volatile int go[2][4][2];  // and their warps, by tile, rows and half: is there a next item?
 };
 constexpr int SMEM_EXTRA = static_cast<int>(sizeof(Shared));
 
@@ -127,13 +126,20 @@ __device__ __forceinline__ bool wait_far(Shared &sh, uint64_t *bar, uint32_t par
     return false;
 }
 
-// Whether both warps of a row's halves say yes.  They meet at barrier `bar` in everything they
-// do, so that after a wait that gave up neither may go on without the other; and they meet there
-// once more before the next question.
-__device__ __forceinline__ bool both(volatile int (&said)[2], int half, bool yes, int bar) {
-    if ((threadIdx.x & 31) == 0) said[half] = yes;
-    asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
-    return said[0] && said[1];
+// Whether all of two warps that share rows say yes.  They meet at barrier `bar` in everything they
+// do, so that after a wait that gave up none may go on without the others.
+__device__ __forceinline__ bool both(bool yes, int bar) {
+    uint32_t all;
+    __syncwarp();
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %2, 0;\n\t"
+        "bar.red.and.pred p, %1, 64, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(all)
+        : "r"(bar), "r"(static_cast<uint32_t>(yes))
+        : "memory");
+    return all != 0;
 }
 
 // The bounded wait of a CTA that leaves, whatever the abort flag says.
@@ -561,8 +567,7 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             tc_fence_before();
             __syncwarp();  // the whole warp is done with the item
             if (lane == 0) mbar_arrive(&sh.item_free[item & 1]);
-            const bool more = __all_sync(0xFFFFFFFFu, next_item(item));
-            if (!both(sh.go[t][warp & 3], half, more, pair_bar)) break;
+            if (!both(next_item(item), pair_bar)) break;
         }
     } else {
         if (warp == 0) {
@@ -768,11 +773,12 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                     if (it.w.pair >= 0) break;
                 }
                 if (!there) break;
-                // the item before this slot's last is left behind by all
-                if (item > 0 && !__all_sync(0xFFFFFFFFu, wait_long(sh, &sh.item_free[(item - 1) & 1],
-                                                                   ((item - 1) >> 1) & 1)))
+                // the item before this slot's last is left behind by all (and there is no more work
+                // for a CTA that leaves)
+                if (!__all_sync(0xFFFFFFFFu, (item == 0 || wait_long(sh, &sh.item_free[(item - 1) & 1],
+                                                                     ((item - 1) >> 1) & 1)) &&
+                                                 !sh.abort))
                     break;
-                if (__any_sync(0xFFFFFFFFu, sh.abort)) break;  // no more work for a CTA that leaves
                 if (lane == 0) {
                     sh.item[(item + 1) & 1] = it;
                     mbar_arrive(&sh.item_full[(item + 1) & 1]);
@@ -826,7 +832,7 @@ __global__ void k_wait_selftest(uint32_t limit, int32_t *status) {
             const int half = threadIdx.x >> 5;
             const bool there = wait_far(sh, half ? never : done, 0, limit);
             ok &= there == (half == 0);
-            got = both(sh.go[0][0], half, __all_sync(0xFFFFFFFFu, there), 1);
+            got = both(there, 1);
         } else {
             got = form == 0 ? wait(sh, never, 0, limit)
                   : form == 1 ? wait_long(sh, never, 0, limit) : wait_far(sh, never, 0, limit);
