@@ -31,7 +31,7 @@
 // 1000 queries x 16 heads behind 7001 keys: 129-135 us, 1.11-1.14 PFLOP/s: 128 pairs, 24 of the 152
 // multiprocessors have none.  300 tokens x 16 heads: 12 us, the way from launch to output.
 //
-// Registers: 640 threads leave 96 a thread, and each instance spills 40 to 52 bytes a thread.
+// Registers: 640 threads leave 96 a thread, and each instance spills 48 or 52 bytes a thread.
 #include <algorithm>
 
 #include "half_types.cuh"
