@@ -404,5 +404,9 @@ uint64_t mtpspec_launch_count(void);
 
 /* The draft head's latent attention: mtp_latent_append, mtp_latent_attn, mtp_latent_prefill. */
 #include "libmtpspec/latent.h"
+/* The same with grouped heads: mtp_heads_append, mtp_heads_attn. */
+#include "libmtpspec/heads.h"
+/* The pages of either cache: mtp_pages_resize, mtp_pages_fork, mtp_pages_compact, mtp_pages_copy. */
+#include "libmtpspec/pages.h"
 
 #endif /* LIBMTPSPEC_H */

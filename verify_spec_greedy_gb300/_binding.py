@@ -18,6 +18,7 @@ F32, BF16, F16 = 0, 1, 2
 STATUS_BAD_DRAFT_ID = 0x1
 STATUS_BAD_PARAM = 0x2
 STATUS_TIMEOUT = 0x4
+STATUS_NO_PAGES = 0x8
 
 _lib = None
 
@@ -66,6 +67,16 @@ def load():
         "mtp_latent_attn_workspace_bytes": ([i64, i32, i32, i32, i32], sz),
         "mtp_latent_prefill": ([p, i64, i64, p, i64, i64, p, i64, p, p, i64, i64, i64, i32, i32, i32,
                                 i32, f32, p, i64, i64, p, C.c_int, p, p], C.c_int),
+        "mtp_heads_append": ([p, i64, i64, p, i64, i64, p, p, i64, i32, i32, p, p, i64, i32, i32, p, i64,
+                              i64, p, p, i64, i32, i64, i64, i64, p, i64, i64, p, p, i64, i64, i32, f32,
+                              C.c_int, p, p], C.c_int),
+        "mtp_heads_attn": ([p, i64, i64, p, p, i64, i32, i64, i64, i64, p, i64, p, p, i64, i64, i32, i32,
+                            i32, i32, i32, f32, p, i64, i64, p, C.c_int, p, sz, p, p], C.c_int),
+        "mtp_heads_attn_workspace_bytes": ([i64, i64, i32, i32, i32], sz),
+        "mtp_pages_resize": ([p, p, p, p, p, i64, i64, i64, i32, p, p, p], C.c_int),
+        "mtp_pages_fork": ([p, p, i64, p, p, p, i64, i64, i64, p, p], C.c_int),
+        "mtp_pages_compact": ([p, p, p, i64, i64, i64, p, p, p, p], C.c_int),
+        "mtp_pages_copy": ([C.POINTER(p), i32, i64, i64, i64, p, i64, p, p, p], C.c_int),
         "mtpspec_status_string": ([C.c_int], C.c_char_p),
         "mtpspec_launch_count": ([], C.c_uint64),
         "mtpspec_selftest_wait_timeout": ([C.c_int, C.c_uint32, C.c_void_p, C.c_void_p], C.c_int),
@@ -544,3 +555,160 @@ def mtp_latent_prefill(q, kv, rot, cu_q, cu_k, out, scale: float, lse=None, stat
           os_[1], lse if lse is None else _vec(lse, "lse", _FLOAT, _F32, Tq * Hq), codes[dt],
           _arg(status, "status", _I32, 1, optional=True), _stream(stream))
     return out
+
+
+# ---------------------------------------------------------------- grouped heads
+
+def _caches(k_cache, v_cache, shape, like):
+    """(k pointer, v pointer, page, slot and head strides) of a cache's two halves, laid out alike."""
+    kp, ks = _view(k_cache, "k_cache", shape, like)
+    vp, vs = _view(v_cache, "v_cache", shape, like)
+    if tuple(ks) != tuple(vs):
+        raise ValueError(f"k_cache and v_cache must have the same strides, got {tuple(ks)} and {tuple(vs)}")
+    return kp, vp, ks[0], ks[1], ks[2]
+
+
+def mtp_heads_append(k, v, cos_sin, tok_row, positions, block_table, k_cache, v_cache, k_norm_w=None,
+                     q=None, q_out=None, q_norm_w=None, eps: float = 0.0, interleaved: bool = False,
+                     status=None, stream=None):
+    """k and v [T, Hkv, D] into the paged caches [pages, page_size, Hkv, D], the keys normed a head
+    and turned by cos_sin [max_pos, R]; q_out[T, Hq, D] = q normed and turned alike (see
+    include/libmtpspec/heads.h).  Token, head, page and slot strides may be any multiple of 8
+    elements."""
+    codes = _HALF_CODES or _half_codes()
+    queries = (None, 0, 0, None, None, 0, 0, 0)
+    try:
+        T, Hkv, D = k.shape
+        max_pos, R = cos_sin.shape
+        B, max_pages = block_table.shape
+        pages, P, _, _ = k_cache.shape
+        if q is not None:
+            _, Hq, _ = q.shape
+    except (AttributeError, TypeError, ValueError):
+        _refuse_axes(k=(k, 3), cos_sin=(cos_sin, 2), block_table=(block_table, 2), k_cache=(k_cache, 4),
+                     q=(q, 3))
+        raise
+    dt = k.dtype
+    kp, ks = _view(k, "k", (T, Hkv, D))
+    vp, vs = _view(v, "v", (T, Hkv, D), dt)
+    kc, vc, ps, ss, hs = _caches(k_cache, v_cache, (pages, P, Hkv, D), dt)
+    weights = []
+    for w, name in ((k_norm_w, "k_norm_w"), (q_norm_w, "q_norm_w")):
+        if w is not None and getattr(w, "dtype", dt) != dt:
+            raise TypeError(f"{name} must hold {dt} values, got {w.dtype}")
+        weights.append(None if w is None else _vec(w, name, dt, _HALF, D))
+    if q is not None or q_out is not None:
+        if q is None or q_out is None:
+            raise ValueError("q and q_out go together")
+        qp, qs = _view(q, "q", (T, Hq, D), dt)
+        op, os_ = _view(q_out, "q_out", (T, Hq, D), dt)
+        queries = (qp, qs[0], qs[1], weights[1], op, os_[0], os_[1], Hq)
+    _call("mtp_heads_append", kp, ks[0], ks[1], vp, vs[0], vs[1], weights[0],
+          _vec(cos_sin, "cos_sin", _FLOAT, _F32), max_pos, R, 1 if interleaved else 0,
+          _vec(tok_row, "tok_row", _INT, _I32, T), _vec(positions, "positions", _INT, _I32, T), T, Hkv, D,
+          _vec(block_table, "block_table", _INT, _I32), B, max_pages, kc, vc, pages, P, ps, ss, hs,
+          *queries, float(eps), codes[dt], _arg(status, "status", _I32, 1, optional=True),
+          _stream(stream))
+    return k_cache, v_cache
+
+
+def mtp_heads_attn_workspace_bytes(B: int, Tq: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(load().mtp_heads_attn_workspace_bytes(int(B), int(Tq), int(Hq), int(Hkv), int(D)))
+
+
+def mtp_heads_attn(q, k_cache, v_cache, block_table, cu_q, kv_len, out, scale: float, window: int = 0,
+                   sinks: int = 0, lse=None, workspace=None, status=None, stream=None):
+    """out[Tq, Hq, D]: attention of each row's last tokens q[Tq, Hq, D], bounded by cu_q [B + 1], over
+    its paged cache of kv_len positions; with a window, a query sees its last `window` positions
+    and the first `sinks` ones (see include/libmtpspec/heads.h)."""
+    codes = _HALF_CODES or _half_codes()
+    try:
+        Tq, Hq, D = q.shape
+        pages, P, Hkv, _ = k_cache.shape
+        B, max_pages = block_table.shape
+    except (AttributeError, TypeError, ValueError):
+        _refuse_axes(q=(q, 3), k_cache=(k_cache, 4), block_table=(block_table, 2))
+        raise
+    dt = q.dtype
+    qp, qs = _view(q, "q", (Tq, Hq, D))
+    op, os_ = _view(out, "out", (Tq, Hq, D), dt)
+    kc, vc, ps, ss, hs = _caches(k_cache, v_cache, (pages, P, Hkv, D), dt)
+    wp, ws = _ws(workspace)
+    _call("mtp_heads_attn", qp, qs[0], qs[1], kc, vc, pages, P, ps, ss, hs,
+          _vec(block_table, "block_table", _INT, _I32), max_pages, _vec(cu_q, "cu_q", _INT, _I32, B + 1),
+          _vec(kv_len, "kv_len", _INT, _I32, B), B, Tq, Hq, Hkv, D, int(window), int(sinks), float(scale),
+          op, os_[0], os_[1], lse if lse is None else _vec(lse, "lse", _FLOAT, _F32, Tq * Hq), codes[dt],
+          wp, ws, _arg(status, "status", _I32, 1, optional=True), _stream(stream))
+    return out
+
+
+# ---------------------------------------------------------------- pages
+
+def _pages(block_table, held, refs):
+    """(table, held, refs pointers; B, max_pages, num_pages)."""
+    if getattr(block_table, "ndim", 0) != 2:
+        _refuse_axes(block_table=(block_table, 2))
+    B, max_pages = block_table.shape
+    return (_arg(block_table, "block_table", _I32), _arg(held, "held", _I32, B),
+            _arg(refs, "refs", _I32)), (B, max_pages, refs.numel())
+
+
+def mtp_pages_resize(keep, lens, block_table, held, refs, page_size: int, copies=None, status=None,
+                     stream=None):
+    """Every row keeps its first keep[b] positions and gets pages for lens[b]: block_table
+    [B, max_pages], held [B] and refs [pages] follow, copies[B, 2] lists the shared last pages that
+    rows left for their own (see include/libmtpspec/pages.h)."""
+    ptrs, sizes = _pages(block_table, held, refs)
+    B = sizes[0]
+    _call("mtp_pages_resize", _arg(keep, "keep", _I32, B), _arg(lens, "lens", _I32, B), *ptrs, *sizes,
+          int(page_size), _arg(copies, "copies", _I32, 2 * B, optional=True),
+          _arg(status, "status", _I32, 1, optional=True), _stream(stream))
+    return block_table
+
+
+def mtp_pages_fork(src_rows, dst_rows, block_table, held, refs, status=None, stream=None):
+    """Row dst_rows[i] gives back its pages and shares those of src_rows[i]."""
+    ptrs, sizes = _pages(block_table, held, refs)
+    src = _arg(src_rows, "src_rows", _I32)
+    n = src_rows.numel()
+    _call("mtp_pages_fork", src, _arg(dst_rows, "dst_rows", _I32, n), n, *ptrs, *sizes,
+          _arg(status, "status", _I32, 1, optional=True), _stream(stream))
+    return block_table
+
+
+def mtp_pages_compact(block_table, held, refs, moves, n_moves, status=None, stream=None):
+    """The live pages move to the lowest numbers; moves[pages // 2, 2] lists them for
+    mtp_pages_copy."""
+    ptrs, sizes = _pages(block_table, held, refs)
+    _call("mtp_pages_compact", *ptrs, *sizes, _arg(moves, "moves", _I32, sizes[2] // 2 * 2),
+          _arg(n_moves, "n_moves", _I32, 1), _arg(status, "status", _I32, 1, optional=True),
+          _stream(stream))
+    return moves, n_moves
+
+
+def mtp_pages_copy(caches, pairs, n_pairs=None, status=None, stream=None):
+    """Page pairs[i][1] of every cache (tensors [pages, ...] of one shape and type, a page's
+    elements contiguous) becomes a copy of its page pairs[i][0]."""
+    caches = list(caches)
+    if not caches:
+        raise ValueError("caches is empty")
+    first, ptrs = caches[0], []
+    for c in caches:
+        if not isinstance(c, _kinds()["tensor"]):
+            raise TypeError("caches must be torch tensors")
+        if not c.is_cuda:
+            raise ValueError("caches must live on a CUDA device")
+        if c.dim() < 2 or c.shape[0] < 1 or not c[0].is_contiguous():
+            raise ValueError("a cache must be [pages, ...] with contiguous pages")
+        if c.shape != first.shape or c.dtype != first.dtype or c.stride() != first.stride():
+            raise ValueError("caches must have one shape, type and layout")
+        ptrs.append(c.data_ptr())
+    size = first.element_size()
+    page = first[0].numel() * size
+    stride = first.stride(0) * size if first.shape[0] > 1 else page
+    p = _arg(pairs, "pairs", _I32)
+    if pairs.dim() != 2 or pairs.shape[1] != 2:
+        raise ValueError(f"pairs must be [n, 2], got {tuple(pairs.shape)}")
+    _call("mtp_pages_copy", (C.c_void_p * len(ptrs))(*ptrs), len(ptrs), first.shape[0], page, stride, p,
+          pairs.shape[0], _arg(n_pairs, "n_pairs", _I32, 1, optional=True),
+          _arg(status, "status", _I32, 1, optional=True), _stream(stream))

@@ -672,3 +672,266 @@ MTPSPEC_API int mtp_latent_prefill(const void *q, int64_t q_tok_stride, int64_t 
     a.status = status;
     return launched(mtpspec::run_latent_prefill(a, dtype, s));
 }
+
+// ---------------------------------------------------------------- grouped heads
+
+namespace {
+
+bool head_sizes(int32_t Hq, int32_t Hkv, int32_t D) {
+    return Hkv >= 1 && Hq >= Hkv && Hq <= kMaxHeads && Hq % Hkv == 0 && Hq / Hkv <= 128 && D >= 16 &&
+           D <= 256 && D % 16 == 0;
+}
+// A cache of keys or values: [num_pages, page_size, Hkv, D], no two elements in one place.
+bool heads_cache(int64_t num_pages, int32_t page_size, int64_t max_pages, int32_t Hkv, int32_t D,
+                 int64_t page_stride, int64_t slot_stride, int64_t head_stride) {
+    return num_pages >= 1 && num_pages <= kMaxV && max_pages >= 1 && max_pages <= kMaxV &&
+           page_size >= 8 && page_size <= (1 << 24) && page_size % 8 == 0 &&
+           stride_ok(page_stride, num_pages, D) && stride_ok(slot_stride, page_size, D) &&
+           stride_ok(head_stride, Hkv, D) &&
+           apart(D, page_stride, num_pages, slot_stride, page_size, head_stride, Hkv);
+}
+
+}  // namespace
+
+MTPSPEC_API int mtp_heads_append(
+    const void *k, int64_t k_tok_stride, int64_t k_head_stride, const void *v, int64_t v_tok_stride,
+    int64_t v_head_stride, const void *k_norm_w, const float *cos_sin, int64_t max_pos, int32_t R,
+    int32_t interleaved, const int32_t *tok_row, const int32_t *positions, int64_t T, int32_t Hkv,
+    int32_t D, const int32_t *block_table, int64_t B, int64_t max_pages, void *k_cache, void *v_cache,
+    int64_t num_pages, int32_t page_size, int64_t page_stride, int64_t slot_stride,
+    int64_t head_stride, const void *q, int64_t q_tok_stride, int64_t q_head_stride,
+    const void *q_norm_w, void *q_out, int64_t q_out_tok_stride, int64_t q_out_head_stride,
+    int32_t Hq, float eps, int dtype, int32_t *status, void *stream) {
+    if (!is_half(dtype)) return MTPSPEC_ERR_DTYPE;
+    const bool queries = q != nullptr || q_out != nullptr;
+    if (T < 0 || T > kMaxTokens || B < 1 || B > kMaxLatentRows || max_pos < 1 || max_pos > kMaxV ||
+        !head_sizes(queries ? Hq : Hkv, Hkv, D) || R < 16 || R > D || R % 16 != 0 ||
+        !heads_cache(num_pages, page_size, max_pages, Hkv, D, page_stride, slot_stride, head_stride))
+        return MTPSPEC_ERR_SHAPE;
+    if (!stride_ok(k_tok_stride, T, D) || !stride_ok(k_head_stride, Hkv, D) ||
+        !stride_ok(v_tok_stride, T, D) || !stride_ok(v_head_stride, Hkv, D))
+        return MTPSPEC_ERR_SHAPE;
+    if (queries) {
+        if (!q || !q_out) return MTPSPEC_ERR_ARG;
+        if (!stride_ok(q_tok_stride, T, D) || !stride_ok(q_head_stride, Hq, D) ||
+            !stride_ok(q_out_tok_stride, T, D) || !stride_ok(q_out_head_stride, Hq, D) ||
+            !apart(D, q_out_tok_stride, T, q_out_head_stride, Hq))
+            return MTPSPEC_ERR_SHAPE;
+    }
+    if (!(eps >= 0.0f)) return MTPSPEC_ERR_ARG;
+    if (T == 0) return MTPSPEC_OK;
+    if (!k || !v || !cos_sin || !tok_row || !positions || !block_table || !k_cache || !v_cache)
+        return MTPSPEC_ERR_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q, 16) || !aligned(q_out, 16) ||
+        !aligned(k_norm_w, 16) || !aligned(q_norm_w, 16) || !aligned(cos_sin, 16) ||
+        !aligned(tok_row, 4) || !aligned(positions, 4) || !aligned(block_table, 4) ||
+        !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(status, 4))
+        return MTPSPEC_ERR_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int rc = prepare_device(s);
+    if (rc != MTPSPEC_OK) return rc;
+    mtpspec::HeadsAppendArgs a = {};
+    a.k = static_cast<const uint16_t *>(k);
+    a.v = static_cast<const uint16_t *>(v);
+    a.q = static_cast<const uint16_t *>(q);
+    a.k_tok = k_tok_stride;
+    a.k_head = k_head_stride;
+    a.v_tok = v_tok_stride;
+    a.v_head = v_head_stride;
+    a.q_tok = q_tok_stride;
+    a.q_head = q_head_stride;
+    a.k_norm_w = static_cast<const uint16_t *>(k_norm_w);
+    a.q_norm_w = static_cast<const uint16_t *>(q_norm_w);
+    a.eps = eps;
+    a.cos_sin = cos_sin;
+    a.R = R;
+    a.interleaved = interleaved;
+    a.tok_row = tok_row;
+    a.positions = positions;
+    a.T = T;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.block_table = block_table;
+    a.B = B;
+    a.max_pages = max_pages;
+    const int64_t slots = max_pages * page_size;
+    a.pos_end = max_pos < slots ? max_pos : slots;
+    a.k_cache = static_cast<uint16_t *>(k_cache);
+    a.v_cache = static_cast<uint16_t *>(v_cache);
+    a.num_pages = num_pages;
+    a.page_stride = page_stride;
+    a.slot_stride = slot_stride;
+    a.head_stride = head_stride;
+    a.page_size = page_size;
+    a.q_out = static_cast<uint16_t *>(q_out);
+    a.q_out_tok = q_out_tok_stride;
+    a.q_out_head = q_out_head_stride;
+    a.status = status;
+    return launched(mtpspec::run_heads_append(a, dtype, s));
+}
+
+namespace {
+
+bool heads_attn_sizes(int64_t B, int64_t Tq, int32_t Hq, int32_t Hkv, int32_t D) {
+    return B >= 1 && B <= 65536 && Tq >= 0 && Tq <= kMaxPromptTokens && head_sizes(Hq, Hkv, D) &&
+           Tq * Hq <= kMaxV;
+}
+
+}  // namespace
+
+MTPSPEC_API size_t mtp_heads_attn_workspace_bytes(int64_t B, int64_t Tq, int32_t Hq, int32_t Hkv,
+                                                  int32_t D) {
+    if (!heads_attn_sizes(B, Tq, Hq, Hkv, D) || Tq == 0) return 0;
+    return mtpspec::heads_attn_workspace_bytes(B, Tq, Hq, Hkv, D);
+}
+
+MTPSPEC_API int mtp_heads_attn(const void *q, int64_t q_tok_stride, int64_t q_head_stride,
+                               const void *k_cache, const void *v_cache, int64_t num_pages,
+                               int32_t page_size, int64_t page_stride, int64_t slot_stride,
+                               int64_t head_stride, const int32_t *block_table, int64_t max_pages,
+                               const int32_t *cu_q, const int32_t *kv_len, int64_t B, int64_t Tq,
+                               int32_t Hq, int32_t Hkv, int32_t D, int32_t window, int32_t sinks,
+                               float scale, void *out, int64_t out_tok_stride,
+                               int64_t out_head_stride, float *lse, int dtype, void *workspace,
+                               size_t workspace_bytes, int32_t *status, void *stream) {
+    if (!is_half(dtype)) return MTPSPEC_ERR_DTYPE;
+    if (!heads_attn_sizes(B, Tq, Hq, Hkv, D) ||
+        !heads_cache(num_pages, page_size, max_pages, Hkv, D, page_stride, slot_stride, head_stride))
+        return MTPSPEC_ERR_SHAPE;
+    if (!stride_ok(q_tok_stride, Tq, D) || !stride_ok(q_head_stride, Hq, D) ||
+        !stride_ok(out_tok_stride, Tq, D) || !stride_ok(out_head_stride, Hq, D) ||
+        !apart(D, out_tok_stride, Tq, out_head_stride, Hq))
+        return MTPSPEC_ERR_SHAPE;
+    if (!good_scale(scale) || window < 0 || sinks < 0) return MTPSPEC_ERR_ARG;
+    if (Tq == 0) return MTPSPEC_OK;
+    if (!q || !k_cache || !v_cache || !block_table || !cu_q || !kv_len || !out) return MTPSPEC_ERR_ARG;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+        !aligned(block_table, 4) || !aligned(cu_q, 4) || !aligned(kv_len, 4) || !aligned(lse, 4) ||
+        !aligned(status, 4))
+        return MTPSPEC_ERR_ARG;
+    if (!workspace || workspace_bytes < mtpspec::heads_attn_workspace_bytes(B, Tq, Hq, Hkv, D))
+        return MTPSPEC_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return MTPSPEC_ERR_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int rc = prepare_device(s);
+    if (rc != MTPSPEC_OK) return rc;
+    mtpspec::HeadsAttnArgs a = {};
+    a.q = static_cast<const uint16_t *>(q);
+    a.q_tok = q_tok_stride;
+    a.q_head = q_head_stride;
+    a.k_cache = static_cast<const uint16_t *>(k_cache);
+    a.v_cache = static_cast<const uint16_t *>(v_cache);
+    a.num_pages = num_pages;
+    a.page_stride = page_stride;
+    a.slot_stride = slot_stride;
+    a.head_stride = head_stride;
+    a.page_size = page_size;
+    a.block_table = block_table;
+    a.max_pages = max_pages;
+    a.cu_q = cu_q;
+    a.kv_len = kv_len;
+    a.B = B;
+    a.Tq = Tq;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.window = window;
+    a.sinks = sinks;
+    a.scale = scale;
+    a.out = static_cast<uint16_t *>(out);
+    a.out_tok = out_tok_stride;
+    a.out_head = out_head_stride;
+    a.lse = lse;
+    a.workspace = workspace;
+    a.status = status;
+    return launched(mtpspec::run_heads_attn(a, dtype, s));
+}
+
+// ---------------------------------------------------------------- pages
+
+namespace {
+
+bool pages_sizes(int64_t B, int64_t max_pages, int64_t num_pages) {
+    return B >= 1 && B <= 16384 && max_pages >= 1 && max_pages <= kMaxV && num_pages >= 1 &&
+           num_pages <= kMaxV && B * max_pages <= (int64_t{1} << 40);
+}
+
+}  // namespace
+
+MTPSPEC_API int mtp_pages_resize(const int32_t *keep, const int32_t *lens, int32_t *block_table,
+                                 int32_t *held, int32_t *refs, int64_t B, int64_t max_pages,
+                                 int64_t num_pages, int32_t page_size, int32_t *copies,
+                                 int32_t *status, void *stream) {
+    if (!pages_sizes(B, max_pages, num_pages) || page_size < 1 || page_size > (1 << 24))
+        return MTPSPEC_ERR_SHAPE;
+    if (!keep || !lens || !block_table || !held || !refs) return MTPSPEC_ERR_ARG;
+    if (!aligned(keep, 4) || !aligned(lens, 4) || !aligned(block_table, 4) || !aligned(held, 4) ||
+        !aligned(refs, 4) || !aligned(copies, 4) || !aligned(status, 4))
+        return MTPSPEC_ERR_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int rc = prepare_device(s);
+    if (rc != MTPSPEC_OK) return rc;
+    return launched(mtpspec::run_pages_resize(
+        {keep, lens, block_table, held, refs, B, max_pages, num_pages, page_size, copies, status}, s));
+}
+
+MTPSPEC_API int mtp_pages_fork(const int32_t *src_rows, const int32_t *dst_rows, int64_t n,
+                               int32_t *block_table, int32_t *held, int32_t *refs, int64_t B,
+                               int64_t max_pages, int64_t num_pages, int32_t *status, void *stream) {
+    if (!pages_sizes(B, max_pages, num_pages) || n < 0 || n > 1024) return MTPSPEC_ERR_SHAPE;
+    if (n == 0) return MTPSPEC_OK;
+    if (!src_rows || !dst_rows || !block_table || !held || !refs) return MTPSPEC_ERR_ARG;
+    if (!aligned(src_rows, 4) || !aligned(dst_rows, 4) || !aligned(block_table, 4) ||
+        !aligned(held, 4) || !aligned(refs, 4) || !aligned(status, 4))
+        return MTPSPEC_ERR_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int rc = prepare_device(s);
+    if (rc != MTPSPEC_OK) return rc;
+    return launched(mtpspec::run_pages_fork(
+        {src_rows, dst_rows, n, block_table, held, refs, B, max_pages, num_pages, status}, s));
+}
+
+MTPSPEC_API int mtp_pages_compact(int32_t *block_table, const int32_t *held, int32_t *refs, int64_t B,
+                                  int64_t max_pages, int64_t num_pages, int32_t *moves,
+                                  int32_t *n_moves, int32_t *status, void *stream) {
+    if (!pages_sizes(B, max_pages, num_pages)) return MTPSPEC_ERR_SHAPE;
+    if (!block_table || !held || !refs || (!moves && num_pages > 1) || !n_moves) return MTPSPEC_ERR_ARG;
+    if (!aligned(block_table, 4) || !aligned(held, 4) || !aligned(refs, 4) || !aligned(moves, 4) ||
+        !aligned(n_moves, 4) || !aligned(status, 4))
+        return MTPSPEC_ERR_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int rc = prepare_device(s);
+    if (rc != MTPSPEC_OK) return rc;
+    return launched(mtpspec::run_pages_compact(
+        {block_table, held, refs, B, max_pages, num_pages, moves, n_moves, status}, s));
+}
+
+MTPSPEC_API int mtp_pages_copy(void *const *caches, int32_t n_caches, int64_t num_pages,
+                               int64_t page_bytes, int64_t page_stride, const int32_t *pairs,
+                               int64_t n, const int32_t *n_pairs, int32_t *status, void *stream) {
+    if (n_caches < 1 || n_caches > mtpspec::kMaxCaches || num_pages < 1 || num_pages > kMaxV ||
+        page_bytes < 16 || page_bytes % 16 != 0 || page_stride % 16 != 0 || page_stride < page_bytes ||
+        page_stride > 2 * kMaxStride || n < 0 || n > (int64_t{1} << 30))
+        return MTPSPEC_ERR_SHAPE;
+    if (n == 0) return MTPSPEC_OK;
+    if (!caches || !pairs) return MTPSPEC_ERR_ARG;
+    mtpspec::PagesCopyArgs a = {};
+    for (int32_t c = 0; c < n_caches; ++c) {
+        if (!caches[c] || !aligned(caches[c], 16)) return MTPSPEC_ERR_ARG;
+        a.caches[c] = static_cast<char *>(caches[c]);
+    }
+    if (!aligned(pairs, 4) || !aligned(n_pairs, 4) || !aligned(status, 4)) return MTPSPEC_ERR_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int rc = prepare_device(s);
+    if (rc != MTPSPEC_OK) return rc;
+    a.n_caches = n_caches;
+    a.num_pages = num_pages;
+    a.page_bytes = page_bytes;
+    a.page_stride = page_stride;
+    a.pairs = pairs;
+    a.n_pairs = n_pairs;
+    a.n = n;
+    a.status = status;
+    return launched(mtpspec::run_pages_copy(a, s));
+}

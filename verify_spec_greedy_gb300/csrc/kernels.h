@@ -276,3 +276,91 @@ struct LatentPrefillArgs {
 cudaError_t run_latent_prefill(const LatentPrefillArgs &a, int dtype, cudaStream_t stream);
 
 }  // namespace mtpspec
+
+namespace mtpspec {
+
+// The draft head's attention with grouped heads (heads_append.cu, heads_attn.cu); 16-bit arrays
+// are passed as their bit patterns, strides are in elements.
+struct HeadsAppendArgs {
+    const uint16_t *k, *v, *q;  // q may be nullptr
+    int64_t k_tok, k_head, v_tok, v_head, q_tok, q_head;
+    const uint16_t *k_norm_w, *q_norm_w;  // or nullptr
+    float eps;
+    const float *cos_sin;
+    int32_t R, interleaved;
+    const int32_t *tok_row, *positions;
+    int64_t T;
+    int32_t Hq, Hkv, D;
+    const int32_t *block_table;
+    int64_t B, max_pages, pos_end;  // positions lie in [0, pos_end)
+    uint16_t *k_cache, *v_cache;
+    int64_t num_pages, page_stride, slot_stride, head_stride;
+    int32_t page_size;
+    uint16_t *q_out;
+    int64_t q_out_tok, q_out_head;
+    int32_t *status;
+};
+cudaError_t run_heads_append(const HeadsAppendArgs &a, int dtype, cudaStream_t stream);
+
+struct HeadsAttnArgs {
+    const uint16_t *q, *k_cache, *v_cache;
+    int64_t q_tok, q_head;
+    int64_t num_pages, page_stride, slot_stride, head_stride;
+    int32_t page_size;
+    const int32_t *block_table;
+    int64_t max_pages;
+    const int32_t *cu_q, *kv_len;
+    int64_t B, Tq;
+    int32_t Hq, Hkv, D, window, sinks;
+    float scale;
+    uint16_t *out;
+    int64_t out_tok, out_head;
+    float *lse;  // or nullptr
+    void *workspace;
+    int32_t *status;
+};
+size_t heads_attn_workspace_bytes(int64_t B, int64_t Tq, int32_t Hq, int32_t Hkv, int32_t D);
+cudaError_t run_heads_attn(const HeadsAttnArgs &a, int dtype, cudaStream_t stream);
+
+// The pages of a draft head's cache (pages.cu).
+struct PagesResizeArgs {
+    const int32_t *keep, *lens;
+    int32_t *block_table, *held, *refs;
+    int64_t B, max_pages, num_pages;
+    int32_t page_size;
+    int32_t *copies;  // [B, 2] or nullptr
+    int32_t *status;
+};
+cudaError_t run_pages_resize(const PagesResizeArgs &a, cudaStream_t stream);
+
+struct PagesForkArgs {
+    const int32_t *src_rows, *dst_rows;
+    int64_t n;
+    int32_t *block_table, *held, *refs;
+    int64_t B, max_pages, num_pages;
+    int32_t *status;
+};
+cudaError_t run_pages_fork(const PagesForkArgs &a, cudaStream_t stream);
+
+struct PagesCompactArgs {
+    int32_t *block_table;
+    const int32_t *held;
+    int32_t *refs;
+    int64_t B, max_pages, num_pages;
+    int32_t *moves, *n_moves;
+    int32_t *status;
+};
+cudaError_t run_pages_compact(const PagesCompactArgs &a, cudaStream_t stream);
+
+constexpr int kMaxCaches = 64;
+struct PagesCopyArgs {
+    char *caches[kMaxCaches];
+    int32_t n_caches;
+    int64_t num_pages, page_bytes, page_stride;  // bytes
+    const int32_t *pairs, *n_pairs;              // n_pairs or nullptr
+    int64_t n;
+    int32_t *status;
+};
+cudaError_t run_pages_copy(const PagesCopyArgs &a, cudaStream_t stream);
+
+}  // namespace mtpspec
