@@ -113,9 +113,12 @@ __global__ void __launch_bounds__(THREADS) k_heads_attn(const HeadsAttnArgs a) {
 
 }  // namespace hat
 
-size_t heads_attn_workspace_bytes(int64_t, int64_t, int32_t, int32_t, int32_t) { return 256; }
+size_t heads_attn_workspace_bytes(int64_t, int64_t, int32_t, int32_t, int32_t D) {
+    return D <= 128 ? heads_chunk_workspace_bytes(D) : 256;
+}
 
 cudaError_t run_heads_attn(const HeadsAttnArgs &a, int dtype, cudaStream_t stream) {
+    if (a.D <= 128) return run_heads_chunk(a, dtype, stream);
     const unsigned grid = static_cast<unsigned>(a.Tq * a.Hq);
     if (dtype == MTPSPEC_BF16)
         hat::k_heads_attn<Bf16><<<grid, hat::THREADS, 0, stream>>>(a);
