@@ -775,7 +775,7 @@ namespace {
 
 bool heads_attn_sizes(int64_t B, int64_t Tq, int32_t Hq, int32_t Hkv, int32_t D) {
     return B >= 1 && B <= 65536 && Tq >= 0 && Tq <= kMaxPromptTokens && head_sizes(Hq, Hkv, D) &&
-           Tq * Hq <= kMaxV;
+           Tq * Hq <= (1 << 30);
 }
 
 }  // namespace

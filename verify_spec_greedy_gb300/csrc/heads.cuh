@@ -1,0 +1,449 @@
+// What the kernels of the attention with grouped heads share: the units of work, their even cut
+// over the CTAs, and the joining of the units that the cut divides.
+#pragma once
+
+#include "half_types.cuh"
+#include "kernels.h"
+#include "tcgen05.cuh"
+
+namespace mtpspec {
+namespace heads {
+
+using namespace tg;
+
+constexpr int SMS = 152;           // multiprocessors of a GB300
+constexpr int64_t START = 2;       // a unit's start and end, in key tiles
+constexpr float LAZY = 8.0f;       // the running maximum may lag by a factor of 2^8
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr uint32_t POLL_LIMIT = 1u << 25;  // polls of some 20 ns: ~1 s
+
+// For the joining kernel, by CTA: the unit that starts there and ends in another.
+struct __align__(32) Plan {
+    int q0, m0, rows, head, parts;  // its row's first token in q, its (token, head) rows, its key
+                                    // head, the CTAs that have a part; 0 parts: there is none
+};
+
+struct Params {
+    const int32_t *cu_q, *kv_len, *block_table;
+    int64_t max_pages;
+    int max_len;         // the table's positions, up to 2^31 - 256
+    int num_pages, page_size, box_rows;
+    int B, Tq, Hq, Hkv, G, D, window, sinks;
+    int tile_rows;       // (token, head) rows that a row tile holds
+    int unit_rows;       // and a unit, of one or two tiles
+    float scale2;        // scale * log2(e), above 0
+    const uint16_t *q;
+    int64_t q_tok, q_head;
+    uint16_t *out;
+    int64_t out_tok, out_head;
+    float *lse;
+    Plan *plan;
+    float *part;         // fp32, normalised partial outputs: two slots a CTA
+    float *part_lse;     // base 2
+    int32_t *status;
+};
+
+struct Maps {
+    CUtensorMap q, k, v;
+};
+
+__device__ __forceinline__ int row_len(const Params &p, int b) {
+    return min(max(p.kv_len[b], 0), p.max_len);
+}
+// Bound i of cu_q as it is taken: in [0, Tq], and not below the ones before it.
+__device__ __forceinline__ int bound(const Params &p, int i, int before) {
+    return max(min(p.cu_q[i], p.Tq), before);
+}
+
+// A unit of work: `unit_rows` (token, head) rows of one key head of a row, against tiles of TN keys.
+// With a window it meets the tiles of the first tokens, then those of the window.
+template <int TN>
+struct Unit {
+    int q0, nq, len, m0;  // the row's first token in q, its tokens and length; the unit's first row
+    int w0, ns;           // the first key tile of its window, and the tiles of first tokens before
+    __device__ __forceinline__ Unit() {}
+    __device__ __forceinline__ Unit(const Params &p, int q0_, int nq_, int len_, int unit)
+        : q0(q0_), nq(nq_), len(len_), m0(unit * p.unit_rows) {
+        w0 = ns = 0;
+        if (p.window > 0 && p.window < len) {
+            w0 = max(0, len - nq + m0 / p.G - p.window + 1) / TN;
+            ns = min(p.sinks / TN + (p.sinks % TN != 0), w0);
+        }
+    }
+    // Key tiles that `rows` rows from row m on meet.
+    __device__ __forceinline__ int tiles(const Params &p, int m, int rows) const {
+        const int hi = len - nq + min((m + rows - 1) / p.G + 1, nq);
+        return m >= nq * p.G || hi <= 0 ? 0 : ns + (hi + TN - 1) / TN - w0;
+    }
+    __device__ __forceinline__ int tiles(const Params &p) const { return tiles(p, m0, p.unit_rows); }
+    // Its length in the cut (one tile at least, so that every unit is somebody's).
+    __device__ __forceinline__ int64_t weight(const Params &p) const { return START + max(tiles(p), 1); }
+    // The number of its i-th key tile.
+    __device__ __forceinline__ int key_tile(int i) const { return i < ns ? i : i - ns + w0; }
+    // The place in its list of the tile that the row's keys end in, if that is not a whole one.
+    __device__ __forceinline__ int tail() const { return len % TN != 0 ? ns + len / TN - w0 : -1; }
+};
+
+// An even cut of all units laid end to end: of the CTAs that take part, the first `rem` have
+// per + 1, the others per.
+struct Cut {
+    int64_t total, per;
+    int active, rem;
+    __device__ __forceinline__ Cut(int64_t sum, int ctas) : total(sum) {
+        active = static_cast<int>(sum < ctas ? sum : ctas);
+        if (active == 0) {
+            per = 0;
+        } else if (sum < (int64_t{1} << 31)) {
+            per = static_cast<uint32_t>(sum) / static_cast<uint32_t>(active);
+        } else {
+            per = sum / active;
+        }
+        rem = static_cast<int>(sum - per * active);
+    }
+    __device__ __forceinline__ int64_t first(int g) const {
+        return g < active ? per * g + (g < rem ? g : rem) : total;
+    }
+    __device__ __forceinline__ int owner(int64_t at) const {
+        const int64_t big = (per + 1) * rem;
+        return static_cast<int>(at < big ? at / (per + 1) : rem + (at - big) / per);
+    }
+};
+
+// A CTA's walk through its part of the cut, by one warp, all lanes alike.
+template <int TN>
+struct Walk {
+    int row, q0, q1, len, head, unit, units;  // the next unit
+    int64_t cur, at, end;                     // what is left of the CTA's part, and where the unit starts
+    bool cut_here;                            // a unit starts here and ends in another CTA
+
+    __device__ __forceinline__ void open_row(const Params &p) {
+        q1 = bound(p, row + 1, q0);
+        len = row_len(p, row);
+        units = units_of(p, q1 - q0);
+    }
+    static __device__ __forceinline__ int units_of(const Params &p, int nq) {
+        return (nq * p.G + p.unit_rows - 1) / p.unit_rows;
+    }
+    // The next unit with tiles for this CTA: tiles i0 .. i1 - 1 of n; false if there is none.
+    __device__ __forceinline__ bool next(const Params &p, const Cut &cut, Unit<TN> &u, int &i0, int &i1, int &n) {
+        while (cur < end) {
+            while (unit >= units) {  // (rows without tokens have no units)
+                unit = 0;
+                if (units == 0 || ++head == p.Hkv) {
+                    head = 0;
+                    q0 = q1;
+                    if (++row >= p.B) return false;
+                    open_row(p);
+                }
+            }
+            u = Unit<TN>(p, q0, q1 - q0, len, unit);
+            n = max(u.tiles(p), 1);
+            const int64_t base = at + START, s = max(cur, base), e = min(end, base + n);
+            at = base + n;
+            cur = min(end, at);
+            ++unit;
+            if (s >= e) continue;
+            i0 = static_cast<int>(s - base);
+            i1 = static_cast<int>(e - base);
+            if (i0 == 0 && i1 < n && (threadIdx.x & 31) == 0) {
+                cut_here = true;
+                p.plan[blockIdx.x] = {q0, u.m0, min(p.unit_rows, (q1 - q0) * p.G - u.m0), head,
+                                      cut.owner(base + n - 1) - static_cast<int>(blockIdx.x) + 1};
+            }
+            return true;
+        }
+        return false;
+    }
+    // A CTA without a cut unit says so.
+    __device__ __forceinline__ void close(const Params &p) const {
+        if ((threadIdx.x & 31) == 0 && !cut_here) p.plan[blockIdx.x] = {0, 0, 0, 0, 0};
+    }
+};
+
+// The scan of the rows' units by a whole block of NT threads, a run of rows a thread, or, of few
+// rows, a row a warp whose lanes share its units; then warp `who` sets its walk up.
+struct Scan {
+    int64_t sums[32];
+    int64_t first_off;
+    int first_row, first_q0;
+};
+template <int TN, int NT>
+__device__ __forceinline__ Cut find_start(const Params &p, Scan &sh, int who, Walk<TN> &walk) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool wide = p.B <= NT / 32;
+    const int run = wide ? 1 : (p.B + NT - 1) / NT;
+    const int b0 = min(p.B, wide ? warp : static_cast<int>(threadIdx.x) * run), b1 = min(p.B, b0 + run);
+    bool bad = false, order = false;
+    int64_t sum = 0;
+    const auto weigh = [&](int q0, int q1, int len, int from, int step) {
+        int64_t w = 0;
+        for (int i = from; i < Walk<TN>::units_of(p, q1 - q0); i += step)
+            w += Unit<TN>(p, q0, q1 - q0, len, i).weight(p);
+        return w;
+    };
+    for (int b = b0; b < b1; ++b) {
+        const int c0 = p.cu_q[b], c1 = p.cu_q[b + 1], len = p.kv_len[b];
+        order |= c0 < 0 || c1 > p.Tq || c1 < c0;
+        bad |= len < 0 || len > p.max_len;
+        if (!order) sum += weigh(c0, c1, min(max(len, 0), p.max_len), wide ? lane : 0, wide ? 32 : 1);
+    }
+    const bool disorder = __syncthreads_or(order);
+    if (bad || order)
+        if (blockIdx.x == 0 && p.status) atomicOr(p.status, MTPSPEC_STATUS_BAD_PARAM);
+    int q_before = 0;  // the largest bound up to the first of the run, as taken
+    if (disorder) {
+        for (int b = 0; b < b0; ++b) q_before = bound(p, b, q_before);
+        sum = 0;
+        int q0 = b0 < b1 ? bound(p, b0, q_before) : 0;
+        for (int b = b0; b < b1; ++b) {
+            const int q1 = bound(p, b + 1, q0);
+            sum += weigh(q0, q1, row_len(p, b), wide ? lane : 0, wide ? 32 : 1);
+            q0 = q1;
+        }
+    }
+    sum *= p.Hkv;
+    int64_t at = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, at, o);
+        if (lane >= o) at += v;
+    }
+    if (lane == 31) sh.sums[warp] = at;
+    __syncthreads();
+    int64_t total = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w == warp) at += total;
+        total += sh.sums[w];
+    }
+    at -= sum;
+    const Cut cut(total, gridDim.x);
+    const int64_t t0 = cut.first(blockIdx.x), t1 = cut.first(blockIdx.x + 1);
+    if (wide) {  // the row's sum is its whole warp's
+        at = __shfl_sync(0xFFFFFFFFu, at, 0);
+        sum = sh.sums[warp];
+    }
+    if (t0 < t1 && at <= t0 && t0 < at + sum && (!wide || lane == 0)) {
+        int q0 = bound(p, b0, q_before), b = b0;
+        int64_t off = t0 - at;
+        for (; b + 1 < b1; ++b) {  // (a run of one row has nothing to look for)
+            const int q1 = bound(p, b + 1, q0);
+            const int64_t mine = weigh(q0, q1, row_len(p, b), 0, 1) * p.Hkv;
+            if (off < mine) break;
+            off -= mine;
+            q0 = q1;
+        }
+        sh.first_row = b;
+        sh.first_q0 = q0;
+        sh.first_off = off;
+    }
+    __syncthreads();
+    if (warp != who) return cut;
+    walk.cur = walk.at = t0;
+    walk.end = t1;
+    walk.cut_here = false;
+    if (t0 >= t1) return cut;
+    walk.row = sh.first_row;
+    walk.q0 = sh.first_q0;
+    walk.open_row(p);
+    // the row's units of one head, 32 at a time, until the one that t0 lies in
+    int64_t off = sh.first_off, mine = weigh(walk.q0, walk.q1, walk.len, lane, 32);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
+    walk.head = static_cast<int>(off / mine);
+    off -= walk.head * mine;
+    for (walk.unit = 0;; walk.unit += 32) {
+        const int i = walk.unit + lane;
+        const int64_t w = i < walk.units ? Unit<TN>(p, walk.q0, walk.q1 - walk.q0, walk.len, i).weight(p) : 0;
+        int64_t to = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xFFFFFFFFu, to, o);
+            if (lane >= o) to += v;
+        }
+        const int64_t here = __shfl_sync(0xFFFFFFFFu, to, 31);
+        if (off < here || walk.unit + 32 >= walk.units) {
+            const unsigned has = __ballot_sync(0xFFFFFFFFu, off < to);
+            const int src = has ? __ffs(has) - 1 : 0;
+            off -= __shfl_sync(0xFFFFFFFFu, to - w, src);
+            walk.unit += src;
+            break;
+        }
+        off -= here;
+    }
+    walk.at = t0 - off;
+    return cut;
+}
+
+// A bounded wait; once any wait of the CTA has given up, the others return at once, and the roles run
+// to their ends without touching what they could not wait for.
+template <typename Shared>
+__device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity,
+                                    uint32_t limit = POLL_LIMIT) {
+    for (uint32_t it = 0; it < limit; ++it) {
+        if (mbar_poll(bar, parity)) return true;
+        if (sh.abort) return false;
+    }
+    sh.abort = 1;
+    return false;
+}
+// The same for a wait that is mostly long: the thread is suspended instead of polling, which
+// leaves issue slots and shared memory to the others.
+template <typename Shared>
+__device__ __forceinline__ bool wait_long(Shared &sh, uint64_t *bar, uint32_t parity,
+                                         uint32_t limit = WAIT_LIMIT) {
+    for (uint32_t it = 0; it < limit; ++it) {
+        if (mbar_test(bar, parity)) return true;
+        if (sh.abort) return false;
+    }
+    sh.abort = 1;
+    return false;
+}
+// And for one on others whose own waits are bounded, which may take as long as a whole item.
+template <typename Shared>
+__device__ __forceinline__ bool wait_far(Shared &sh, uint64_t *bar, uint32_t parity) {
+    return wait_long(sh, bar, parity, 64 * WAIT_LIMIT);
+}
+// The bounded wait of a CTA that leaves, whatever the abort flag says.
+__device__ __forceinline__ void wait_out(uint64_t *bar, uint32_t parity) {
+    for (uint32_t it = 0; it < WAIT_LIMIT; ++it)
+        if (mbar_test(bar, parity)) return;
+}
+
+// A tile of keys in boxes that stay within a page, one a lane: where this lane's box of the tile
+// lies.  Beyond the row's length, and where the table has no such page, TMA fills zeros.
+__device__ __forceinline__ int2 find_box(const Params &p, const int32_t *table, int key, int len, bool mine) {
+    const int pi = key / p.page_size, slot = key - pi * p.page_size;
+    int page = p.num_pages;
+    if (mine && key < len) {
+        page = table[pi];
+        if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) {
+            page = p.num_pages;
+            if (p.status) atomicOr(p.status, MTPSPEC_STATUS_BAD_PARAM);
+        }
+    }
+    return make_int2(page, slot);
+}
+
+// Units cut among CTAs: each row's partial outputs, weighted by their sums, become the output.  A
+// warp a row; blockIdx.y is the CTA of the first kernel in which the unit starts.  A slot holds
+// TILES tiles of TM rows, of which tile_rows are used.
+constexpr int JOIN_THREADS = 256, JOIN_WARPS = JOIN_THREADS / 32;
+
+template <typename T, int NC, int TM, int TILES>
+__global__ void __launch_bounds__(JOIN_THREADS) k_heads_join(const Params p) {
+    pdl_wait_primary();
+    const Plan u = p.plan[blockIdx.y];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rr = blockIdx.x * JOIN_WARPS + warp, r = rr % TM, in = rr / TM * p.tile_rows + r;
+    // (what an aborted call left there is checked)
+    if (u.parts < 2 || u.parts > static_cast<int>(gridDim.y - blockIdx.y) || r >= p.tile_rows || in >= u.rows ||
+        u.q0 < 0 || u.m0 < 0 || u.q0 + (u.m0 + in) / p.G >= p.Tq || u.head < 0 || u.head >= p.Hkv)
+        return;
+    const int m = u.m0 + in, h = u.head * p.G + m % p.G;
+    // a CTA's partial of this row: the second slot where the unit starts, else the first
+    const auto part_row = [&](int i) {
+        return static_cast<int64_t>(2 * (blockIdx.y + i) + (i == 0)) * (TILES * TM) + rr;
+    };
+    float top = -INFINITY, sum = 0.0f;
+    for (int i = lane; i < u.parts; i += 32) top = fmaxf(top, p.part_lse[part_row(i)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    const float ref = top == -INFINITY ? 0.0f : top;
+    constexpr int PER = 2 * NC;  // a lane's columns
+    float acc[PER] = {};
+#pragma unroll 4
+    for (int i = 0; i < u.parts; ++i) {
+        const int64_t row = part_row(i);
+        const float w = exp2f(p.part_lse[row] - ref);
+        sum += w;
+        float v[PER];
+#pragma unroll
+        for (int k = 0; k < PER; k += 2)
+            *reinterpret_cast<float2 *>(v + k) =
+                *reinterpret_cast<const float2 *>(p.part + row * (64 * NC) + k * 32 + lane * 2);
+#pragma unroll
+        for (int k = 0; k < PER; ++k) acc[k] += w * v[k];
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int64_t out_row = u.q0 + m / p.G;
+    uint16_t *dst = p.out + out_row * p.out_tok + h * p.out_head;
+#pragma unroll
+    for (int k = 0; k < PER; k += 2)
+        if (k * 32 + lane * 2 < p.D)
+            *reinterpret_cast<uint32_t *>(dst + k * 32 + lane * 2) = T::narrow2(acc[k] * inv, acc[k + 1] * inv);
+    if (p.lse && lane == 0) p.lse[out_row * p.Hq + h] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * LN2;
+}
+
+// The parameters and tensor maps of a call whose row tiles hold `tile_rows` rows and whose units
+// `tiles` of them; the workspace's parts lie at the given offsets.  The queries' map brings a whole
+// tile of them, as tile_rows / G tokens of G heads, if G divides it; q comes as it is otherwise.
+inline bool set_up(const HeadsAttnArgs &a, int tile_rows, int tiles, int TN, size_t plan, size_t part,
+                   size_t lse, Params &p, Maps &maps) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    p = {};
+    p.G = a.Hq / a.Hkv;
+    p.tile_rows = tile_rows;
+    p.unit_rows = tiles * tile_rows;
+    // boxes of the largest power of two (up to a tile) that divides the page: a box never leaves
+    // its page, and its rows start at a multiple of eight, the swizzle's period
+    const int two = a.page_size & -a.page_size;
+    p.box_rows = two < TN ? two : TN;
+    // an axis of one element may come with any stride
+    const int64_t slot = a.slot_stride, head = a.Hkv == 1 ? a.D : a.head_stride;
+    const int64_t page = a.num_pages == 1 ? slot * a.page_size : a.page_stride;
+    const int64_t q_head = a.Hq == 1 ? a.D : a.q_head, q_tok = a.Tq == 1 ? a.D : a.q_tok;
+    const auto encode = [&](CUtensorMap *m, const uint16_t *ptr, const cuuint64_t (&dims)[4],
+                            const cuuint64_t (&strides)[3], const cuuint32_t (&box)[4]) {
+        const cuuint32_t es[4] = {1, 1, 1, 1};
+        return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t *>(ptr), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    const auto u = [](int64_t x) { return static_cast<cuuint64_t>(x); };
+    const cuuint64_t cd[4] = {u(a.D), u(a.Hkv), u(a.page_size), u(a.num_pages)},
+                     cs[3] = {u(head * 2), u(slot * 2), u(page * 2)};
+    const cuuint32_t cb[4] = {64, 1, static_cast<cuuint32_t>(p.box_rows), 1};
+    if (!encode(&maps.k, a.k_cache, cd, cs, cb) || !encode(&maps.v, a.v_cache, cd, cs, cb)) return false;
+    if (tiles == 2) {
+        const cuuint64_t qd[4] = {u(a.D), u(p.G), u(a.Tq), u(a.Hkv)},
+                         qs[3] = {u(q_head * 2), u(q_tok * 2), u(q_head * p.G * 2)};
+        const cuuint32_t qb[4] = {64, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(tile_rows / p.G), 1};
+        if (!encode(&maps.q, a.q, qd, qs, qb)) return false;
+    } else {
+        maps.q = maps.k;
+    }
+    unsigned char *ws = static_cast<unsigned char *>(a.workspace);
+    p.cu_q = a.cu_q;
+    p.kv_len = a.kv_len;
+    p.block_table = a.block_table;
+    p.max_pages = a.max_pages;
+    const int64_t slots = a.max_pages * a.page_size, most = (int64_t{1} << 31) - 256;
+    p.max_len = static_cast<int>(slots < most ? slots : most);
+    p.num_pages = static_cast<int>(a.num_pages);
+    p.page_size = a.page_size;
+    p.B = static_cast<int>(a.B);
+    p.Tq = static_cast<int>(a.Tq);
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.D = a.D;
+    p.window = a.window;
+    p.sinks = a.sinks;
+    p.scale2 = a.scale * LOG2E;
+    p.q = a.q;
+    p.q_tok = a.q_tok;
+    p.q_head = a.q_head;
+    p.out = a.out;
+    p.out_tok = a.out_tok;
+    p.out_head = a.out_head;
+    p.lse = a.lse;
+    p.plan = reinterpret_cast<Plan *>(ws + plan);
+    p.part = reinterpret_cast<float *>(ws + part);
+    p.part_lse = reinterpret_cast<float *>(ws + lse);
+    p.status = a.status;
+    return true;
+}
+
+}  // namespace heads
+}  // namespace mtpspec

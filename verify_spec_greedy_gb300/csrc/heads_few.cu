@@ -1,0 +1,623 @@
+// Attention with grouped heads over the paged cache, for rows of few tokens: draft steps and
+// verifications.  What bounds them is the cache's bytes.
+//
+// One pass over the keys with the running maximum m and sum l of a softmax, as in heads_chunk.cu.
+// A unit's rows, the (token, head) rows of a key head, are ROWS = 32 or 64, whose accumulators are
+// folded into all 128 lanes of tensor memory: NQ = 128 / ROWS threads share a row, so that with few
+// rows every thread of the four softmax warps has work, TN / NQ keys of a tile each.
+//
+// Keys and values stream through a ring of chunks (TN tokens x 64 columns), released one by one.
+// The scores of a tile are computed ahead of the weights of the tile before, across units as well.
+// With 32 rows and heads of up to 128 elements two CTAs share an SM: while one is in a
+// softmax, the other's copies and products go on.
+#include <algorithm>
+
+#include "heads.cuh"
+
+namespace mtpspec {
+namespace hfw {
+
+using namespace heads;
+
+constexpr int NTHREADS = 224;  // warp 0 TMA, 1 MMA and TMEM, 2-5 softmax, 6 items and queries
+constexpr int SOFTMAX0 = 64;   // the first softmax thread
+constexpr int MAX_SLOTS = 16;
+
+// Tiles i0 .. i1 - 1 of a unit's n (at least 1); g0: the CTA's tiles before it.  head -1: no more.
+template <int TN>
+struct Item {
+    Unit<TN> u;
+    int row, head, i0, i1, n, tiles;
+    uint32_t g0;
+};
+
+template <int TN, int ROWS>
+struct __align__(16) Shared {
+    uint64_t full[MAX_SLOTS], empty[MAX_SLOTS];
+    uint64_t s_full[2], p_ready, pv_done, q_full[2], item_full[2], item_free[2], drained;
+    Item<TN> item[2];
+    Scan scan;
+    uint32_t tmem;
+    volatile int abort;
+    float other[2][128 / ROWS][ROWS];  // what the threads of a row tell each other
+};
+
+template <int NC, int ROWS>
+struct Sizes {
+    static constexpr int TN = NC <= 2 ? 128 : 64;   // keys of a tile
+    static constexpr int NQ = 128 / ROWS;           // threads of a row
+    static constexpr int C = TN / NQ;               // keys of a tile that a thread has
+    static constexpr int W = 64 / NQ;               // and columns of an output chunk
+    static constexpr int CHUNK = TN * 128;
+    static constexpr int Q_CHUNK = ROWS * 128, Q_BYTES = NC * Q_CHUNK;
+    static constexpr int P_BYTES = TN / 64 * ROWS * 128;
+    static constexpr int CTAS = ROWS == 32 && NC <= 2 ? 2 : 1;  // of an SM
+    static constexpr int EXTRA = static_cast<int>(sizeof(Shared<TN, ROWS>));
+    static constexpr int LEFT = (CTAS == 2 ? 113 : 227) * 1024 - EXTRA - 2 * Q_BYTES - P_BYTES;
+    static constexpr int SLOTS = LEFT / CHUNK < MAX_SLOTS ? LEFT / CHUNK : MAX_SLOTS;
+    static constexpr int NEED = 2 * Q_BYTES + P_BYTES + SLOTS * CHUNK + EXTRA;
+    // (a CTA alone on its SM takes more than half of the SM's)
+    static constexpr int SMEM = CTAS == 1 && NEED < 120 * 1024 ? 120 * 1024 : NEED;
+    static constexpr int S_COL = 0, O_COL = 2 * C;
+    static constexpr int COLS = O_COL + NC * W <= 128 ? 128 : 256;
+    static_assert(SLOTS > 2 * NC, "a tile's keys and values and the start of the next");
+    static_assert(O_COL + NC * W <= 256, "tensor memory");
+    // the slot n chunks on (at most SLOTS), and whether that is around the end
+    static __device__ __forceinline__ void step(int &s, uint32_t &ph, int n) {
+        s += n;
+        if (s >= SLOTS) {
+            s -= SLOTS;
+            ph ^= 1;
+        }
+    }
+};
+
+// D[ROWS, n] (+)= A[ROWS, 16] B[16, n], the accumulator folded into 128 lanes: lanes q * ROWS ..
+// hold the columns q * n / NQ ..
+__device__ __forceinline__ void mma_ws(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.ws.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// A chunk whose rows are the products' K axis.
+__device__ __forceinline__ uint64_t smem_desc_rows_k(uint32_t addr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(1) << 16;  // (unused: one chunk of 64 columns)
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+template <typename T>
+__host__ __device__ constexpr uint32_t idesc_of(int m, int n, bool b_rows_k) {
+    return (1u << 4) | (T::mma_format << 7) | (T::mma_format << 10) |
+           (static_cast<uint32_t>(b_rows_k) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(m >> 4) << 24);
+}
+// N columns of this thread's lane (no wait), and back.
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t *x) {
+    if constexpr (N == 16) {
+        tmem_ld16(addr, *reinterpret_cast<uint32_t(*)[16]>(x));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 32) tmem_ld32(addr + i, *reinterpret_cast<uint32_t(*)[32]>(x + i));
+    }
+}
+
+template <typename T, int NC, int ROWS>
+__global__ void __launch_bounds__(NTHREADS, Sizes<NC, ROWS>::CTAS)
+k_heads_few(const __grid_constant__ Maps maps, const Params p) {
+    extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's period
+    using Z = Sizes<NC, ROWS>;
+    constexpr int TN = Z::TN, NQ = Z::NQ, C = Z::C, W = Z::W, CHUNK = Z::CHUNK;
+    const uint32_t q_s = smem_addr(smem), p_s = q_s + 2 * Z::Q_BYTES, ring = p_s + Z::P_BYTES;
+    Shared<TN, ROWS> &sh = *reinterpret_cast<Shared<TN, ROWS> *>(smem + Z::SMEM - Z::EXTRA);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (warp == 0) {
+        if (lane < MAX_SLOTS) {
+            mbar_init(&sh.full[lane], 1);
+            mbar_init(&sh.empty[lane], 1);
+        } else if (lane == 16) {
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&sh.s_full[i], 1);
+                mbar_init(&sh.q_full[i], 32);
+                mbar_init(&sh.item_full[i], 1);
+                mbar_init(&sh.item_free[i], 6);  // the producer, the issuer, four softmax warps
+            }
+            mbar_init(&sh.p_ready, 128);
+            mbar_init(&sh.pv_done, 1);
+            mbar_init(&sh.drained, 1);
+            sh.abort = 0;
+        } else if (lane == 17) {
+            prefetch_map(&maps.k);
+            prefetch_map(&maps.v);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    // (tensor memory is taken only once the kernel before has ended: holding it would stop that
+    // kernel's blocks, if they were still to take theirs)
+    pdl_wait_primary();
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_addr(&sh.tmem)),
+                     "r"(static_cast<uint32_t>(Z::COLS))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    Walk<TN> walk;
+    const Cut cut = find_start<TN, NTHREADS>(p, sh.scan, 6, walk);
+    const auto next = [&](Item<TN> &it) {
+        const bool more = walk.next(p, cut, it.u, it.i0, it.i1, it.n);
+        it.row = walk.row;
+        it.head = more ? walk.head : -1;
+        it.tiles = more ? max(0, min(it.i1, it.u.tiles(p)) - it.i0) : 0;
+        return more;
+    };
+    if (warp == 6) {
+        Item<TN> it = {};
+        next(it);
+        if (lane == 0) sh.item[0] = it;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    // Every role goes through the CTA's items: is there one after number `item`, and no abort?
+    const auto next_item = [&](uint32_t item) {
+        ++item;
+        return wait_far(sh, &sh.item_full[item & 1], ((item - 1) >> 1) & 1) && sh.item[item & 1].head >= 0;
+    };
+
+    if (sh.item[0].head < 0) {
+        // nothing: fewer tiles than CTAs
+    } else if (warp == 0) {
+        // ---- producer: a box of a tile a lane
+        const int boxes = TN / p.box_rows;
+        const auto all = [](bool yes) { return __all_sync(0xFFFFFFFFu, yes) != 0; };
+        int s = 0, filled = 0;
+        uint32_t ph = 1;  // phase of the slot's release
+        bool ok = true;
+        for (uint32_t item = 0;; ++item) {
+            const Item<TN> my = sh.item[item & 1];
+            const int32_t *table = p.block_table + static_cast<int64_t>(my.row) * p.max_pages;
+            int2 box = {};
+            const auto look = [&](int i) {
+                box = find_box(p, table, my.u.key_tile(my.i0 + i) * TN + lane * p.box_rows, my.u.len, lane < boxes);
+            };
+            if (my.tiles > 0) look(0);
+            for (int i = 0; ok && i < my.tiles; ++i) {
+                const int2 to = box;
+                if (i + 1 < my.tiles) look(i + 1);
+#pragma unroll
+                for (int c = 0; c < 2 * NC; ++c) {
+                    if (!all(wait(sh, &sh.empty[s], ph))) {
+                        ok = false;
+                        break;
+                    }
+                    ++filled;
+                    if (lane == 0) mbar_expect_tx(&sh.full[s], CHUNK);
+                    __syncwarp();
+                    if (lane < boxes)
+                        tma_load_4d(ring + s * CHUNK + lane * p.box_rows * 128, c < NC ? &maps.k : &maps.v,
+                                    c % NC * 64, my.head, to.y, to.x, &sh.full[s]);
+                    __syncwarp();
+                    Z::step(s, ph, 1);
+                }
+            }
+            if (lane == 0) mbar_arrive(&sh.item_free[item & 1]);
+            if (!ok || !all(next_item(item))) break;
+        }
+        if (__any_sync(0xFFFFFFFFu, sh.abort)) {
+            // let the copies in flight land (the last fill of each barrier)
+            for (int k = 0; k < Z::SLOTS; ++k) {
+                const int fills = (filled + Z::SLOTS - 1 - k) / Z::SLOTS;
+                if (fills > 0) wait_out(&sh.full[k], (fills - 1) & 1);
+            }
+        }
+    } else if (warp == 1) {
+        if (elect_one()) {
+            // ---- MMA issuer.  Two kinds of work wait for different things: the scores of tile a
+            // for its keys, the products of tile b for its weights and values.  Whichever is there
+            // is issued, the products first, since they free slots.
+            constexpr uint32_t id_s = idesc_of<T>(ROWS, TN, false), id_o = idesc_of<T>(ROWS, 64, true);
+            const uint64_t qd = smem_desc_sw128(q_s), pd = smem_desc_sw128(p_s);
+            const uint64_t kd = smem_desc_sw128(ring), vd = smem_desc_rows_k(ring);
+            int sa = 0, sb = NC;            // the next slots of tile a's keys and tile b's values
+            uint32_t pa = 0, pb = 0;        // their phases
+            uint32_t ga = 0, gb = 0;        // the numbers of tiles a and b
+            uint32_t ahead = 0, firsts = 0, idle = 0;  // tiles between; which are their item's first
+            const auto products = [&]() {
+                bool there = ahead > 0 && mbar_poll(&sh.p_ready, gb & 1);
+                {
+                    int k = sb;
+                    uint32_t ph = pb;
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        there = there && mbar_poll(&sh.full[k], ph);
+                        Z::step(k, ph, 1);
+                    }
+                }
+                if (!there) {
+                    if (++idle > POLL_LIMIT) sh.abort = 1;
+                    return;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    const uint64_t v = vd + sb * (CHUNK >> 4);
+#pragma unroll
+                    for (int u = 0; u < TN / 16; ++u)
+                        mma_ws(tmem + Z::O_COL + c * W, pd + (u >> 2) * (Z::Q_CHUNK >> 4) + 2 * (u & 3),
+                               v + u * (2048 >> 4), id_o, !(firsts & 1) || u > 0);
+                    mma_commit(&sh.empty[sb]);
+                    Z::step(sb, pb, 1);
+                }
+                mma_commit(&sh.pv_done);
+                Z::step(sb, pb, NC);
+                ++gb;
+                --ahead;
+                firsts >>= 1;
+                idle = 0;
+            };
+            // waits for a fill, with products between the polls
+            const auto filled = [&](uint64_t *bar, uint32_t phase) {
+                do {
+                    products();
+                } while (!mbar_poll(bar, phase) && !sh.abort);
+                idle = 0;
+                tc_fence_after();
+                return !sh.abort;
+            };
+            for (uint32_t item = 0;; ++item) {
+                const int tiles = sh.item[item & 1].tiles;
+                mbar_arrive(&sh.item_free[item & 1]);
+                const uint64_t q = qd + (item & 1) * (Z::Q_BYTES >> 4);
+                if (!filled(&sh.q_full[item & 1], (item >> 1) & 1)) break;
+                for (int i = 0; i < tiles && !sh.abort; ++i) {
+                    while (ahead > 1 && !sh.abort) products();  // the scores' buffer is free
+                    const uint32_t d = tmem + Z::S_COL + (ga & 1) * C;
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        if (!filled(&sh.full[sa], pa)) break;
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            mma_ws(d, q + c * (Z::Q_CHUNK >> 4) + 2 * u, kd + sa * (CHUNK >> 4) + 2 * u, id_s,
+                                   (c | u) != 0);
+                        mma_commit(&sh.empty[sa]);
+                        Z::step(sa, pa, 1);
+                    }
+                    if (sh.abort) break;
+                    mma_commit(&sh.s_full[ga & 1]);
+                    Z::step(sa, pa, NC);
+                    firsts |= static_cast<uint32_t>(i == 0) << ahead;
+                    ++ga;
+                    ++ahead;
+                }
+                // (the next item is known one ahead; while it is not, products go on)
+                const uint32_t nxt = item + 1;
+                uint64_t *bar = &sh.item_full[nxt & 1];
+                while (!sh.abort && !mbar_poll(bar, ((nxt - 1) >> 1) & 1)) products();
+                idle = 0;
+                if (sh.abort || sh.item[nxt & 1].head < 0) break;
+            }
+            while (ahead > 0 && !sh.abort) products();
+            mma_commit(&sh.drained);
+            wait_out(&sh.drained, 0);
+        }
+    } else if (warp == 6) {
+        // ---- the items, each published when the one two before it is left behind, and their queries
+        Item<TN> it = sh.item[0];
+        for (uint32_t item = 0;; ++item) {
+            const uint32_t to = q_s + (item & 1) * Z::Q_BYTES;
+            const int rows = it.u.nq * p.G - it.u.m0;
+#pragma unroll 8
+            for (int v = lane; v < ROWS * NC * 8; v += 32) {
+                const int r = v / (NC * 8), cv = v % (NC * 8), m = it.u.m0 + r, tok = m / p.G;
+                const bool real = r < rows && cv * 8 < p.D;
+                const uint16_t *src = p.q + (it.u.q0 + tok) * p.q_tok + (it.head * p.G + m - tok * p.G) * p.q_head + cv * 8;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                 to + (cv >> 3) * Z::Q_CHUNK + r * 128 + (((cv & 7) ^ (r & 7)) << 4)),
+                             "l"(real ? src : p.q), "r"(real ? 16 : 0)
+                             : "memory");
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_async_smem();
+            mbar_arrive(&sh.q_full[item & 1]);
+            it.g0 += it.tiles;
+            const bool more = next(it);
+            if (!__all_sync(0xFFFFFFFFu, item == 0 || wait_far(sh, &sh.item_free[(item - 1) & 1],
+                                                               ((item - 1) >> 1) & 1)))
+                break;
+            if (lane == 0) {
+                sh.item[(item + 1) & 1] = it;
+                mbar_arrive(&sh.item_full[(item + 1) & 1]);
+            }
+            __syncwarp();
+            if (!more) break;
+        }
+    } else {
+        // ---- softmax: NQ threads a row, C of a tile's keys each
+        const int wq = warp & 3, tid = threadIdx.x - SOFTMAX0;
+        const int r = (wq * 32 + lane) % ROWS, part = (wq * 32 + lane) / ROWS;
+        const uint32_t trow = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+        int slot = 0;
+        // the threads of a row meet, and each sees the others' values
+        const auto meet = [&](float v, auto join) {
+            sh.other[slot][part][r] = v;
+            if constexpr (ROWS == 64)
+                asm volatile("bar.sync %0, 64;" ::"r"(1 + (wq & 1)) : "memory");
+            else
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+            for (int k = 1; k < NQ; ++k) v = join(v, sh.other[slot][(part + k) % NQ][r]);
+            slot ^= 1;
+            return v;
+        };
+        uint32_t g = 0;
+        for (uint32_t item = 0;; ++item) {
+            const volatile Item<TN> &my = sh.item[item & 1];
+            const int tiles = my.tiles, i0 = my.i0, ns = my.u.ns, skip = my.u.w0 - ns, len = my.u.len;
+            const int m0 = my.u.m0, base = len - my.u.nq, rows = my.u.nq * p.G - m0;
+            const int tail = (len % TN != 0 ? ns + len / TN - my.u.w0 : -1) - i0;
+            const int sure = base + m0 / p.G + 1;             // one past the last key of the first row,
+            const int limit = base + (m0 + r) / p.G + 1;      // of this one,
+            const int most = base + (m0 + min(ROWS, rows) - 1) / p.G + 1;  // and of the last
+            const int width = p.window > 0 && p.window < len ? p.window : 0;
+            float m_ref = -INFINITY, l = 0.0f;
+            for (int j = 0; j < tiles; ++j, ++g) {
+                wait_long(sh, &sh.s_full[g & 1], (g >> 1) & 1);
+                tc_fence_after();
+                uint32_t x[C];
+                tmem_load<C>(trow + Z::S_COL + (g & 1) * C, x);
+                tmem_wait_ld();
+                const int key0 = (i0 + j < ns ? i0 + j : i0 + j + skip) * TN;
+                if (__builtin_expect(key0 + TN > sure || (width && key0 < most - width), 0)) {
+                    // more than every row sees
+                    const int seen = limit - key0 - part * C;
+                    const int low = width ? seen - width : -1, first = p.sinks - key0 - part * C;
+#pragma unroll
+                    for (int i = 0; i < C; ++i)
+                        if (i >= seen || (i < low && i >= first)) x[i] = 0xFF800000u;
+                }
+                float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < C; i += 2)
+                    top4[(i >> 1) & 3] = max3(top4[(i >> 1) & 3], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+                const float top = meet(fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]),
+                                       [](float a, float b) { return fmaxf(a, b); }) * p.scale2;
+                const bool raise = top > m_ref + (LAZY + T::first_weight);
+                const float m_old = m_ref;
+                if (raise) m_ref = top - T::first_weight;
+                const float m_use = m_ref == -INFINITY ? 0.0f : m_ref;
+                const uint64_t scale_2 = pack2(p.scale2, p.scale2), minus_m = pack2(-m_use, -m_use);
+                uint64_t sums[2] = {0, 0};  // two pairs of sums
+                uint4 weights[C / 8];
+#pragma unroll
+                for (int v = 0; v < C / 8; ++v) {
+                    float e[8];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        float e0, e1;
+                        unpack2(fma2(pack2(__uint_as_float(x[8 * v + 2 * u]), __uint_as_float(x[8 * v + 2 * u + 1])),
+                                     scale_2, minus_m), e0, e1);
+                        e[2 * u] = ex2(e0);
+                        e[2 * u + 1] = ex2(e1);
+                        sums[u & 1] = add2(sums[u & 1], pack2(e[2 * u], e[2 * u + 1]));
+                    }
+                    weights[v] = float_to_half8<T>(e);
+                }
+                // the products of the tile before are done: the weights' buffer and the output are
+                // free to change
+                if (g > 0) wait(sh, &sh.pv_done, (g - 1) & 1);
+                if (__builtin_expect(j > 0 && __any_sync(0xFFFFFFFFu, raise), 0)) {
+                    tc_fence_after();
+                    const float f = raise ? ex2(m_old - m_ref) : 1.0f;
+                    l *= f;
+#pragma unroll 1
+                    for (int c = 0; c < NC * W; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(trow + Z::O_COL + c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st16(trow + Z::O_COL + c, o);
+                    }
+                    tmem_wait_st();
+                }
+                float l0, l1;
+                unpack2(add2(sums[0], sums[1]), l0, l1);
+                l += l0 + l1;
+#pragma unroll
+                for (int v = 0; v < C / 8; ++v) {
+                    const int at = part * (C / 8) + v;  // 16 bytes of the row's 2 TN
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     p_s + (at >> 3) * Z::Q_CHUNK + r * 128 + (((at & 7) ^ (r & 7)) << 4)),
+                                 "r"(weights[v].x), "r"(weights[v].y), "r"(weights[v].z), "r"(weights[v].w)
+                                 : "memory");
+                }
+                if (__builtin_expect(j == tail, 0)) {
+                    // value rows behind the row's last key: whatever lies there must not meet the
+                    // zero weights
+                    const int z0 = len % TN;
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        const uint32_t n = g * (2 * NC) + NC + c, at = n % Z::SLOTS;
+                        wait(sh, &sh.full[at], (n / Z::SLOTS) & 1);
+                        for (int i = tid; i < (TN - z0) * 8; i += 128)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                             ring + at * CHUNK + z0 * 128 + i * 16),
+                                         "r"(0)
+                                         : "memory");
+                    }
+                }
+                fence_async_smem();
+                tc_fence_before();
+                mbar_arrive(&sh.p_ready);
+            }
+            // ---- epilogue
+            l = meet(l, [](float a, float b) { return a + b; });
+            if (tiles > 0) {
+                wait(sh, &sh.pv_done, (g - 1) & 1);
+                tc_fence_after();
+            }
+            // (a sum of zero: nothing was seen; one that is NaN stays so)
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const float lse2 = l == 0.0f ? -INFINITY : m_ref + log2f(l);
+            const bool real = r < rows, whole = i0 == 0 && my.i1 == my.n;
+            const int tok = (m0 + r) / p.G, h = my.head * p.G + m0 + r - tok * p.G;
+            const int64_t out_row = my.u.q0 + tok;
+            const int64_t part_row = static_cast<int64_t>(2 * blockIdx.x + (i0 > 0 ? 0 : 1)) * ROWS + r;
+            if (real && part == 0) {
+                if (!whole)
+                    p.part_lse[part_row] = lse2;
+                else if (p.lse)
+                    p.lse[out_row * p.Hq + h] = lse2 * LN2;
+            }
+            uint16_t *dst = p.out + out_row * p.out_tok + h * p.out_head + part * W;
+            float *pdst = p.part + part_row * (64 * NC) + part * W;
+            // 32 bytes a store, a whole sector, where the rows allow it
+            const bool sectors = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                uint32_t o[W] = {};
+                if (tiles > 0) {
+                    tmem_load<W>(trow + Z::O_COL + c * W, o);
+                    tmem_wait_ld();
+                }
+                if (!real) continue;
+#pragma unroll
+                for (int v = 0; v < W; v += 16) {
+                    float f[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) f[i] = tiles > 0 ? __uint_as_float(o[v + i]) * inv : 0.0f;
+                    if (whole) {
+                        if (c * 64 + part * W + v >= p.D) continue;
+                        uint32_t y[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) y[i] = T::narrow2(f[2 * i], f[2 * i + 1]);
+                        uint16_t *d = dst + c * 64 + v;
+                        if (sectors) {
+                            st_global_32B(d, y);
+                        } else {
+                            *reinterpret_cast<uint4 *>(d) = make_uint4(y[0], y[1], y[2], y[3]);
+                            *reinterpret_cast<uint4 *>(d + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            uint32_t y[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) y[i] = __float_as_uint(f[8 * k + i]);
+                            st_global_32B(pdst + c * 64 + v + 8 * k, y);
+                        }
+                    }
+                }
+            }
+            // The next item's products overwrite this output once its first weights are there, which
+            // come after these reads.
+            tc_fence_before();
+            __syncwarp();  // the whole warp is done with the item
+            if (lane == 0) mbar_arrive(&sh.item_free[item & 1]);
+            // (the warps that share rows leave together: they meet in everything they do)
+            bool more = next_item(item);
+            uint32_t every;
+            __syncwarp();
+            if constexpr (ROWS == 64)
+                asm volatile(
+                    "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
+                    "bar.red.and.pred p, %1, 64, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                    : "=r"(every)
+                    : "r"(1 + (wq & 1)), "r"(static_cast<uint32_t>(more))
+                    : "memory");
+            else
+                asm volatile(
+                    "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+                    "bar.red.and.pred p, 1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                    : "=r"(every)
+                    : "r"(static_cast<uint32_t>(more))
+                    : "memory");
+            if (!every) break;
+        }
+    }
+    if (warp == 6) walk.close(p);
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        pdl_launch_dependents();
+        if (sh.abort && p.status) atomicOr(p.status, MTPSPEC_STATUS_TIMEOUT);
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(static_cast<uint32_t>(Z::COLS))
+                     : "memory");
+    }
+}
+
+struct Layout {
+    size_t plan, part, lse, total;
+};
+Layout layout(int rows, int ctas, int NC) {
+    const auto align256 = [](size_t n) { return (n + 255) & ~static_cast<size_t>(255); };
+    const size_t slots = static_cast<size_t>(2) * ctas * SMS;
+    Layout y;
+    y.plan = 0;
+    y.part = align256(slots * sizeof(Plan));
+    y.lse = y.part + slots * rows * (64 * NC) * 4;
+    y.total = y.lse + align256(slots * rows * 4);
+    return y;
+}
+
+template <typename T, int NC, int ROWS>
+cudaError_t launch(const HeadsAttnArgs &a, cudaStream_t stream) {
+    using Z = Sizes<NC, ROWS>;
+    const Layout y = layout(ROWS, Z::CTAS, NC);
+    Params p;
+    Maps maps;
+    if (!set_up(a, ROWS, 1, Z::TN, y.plan, y.part, y.lse, p, maps)) return cudaErrorInvalidValue;
+    static AttrCache attr;
+    cudaError_t e = ensure_attr(k_heads_few<T, NC, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::SMEM, attr);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(Z::CTAS * SMS);
+    cfg.blockDim = dim3(NTHREADS);
+    cfg.dynamicSmemBytes = Z::SMEM;
+    cfg.stream = stream;
+    cfg.attrs = pdl_attr();  // set up beside the end of whatever the stream runs before
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, k_heads_few<T, NC, ROWS>, maps, p);
+    if (e != cudaSuccess) return e;
+    count_launches(1);
+    cfg.gridDim = dim3(ROWS / JOIN_WARPS, Z::CTAS * SMS);
+    cfg.blockDim = dim3(JOIN_THREADS);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, k_heads_join<T, NC, ROWS, 1>, p);
+    if (e == cudaSuccess) count_launches(1);
+    return e;
+}
+template <typename T, int ROWS>
+cudaError_t pick(const HeadsAttnArgs &a, cudaStream_t s) {
+    return a.D <= 64 ? launch<T, 1, ROWS>(a, s) : a.D <= 128 ? launch<T, 2, ROWS>(a, s) : launch<T, 4, ROWS>(a, s);
+}
+
+}  // namespace hfw
+
+size_t heads_few_workspace_bytes(int32_t D, bool rows32) {
+    const int NC = D <= 64 ? 1 : D <= 128 ? 2 : 4;
+    return hfw::layout(rows32 ? 32 : 64, rows32 && NC <= 2 ? 2 : 1, NC).total;
+}
+
+cudaError_t run_heads_few(const HeadsAttnArgs &a, bool rows32, int dtype, cudaStream_t stream) {
+    if (dtype == MTPSPEC_BF16)
+        return rows32 ? hfw::pick<Bf16, 32>(a, stream) : hfw::pick<Bf16, 64>(a, stream);
+    return rows32 ? hfw::pick<F16, 32>(a, stream) : hfw::pick<F16, 64>(a, stream);
+}
+
+}  // namespace mtpspec
