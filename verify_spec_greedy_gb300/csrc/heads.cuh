@@ -325,61 +325,94 @@ __device__ __forceinline__ int2 find_box(const Params &p, const int32_t *table, 
     return make_int2(page, slot);
 }
 
+// Partial outputs lie by fours of columns, the rows side by side (a thread that has a row's columns
+// writes beside its neighbours): float4 number ((slot * TILES + tile) * 16 NC + column / 4) * TM + row.
+template <int NC, int TM, int TILES>
+__device__ __forceinline__ float4 *part_at(const Params &p, int slot, int tile, int column, int row) {
+    return reinterpret_cast<float4 *>(p.part) +
+           (static_cast<int64_t>(slot * TILES + tile) * (16 * NC) + column / 4) * TM + row;
+}
+
 // Units cut among CTAs: each row's partial outputs, weighted by their sums, become the output.  A
-// warp a row; blockIdx.y is the CTA of the first kernel in which the unit starts.  A slot holds
-// TILES tiles of TM rows, of which tile_rows are used.
+// block takes 32 rows, a row a lane; blockIdx.y is the CTA of the first kernel in which the unit
+// starts.  Its eight warps take the columns, or, with SPREAD, for units cut into many parts, an
+// eighth of the parts each, and blockIdx.z the columns.
 constexpr int JOIN_THREADS = 256, JOIN_WARPS = JOIN_THREADS / 32;
 
-template <typename T, int NC, int TM, int TILES>
+template <typename T, int NC, int TM, int TILES, bool SPREAD>
 __global__ void __launch_bounds__(JOIN_THREADS) k_heads_join(const Params p) {
+    constexpr int COLS = 8 * NC, QUADS = 2 * NC;  // of a warp
+    __shared__ float shared[SPREAD ? JOIN_WARPS : 1][SPREAD ? 32 : 1][COLS + 2];
     pdl_wait_primary();
     const Plan u = p.plan[blockIdx.y];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rr = blockIdx.x * JOIN_WARPS + warp, r = rr % TM, in = rr / TM * p.tile_rows + r;
+    const int rr = blockIdx.x * 32 + lane, tile = rr / TM, r = rr % TM, in = tile * p.tile_rows + r;
     // (what an aborted call left there is checked)
-    if (u.parts < 2 || u.parts > static_cast<int>(gridDim.y - blockIdx.y) || r >= p.tile_rows || in >= u.rows ||
-        u.q0 < 0 || u.m0 < 0 || u.q0 + (u.m0 + in) / p.G >= p.Tq || u.head < 0 || u.head >= p.Hkv)
+    if (u.parts < 2 || u.parts > static_cast<int>(gridDim.y - blockIdx.y) || u.q0 < 0 || u.m0 < 0 ||
+        u.q0 + (u.m0 + u.rows - 1) / p.G >= p.Tq || u.head < 0 || u.head >= p.Hkv ||
+        blockIdx.x * 32 / TM * p.tile_rows + blockIdx.x * 32 % TM >= u.rows)
         return;
-    const int m = u.m0 + in, h = u.head * p.G + m % p.G;
-    // a CTA's partial of this row: the second slot where the unit starts, else the first
-    const auto part_row = [&](int i) {
-        return static_cast<int64_t>(2 * (blockIdx.y + i) + (i == 0)) * (TILES * TM) + rr;
-    };
+    // a CTA's partial: the second slot where the unit starts, else the first
+    const auto slot = [&](int i) { return static_cast<int>(2 * (blockIdx.y + i) + (i == 0)); };
+    const auto lse2 = [&](int i) { return p.part_lse[static_cast<int64_t>(slot(i)) * (TILES * TM) + rr]; };
+    const bool real = r < p.tile_rows && in < u.rows;
+    const int col = (SPREAD ? blockIdx.z : warp) * COLS;
     float top = -INFINITY, sum = 0.0f;
-    for (int i = lane; i < u.parts; i += 32) top = fmaxf(top, p.part_lse[part_row(i)]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    const float ref = top == -INFINITY ? 0.0f : top;
-    constexpr int PER = 2 * NC;  // a lane's columns
-    float acc[PER] = {};
+    float acc[COLS] = {};
+    if (real) {
 #pragma unroll 4
-    for (int i = 0; i < u.parts; ++i) {
-        const int64_t row = part_row(i);
-        const float w = exp2f(p.part_lse[row] - ref);
-        sum += w;
-        float v[PER];
+        for (int i = 0; i < u.parts; ++i) top = fmaxf(top, lse2(i));
+        const float ref = top == -INFINITY ? 0.0f : top;
+#pragma unroll 4
+        for (int i = SPREAD ? warp : 0; i < u.parts; i += SPREAD ? JOIN_WARPS : 1) {
+            const float w = exp2f(lse2(i) - ref);
+            float4 v[QUADS];
 #pragma unroll
-        for (int k = 0; k < PER; k += 2)
-            *reinterpret_cast<float2 *>(v + k) =
-                *reinterpret_cast<const float2 *>(p.part + row * (64 * NC) + k * 32 + lane * 2);
+            for (int k = 0; k < QUADS; ++k) v[k] = *part_at<NC, TM, TILES>(p, slot(i), tile, col + 4 * k, r);
+            sum += w;
 #pragma unroll
-        for (int k = 0; k < PER; ++k) acc[k] += w * v[k];
+            for (int k = 0; k < QUADS; ++k) {
+                acc[4 * k] += w * v[k].x;
+                acc[4 * k + 1] += w * v[k].y;
+                acc[4 * k + 2] += w * v[k].z;
+                acc[4 * k + 3] += w * v[k].w;
+            }
+        }
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int64_t out_row = u.q0 + m / p.G;
-    uint16_t *dst = p.out + out_row * p.out_tok + h * p.out_head;
+    if (SPREAD) {
 #pragma unroll
-    for (int k = 0; k < PER; k += 2)
-        if (k * 32 + lane * 2 < p.D)
-            *reinterpret_cast<uint32_t *>(dst + k * 32 + lane * 2) = T::narrow2(acc[k] * inv, acc[k + 1] * inv);
-    if (p.lse && lane == 0) p.lse[out_row * p.Hq + h] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * LN2;
+        for (int k = 0; k < COLS; ++k) shared[warp][lane][k] = acc[k];
+        shared[warp][lane][COLS] = sum;
+        __syncthreads();
+        if (warp != 0) return;
+#pragma unroll
+        for (int w = 1; w < JOIN_WARPS; ++w) {
+#pragma unroll
+            for (int k = 0; k < COLS; ++k) acc[k] += shared[w][lane][k];
+            sum += shared[w][lane][COLS];
+        }
+    }
+    if (!real) return;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int m = u.m0 + in, tok = m / p.G, head = u.head * p.G + m - tok * p.G;
+    const int64_t out_row = u.q0 + tok;
+    uint16_t *dst = p.out + out_row * p.out_tok + head * p.out_head + col;
+#pragma unroll
+    for (int k = 0; k < COLS; k += 8) {
+        if (col + k >= p.D) break;
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = acc[k + i] * inv;
+        *reinterpret_cast<uint4 *>(dst + k) = float_to_half8<T>(f);
+    }
+    if (p.lse && col == 0) p.lse[out_row * p.Hq + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * LN2;
 }
 
 // The parameters and tensor maps of a call whose row tiles hold `tile_rows` rows and whose units
-// `tiles` of them; the workspace's parts lie at the given offsets.  The queries' map brings a whole
-// tile of them, as tile_rows / G tokens of G heads, if G divides it; q comes as it is otherwise.
-inline bool set_up(const HeadsAttnArgs &a, int tile_rows, int tiles, int TN, size_t plan, size_t part,
-                   size_t lse, Params &p, Maps &maps) {
+// `tiles` of them; the workspace's parts lie at the given offsets.  The queries' map, if it is asked
+// for, brings a whole tile of them, as tile_rows / G tokens of G heads.
+inline bool set_up(const HeadsAttnArgs &a, int tile_rows, int tiles, int TN, bool q_map, size_t plan,
+                   size_t part, size_t lse, Params &p, Maps &maps) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     p = {};
@@ -406,7 +439,7 @@ inline bool set_up(const HeadsAttnArgs &a, int tile_rows, int tiles, int TN, siz
                      cs[3] = {u(head * 2), u(slot * 2), u(page * 2)};
     const cuuint32_t cb[4] = {64, 1, static_cast<cuuint32_t>(p.box_rows), 1};
     if (!encode(&maps.k, a.k_cache, cd, cs, cb) || !encode(&maps.v, a.v_cache, cd, cs, cb)) return false;
-    if (tiles == 2) {
+    if (q_map) {
         const cuuint64_t qd[4] = {u(a.D), u(p.G), u(a.Tq), u(a.Hkv)},
                          qs[3] = {u(q_head * 2), u(q_tok * 2), u(q_head * p.G * 2)};
         const cuuint32_t qb[4] = {64, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(tile_rows / p.G), 1};

@@ -9,14 +9,17 @@
 // are subnormal: half_types.cuh.)
 //
 // Rows: the G = Hq / Hkv query heads of a key head meet the same keys, so a tile's 128 rows are
-// TOK = 128 / G tokens times G heads.  A pair of such tiles is a unit of work: while the tensor
-// cores work on one tile's products, the other tile's softmax runs, eight warps a tile, two threads
-// a row.  Tensor memory holds both tiles' scores (128 columns each, whose first half becomes the
-// weights, the left operand of the second product) and outputs.
+// 128 / G tokens times G heads.  A unit of work is two such tiles (one, for heads of more than 128
+// elements), a thread a row in the softmax.
 //
-// Keys: tiles of 128 positions, two of them with their values on their way or in use.  A tile is
-// brought in boxes that stay within a page, up to sixteen of them, one a lane of the producing
-// warp.  With a window, a unit meets the tiles of the first tokens, then those of the window.
+// Keys: tiles of 64.  A row tile has two score buffers of 64 columns in tensor memory (whose first
+// half becomes the weights, the left operand of the second product) beside its output: 512 columns
+// in all.  So the scores of a tile are there before the weights of the one before are, and no
+// row tile's chain scores - softmax - products is waited for from end to end.  (Tiles of 128 keys
+// with one buffer each: a round of both row tiles took 3,700 cycles for 2,048 of products.)
+//
+// A tile is brought in boxes that stay within a page, a box a lane of the producing warp.  With a
+// window, a unit meets the tiles of the first tokens, then those of the window.
 //
 // Work: all units laid end to end, a unit's length its key tiles and a constant for its start and
 // end, and cut evenly over 152 CTAs, one a multiprocessor, whatever the lengths; every CTA finds
@@ -32,47 +35,39 @@ namespace hch {
 using namespace heads;
 
 constexpr int TM = 128;            // rows of a tile in tensor memory
-constexpr int TN = 128;            // keys of a tile
-constexpr int CHUNK = TN * 128;    // bytes of 128 rows x 64 columns of 16 bits
-constexpr int NTHREADS = 640;      // warp 0 TMA, 1 MMA, 2 next work, 3 TMEM; 4-11, 12-19 softmax
+constexpr int TN = 64;             // keys of a tile
+constexpr int Q_CHUNK = TM * 128;  // bytes of a row tile x 64 columns of 16 bits
+constexpr int CHUNK = TN * 128;    // and of a key tile
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int S_COL = 0, O_COL = 256;  // tile t: + 128 t
+constexpr int O_COL = 256;         // row tile t's scores: 128 t + 64 (buffer), its output: 256 + 128 t
+constexpr int ITEMS = 4;
 
-// An item of a CTA: tiles i0 .. i1 - 1 of a unit's list; with the key tiles before it, and the
-// items before it in which either row tile had keys to meet, and the key tiles that it met (as
-// far as parities go).  head -1: no more.
+// An item of a CTA: tiles i0 .. i1 - 1 of a unit's list of n (at least 1); how many of them either
+// row tile meets, and which of them the row's keys end in, if that is not a whole tile; with the key
+// tiles before it, and the key tiles that either row tile met before.  head -1: no more.
 struct Item {
     Unit<TN> u;
-    int row, head, i0, i1, n;   // n: the unit's tiles, at least 1
-    uint32_t g0, outputs[2], met[2];
+    int row, head, i0, i1, n;
+    int nt[2], tail;
+    uint32_t g0, met[2];
+    __device__ __forceinline__ int tiles() const { return max(nt[0], nt[1]); }
+    // the row tile that uses every chunk last
+    __device__ __forceinline__ int last() const { return nt[1] >= nt[0] ? 1 : 0; }
 };
 
+constexpr int MAX_RING = 8;
+// Barriers by row tile are doubled, a phase for every other key tile: who waits for a tile may be one
+// behind, and a parity cannot tell two phases from none.
 struct __align__(16) Shared {
-    uint64_t k_full[2], v_full[2], k_free[2], v_free[2];  // by the tile's number mod 2
-    uint64_t q_full[2], q_free[2], s_full[2], p_ready[2], o_done[2], v_clean, drained;
-    uint64_t item_full[2], item_free[2];
-    Item item[2];
+    uint64_t k_full[MAX_RING], v_full[MAX_RING], k_free[MAX_RING], v_free[MAX_RING];  // by the tile's slot
+    uint64_t q_full[2], q_free[2], s_full[2][2], p_ready[2][2], pv_done[2][2], v_clean, drained;
+    uint64_t item_full[ITEMS], item_free[ITEMS];
+    Item item[ITEMS];
     Scan scan;
     uint32_t tmem;
     volatile int abort;
-    float other[2][2][TM];  // what the two threads of a row tell each other, by tile and half
 };
 
-// Whether all of two warps that share rows say yes.  They meet at barrier `bar` in everything they
-// do, so that after a wait that gave up none may go on without the others.
-__device__ __forceinline__ bool both(bool yes, int bar) {
-    uint32_t all;
-    __syncwarp();
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 q, %2, 0;\n\t"
-        "bar.red.and.pred p, %1, 64, q;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(all)
-        : "r"(bar), "r"(static_cast<uint32_t>(yes))
-        : "memory");
-    return all != 0;
-}
 // D[128, n] (+)= A[128, 16] B[16, n], A from tensor memory.
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                        uint32_t accumulate) {
@@ -100,54 +95,51 @@ __host__ __device__ constexpr uint32_t idesc_of(int n, bool b_rows_k) {
            (static_cast<uint32_t>(TM >> 4) << 24);
 }
 
-// What an item's row tiles and its producer go by.
-struct Extent {
-    int n0, n1, n, tail;
-    __device__ __forceinline__ Extent(const Params &p, const Item &it) {
-        n0 = max(0, min(it.i1, it.u.tiles(p, it.u.m0, p.tile_rows)) - it.i0);
-        n1 = max(0, min(it.i1, it.u.tiles(p, it.u.m0 + p.tile_rows, p.tile_rows)) - it.i0);
-        n = max(n0, n1);
-        tail = it.u.tail() - it.i0;  // as far as the item meets it
-        if (tail >= n) tail = -1;
-    }
-    __device__ __forceinline__ int tiles(int t) const { return t ? n1 : n0; }
-    // the tile of rows that uses every chunk last
-    __device__ __forceinline__ int last() const { return n1 >= n0 ? 1 : 0; }
-};
+// NC: the 64-column chunks of a head.
 template <int NC>
 struct Sizes {
-    static constexpr int TILE = 2 * NC, RING = 2 * TILE;   // chunks of a tile's keys and values
+    static constexpr int NT = NC <= 2 ? 2 : 1;                      // row tiles of a unit
+    static constexpr int THREADS = 128 + 128 * NT;                  // warp 0 TMA, 1 MMA, 2 items, 3 TMEM; softmax
+    static constexpr int TILE = 2 * NC * CHUNK, RING = 16 / (2 * NC) < MAX_RING ? 16 / (2 * NC) : MAX_RING;
+    static constexpr int STAGE = 4096;                              // of a softmax warp: 32 rows x 64 columns
+    static constexpr int Q_BYTES = NT * NC * Q_CHUNK, STAGES = Q_BYTES + RING * TILE;
     static constexpr int EXTRA = static_cast<int>(sizeof(Shared));
-    // (more than half of an SM's, so that no two CTAs, which take all its tensor memory, share one)
-    static constexpr int SMEM = ((2 * NC + RING) * CHUNK > 120 * 1024 ? (2 * NC + RING) * CHUNK : 120 * 1024) + EXTRA;
-    static constexpr int COLS = 64 * NC;
+    static constexpr int SMEM = STAGES + 4 * NT * STAGE + EXTRA;
+    static_assert(SMEM <= 232448, "227 KB a CTA");
+    static_assert(SMEM > 116 * 1024, "two CTAs, which take all tensor memory, may not share an SM");
 };
 
-// NC: the 64-column chunks of a head.
 template <typename T, int NC>
-__global__ void __launch_bounds__(NTHREADS, 1)
+__global__ void __launch_bounds__(Sizes<NC>::THREADS, 1)
 k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
     extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's period
     using Z = Sizes<NC>;
-    const uint32_t q_s = smem_addr(smem), ring = q_s + 2 * NC * CHUNK;
+    constexpr int NT = Z::NT, RING = Z::RING;
+    const uint32_t q_s = smem_addr(smem), ring = q_s + Z::Q_BYTES;
     Shared &sh = *reinterpret_cast<Shared *>(smem + Z::SMEM - Z::EXTRA);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int t = 0; t < 2; ++t) {
+        for (int i = 0; i < RING; ++i) {
+            mbar_init(&sh.k_full[i], 1);
+            mbar_init(&sh.v_full[i], 1);
+            mbar_init(&sh.k_free[i], 1);
+            mbar_init(&sh.v_free[i], 1);
+        }
+        for (int t = 0; t < NT; ++t) {
             mbar_init(&sh.q_full[t], 1);
             mbar_init(&sh.q_free[t], 1);
-            mbar_init(&sh.k_full[t], 1);
-            mbar_init(&sh.v_full[t], 1);
-            mbar_init(&sh.k_free[t], 1);
-            mbar_init(&sh.v_free[t], 1);
-            mbar_init(&sh.s_full[t], 1);
-            mbar_init(&sh.p_ready[t], 256);
-            mbar_init(&sh.o_done[t], 1);
-            mbar_init(&sh.item_full[t], 1);
-            mbar_init(&sh.item_free[t], 18);  // the producer, the issuer, sixteen softmax warps
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&sh.s_full[t][b], 1);
+                mbar_init(&sh.p_ready[t][b], 128);
+                mbar_init(&sh.pv_done[t][b], 1);
+            }
         }
-        mbar_init(&sh.v_clean, 256);
+        for (int i = 0; i < ITEMS; ++i) {
+            mbar_init(&sh.item_full[i], 1);
+            mbar_init(&sh.item_free[i], 2 + 4 * NT);  // the producer, the issuer, the softmax warps
+        }
+        mbar_init(&sh.v_clean, 128);
         mbar_init(&sh.drained, 1);
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -167,86 +159,73 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
     }
     // ---- where this CTA starts, and its first item
     Walk<TN> walk;
-    const Cut cut = find_start<TN, NTHREADS>(p, sh.scan, 2, walk);
+    const Cut cut = find_start<TN, Z::THREADS>(p, sh.scan, 2, walk);
     const auto next = [&](Item &it) {
         const bool more = walk.next(p, cut, it.u, it.i0, it.i1, it.n);
         it.row = walk.row;
         it.head = more ? walk.head : -1;
+        it.nt[0] = it.nt[1] = 0;
+        if (more) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                it.nt[t] = max(0, min(it.i1, it.u.tiles(p, it.u.m0 + t * p.tile_rows, p.tile_rows)) - it.i0);
+            it.tail = it.u.tail() - it.i0;
+        }
         return more;
     };
     if (warp == 2) {
         Item it = {};
         next(it);
-        if (lane == 0) sh.item[0] = it;
+        if (lane == 0) {
+            sh.item[0] = it;
+            mbar_arrive(&sh.item_full[0]);
+        }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    // Every role goes through the CTA's items: is there one after number `item`, and no abort?
-    const auto next_item = [&](uint32_t item) {
-        ++item;
-        return wait_far(sh, &sh.item_full[item & 1], ((item - 1) >> 1) & 1) && sh.item[item & 1].head >= 0;
+    // Every role goes through the CTA's items: is there one of number `item`, and no abort?
+    const auto there_is = [&](uint32_t item) {
+        return wait_far(sh, &sh.item_full[item % ITEMS], (item / ITEMS) & 1) && sh.item[item % ITEMS].head >= 0;
     };
 
-    if (sh.item[0].head < 0) {
-        // nothing: fewer tiles than CTAs
-    } else if (warp >= 4) {
-        // ---- softmax: two threads a row, 64 of a tile's 128 keys each
-        const int t = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, r = (warp & 3) * 32 + lane;
+    if (warp >= 4) {
+        // ---- softmax: a thread a row
+        const int t = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lane_bits = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t s_t = tmem + lane_bits + S_COL + t * 128, o_t = tmem + lane_bits + O_COL + t * 128;
-        const int pair_bar = 1 + t * 4 + (warp & 3);
+        const uint32_t s_t = tmem + lane_bits + t * 128, o_t = tmem + lane_bits + O_COL + t * 128;
         const int my_tok = r / p.G, last_tok = p.tile_rows / p.G - 1;  // within the tile
-        // this thread's value for the row's other thread, and the other's
-        const auto swap = [&](float v) {
-            sh.other[t][half][r] = v;
-            asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
-            return sh.other[t][half ^ 1][r];
-        };
-        for (uint32_t item = 0;; ++item) {
+        for (uint32_t item = 0; there_is(item); ++item) {
             // (what only the item's end needs stays in shared memory meanwhile)
-            const volatile Item &my = sh.item[item & 1];
-            int nt, tail, limit, sure, width;  // limit: one past the last key that this row sees
-            int ns, skip, i0;
-            {
-                Item it;
-                it.u.nq = my.u.nq;
-                it.u.len = my.u.len;
-                it.u.m0 = my.u.m0;
-                it.u.w0 = my.u.w0;
-                it.u.ns = my.u.ns;
-                it.i0 = i0 = my.i0;
-                it.i1 = my.i1;
-                const Extent e(p, it);
-                nt = e.tiles(t);
-                tail = e.last() == t ? e.tail : -1;  // the tile whose values are to be cleared
-                sure = it.u.len - it.u.nq + (it.u.m0 + t * p.tile_rows) / p.G + 1;  // the least limit of the tile's rows
-                limit = sure + my_tok;
-                width = p.window > 0 && p.window < it.u.len ? p.window : 0;
-                ns = it.u.ns;
-                skip = it.u.w0 - ns;
-            }
-            uint32_t parity = my.met[t] & 1;
+            const volatile Item &my = sh.item[item % ITEMS];
+            const int nt = my.nt[t], len = my.u.len, ns = my.u.ns, skip = my.u.w0 - ns, i0 = my.i0;
+            // the tile whose values are to be cleared
+            const int tail = t == (my.nt[1] >= my.nt[0] ? NT - 1 : 0) ? my.tail : -1;
+            const int tok = (my.u.m0 + t * p.tile_rows) / p.G + my_tok;
+            const int limit = len - my.u.nq + tok + 1;  // one past the last key that this row sees,
+            const int sure = limit - my_tok;            // and the least of the tile's rows
+            const int width = p.window > 0 && p.window < len ? p.window : 0;
+            uint32_t met = my.met[t];  // the row tile's key tiles so far
             float m_ref = -INFINITY, l = 0.0f;
-            for (int j = 0; j < nt; ++j) {
-                wait_long(sh, &sh.s_full[t], parity);
-                parity ^= 1;
+            for (int j = 0; j < nt; ++j, ++met) {
+                const uint32_t s_b = s_t + (met & 1) * 64;
+                wait_long(sh, &sh.s_full[t][met & 1], (met >> 1) & 1);
                 tc_fence_after();
                 uint32_t x[2][32];
-                tmem_ld32(s_t + half * 64, x[0]);
-                tmem_ld32(s_t + half * 64 + 32, x[1]);
+                tmem_ld32(s_b, x[0]);
+                tmem_ld32(s_b + 32, x[1]);
                 if (__builtin_expect(j == tail, 0)) {
                     // value rows behind the row's last key: whatever lies there must not meet the
-                    // zero weights.  (The barrier's fill before this one is used up by now, so
-                    // the phase is this fill's.)
-                    const uint32_t g = my.g0 + tail;
-                    wait(sh, &sh.v_full[g & 1], (g >> 1) & 1);
-                    const int z0 = my.u.len % TN;
-#pragma unroll
+                    // zero weights
+                    const uint32_t g = my.g0 + tail, slot = g % RING;
+                    wait(sh, &sh.v_full[slot], (g / RING) & 1);
+                    const int z0 = len % TN;
+#pragma unroll 1
                     for (int c = 0; c < NC; ++c) {
-                        const uint32_t v = ring + ((g & 1) * Z::TILE + NC + c) * CHUNK + z0 * 128;
-                        for (int i = half * 128 + r; i < (TN - z0) * 8; i += 256)
+                        const uint32_t v = ring + slot * Z::TILE + (NC + c) * CHUNK + z0 * 128;
+#pragma unroll 1
+                        for (int i = r; i < (TN - z0) * 8; i += 128)
                             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + i * 16), "r"(0)
                                          : "memory");
                     }
@@ -255,32 +234,37 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
                 }
                 tmem_wait_ld();
                 const int key0 = (i0 + j < ns ? i0 + j : i0 + j + skip) * TN;
-                if (__builtin_expect(key0 + TN > sure || (width && key0 < sure + last_tok - width), 0)) {
-                    // more than every row sees
-                    const int seen = limit - key0 - half * 64;
-                    const int low = width ? seen - width : -1, first = p.sinks - key0 - half * 64;
+                if (__builtin_expect(key0 + TN > sure, 0)) {  // more than every row sees
+                    const int seen = limit - key0;
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        if (i >= seen || (i < low && i >= first)) x[0][i] = 0xFF800000u;
-                        if (i + 32 >= seen || (i + 32 < low && i + 32 >= first)) x[1][i] = 0xFF800000u;
+                        if (i >= seen) x[0][i] = 0xFF800000u;
+                        if (i + 32 >= seen) x[1][i] = 0xFF800000u;
+                    }
+                }
+                if (__builtin_expect(width && key0 < sure + last_tok - width, 0)) {  // not in every window
+                    const int first = max(p.sinks - key0, 0);
+                    const uint32_t gap = max(limit - width - key0 - first, 0);  // hidden keys from `first` on
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        if (static_cast<uint32_t>(i - first) < gap) x[0][i] = 0xFF800000u;
+                        if (static_cast<uint32_t>(i + 32 - first) < gap) x[1][i] = 0xFF800000u;
                     }
                 }
                 float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     top4[i & 3] = max3(top4[i & 3], __uint_as_float(x[0][i]), __uint_as_float(x[1][i]));
-                const float mine = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
-                // (the second barrier of a tile is p_ready: nobody writes the next value before
-                // the products have taken both threads' weights)
-                const float top = fmaxf(mine, swap(mine)) * p.scale2;
+                const float top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]) * p.scale2;
                 const bool raise = top > m_ref + (LAZY + T::first_weight);
                 const float m_new = top - T::first_weight;
                 if (__builtin_expect(j > 0 && __any_sync(0xFFFFFFFFu, raise), 0)) {
-                    // the scores came after the products of the tile before: the output is free
+                    wait(sh, &sh.pv_done[t][(met - 1) & 1], ((met - 1) >> 1) & 1);  // the output is free
+                    tc_fence_after();
                     const float f = raise ? ex2(m_ref - m_new) : 1.0f;
                     l *= f;
-#pragma unroll
-                    for (int c = half * (NC * 32); c < (half + 1) * (NC * 32); c += 16) {
+#pragma unroll 1
+                    for (int c = 0; c < NC * 64; c += 16) {
                         uint32_t o[16];
                         tmem_ld16(o_t + c, o);
                         tmem_wait_ld();
@@ -306,257 +290,237 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
                         part[i & 1] = add2(part[i & 1], pack2(e0, e1));
                         w[i] = T::narrow2(e0, e1);
                     }
-                    tmem_st16(s_t + half * 32 + 16 * c, w);
+                    tmem_st16(s_b + 16 * c, w);
                 }
                 tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&sh.p_ready[t][met & 1]);
                 float l0, l1;
                 unpack2(add2(part[0], part[1]), l0, l1);
                 l += l0 + l1;
-                tc_fence_before();
-                mbar_arrive(&sh.p_ready[t]);
             }
-            if (nt > 0) {
-                wait_long(sh, &sh.o_done[t], my.outputs[t] & 1);
-                tc_fence_after();
-            }
-            l += swap(l);
             // (a sum of zero: nothing was seen; one that is NaN stays so)
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             const float lse2 = l == 0.0f ? -INFINITY : m_ref + log2f(l);
-            const int tok = (my.u.m0 + t * p.tile_rows) / p.G + my_tok, h = my.head * p.G + r - my_tok * p.G;
+            const int h = my.head * p.G + r - my_tok * p.G;
             const bool real = r < p.tile_rows && tok < my.u.nq;
-            const bool whole = my.i0 == 0 && my.i1 == my.n;
+            const bool whole = i0 == 0 && my.i1 == my.n;
             const int64_t out_row = my.u.q0 + tok;
-            const int64_t part_row = static_cast<int64_t>(2 * blockIdx.x + (my.i0 > 0 ? 0 : 1)) * (2 * TM) +
-                                     t * TM + r;
-            if (real && half == 0) {
+            const int slot_out = 2 * blockIdx.x + (i0 > 0 ? 0 : 1);
+            if (real) {
                 if (!whole)
-                    p.part_lse[part_row] = lse2;
+                    p.part_lse[static_cast<int64_t>(slot_out) * (NT * TM) + t * TM + r] = lse2;
                 else if (p.lse)
                     p.lse[out_row * p.Hq + h] = lse2 * LN2;
             }
-            uint16_t *dst = p.out + out_row * p.out_tok + h * p.out_head + half * (NC * 32);
-            float *pdst = p.part + part_row * Z::COLS + half * (NC * 32);
-            // 32 bytes a store, a whole sector, where the rows allow it
-            const bool sectors = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
-#pragma unroll
+            // A warp's 32 rows x 64 columns go through shared memory, so that eight lanes write a
+            // whole line of a row.
+            const uint32_t stage = q_s + Z::STAGES + (warp - 4) * Z::STAGE;
+            const int64_t mine = reinterpret_cast<int64_t>(p.out + out_row * p.out_tok + h * p.out_head);
+            if (nt > 0) {
+                wait_long(sh, &sh.pv_done[t][(met - 1) & 1], ((met - 1) >> 1) & 1);
+                tc_fence_after();
+            }
+#pragma unroll 1
             for (int c = 0; c < NC; ++c) {
-                uint32_t o[32] = {};
-                if (nt > 0) {
-                    tmem_ld32(o_t + half * (NC * 32) + 32 * c, o);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t o[32];
+                    tmem_ld32(o_t + c * 64 + half * 32, o);
                     tmem_wait_ld();
-                }
-                if (!real) continue;
-                if (!whole) {
+                    // (where no key was met, the columns hold anything)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = nt > 0 ? __float_as_uint(__uint_as_float(o[i]) * inv) : 0u;
+                    if (!whole) {
+                        if (real)
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4)
+                                *part_at<NC, TM, NT>(p, slot_out, t, c * 64 + half * 32 + i, r) =
+                                    make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]),
+                                                __uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
+                        continue;
+                    }
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
-                        uint32_t y[8];
+                        uint32_t y[4];
 #pragma unroll
-                        for (int u = 0; u < 8; ++u)
-                            y[u] = nt > 0 ? __float_as_uint(__uint_as_float(o[8 * v + u]) * inv) : 0u;
-                        st_global_32B(pdst + c * 32 + v * 8, y);
-                    }
-                    continue;
-                }
-#pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    if (half * (NC * 32) + c * 32 + v * 16 >= p.D) break;
-                    uint32_t y[8];
-#pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        y[u] = nt > 0 ? T::narrow2(__uint_as_float(o[16 * v + 2 * u]) * inv,
-                                                   __uint_as_float(o[16 * v + 2 * u + 1]) * inv)
-                                      : 0u;
-                    uint16_t *d = dst + c * 32 + v * 16;
-                    if (sectors) {
-                        st_global_32B(d, y);
-                    } else {
-                        *reinterpret_cast<uint4 *>(d) = make_uint4(y[0], y[1], y[2], y[3]);
-                        *reinterpret_cast<uint4 *>(d + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+                        for (int u = 0; u < 4; ++u)
+                            y[u] = T::narrow2(__uint_as_float(o[8 * v + 2 * u]), __uint_as_float(o[8 * v + 2 * u + 1]));
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         stage + lane * 128 + (((half * 4 + v) ^ (lane & 7)) << 4)),
+                                     "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+                                     : "memory");
                     }
                 }
+                if (!whole) continue;
+                __syncwarp();
+                const bool in = c * 64 + (lane & 7) * 8 < p.D;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int row = k * 4 + lane / 8;
+                    uint4 y;
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
+                                 : "r"(stage + row * 128 + (((lane & 7) ^ (row & 7)) << 4))
+                                 : "memory");
+                    const int64_t to = __shfl_sync(0xFFFFFFFFu, mine, row) + c * 128 + (lane & 7) * 16;
+                    if (__shfl_sync(0xFFFFFFFFu, static_cast<int>(real), row) && in)
+                        *reinterpret_cast<uint4 *>(to) = y;
+                }
+                __syncwarp();
             }
             // The next item's products overwrite this output once its first weights are there,
             // which come after these reads.
             tc_fence_before();
             __syncwarp();  // the whole warp is done with the item
-            if (lane == 0) mbar_arrive(&sh.item_free[item & 1]);
-            if (!both(next_item(item), pair_bar)) break;
+            if (lane == 0) mbar_arrive(&sh.item_free[item % ITEMS]);
         }
     } else if (warp == 0) {
         // ---- producer: a box of a tile a lane.  Tiles are numbered through all items of the CTA,
-        // and tile j takes the half j mod 2 of the ring.
+        // and tile j takes slot j mod RING.
         const int boxes = TN / p.box_rows;
         const uint32_t q_bytes = NC * p.tile_rows * 128;
         uint32_t j = 0, q_uses[2] = {0, 0};
         const auto all = [](bool yes) { return __all_sync(0xFFFFFFFFu, yes) != 0; };
-        for (uint32_t item = 0;; ++item) {
-            const Item my = sh.item[item & 1];
-            const Extent x(p, my);
+        bool ok = true;
+        for (uint32_t item = 0; ok && all(there_is(item)); ++item) {
+            const Item my = sh.item[item % ITEMS];
+            const int n = my.tiles();
             // the page of this lane's box of the item's tile i
             const int32_t *table = p.block_table + static_cast<int64_t>(my.row) * p.max_pages;
             int2 box = {};
             const auto look = [&](int i) {
                 box = find_box(p, table, my.u.key_tile(my.i0 + i) * TN + lane * p.box_rows, my.u.len, lane < boxes);
             };
-            if (x.n > 0) look(0);
-            bool ok = true;
+            // a tile's keys or values into their slot, once that is free
+            const auto bring = [&](const CUtensorMap *map, uint64_t *full, uint64_t *free, int chunk, int2 at) {
+                if (j >= RING && !all(wait(sh, free, (j / RING - 1) & 1))) return false;
+                if (lane == 0) mbar_expect_tx(full, NC * CHUNK);
+                __syncwarp();
+                const uint32_t dst = ring + j % RING * Z::TILE + chunk * CHUNK + lane * p.box_rows * 128;
+                if (lane < boxes)
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-                if (ok && x.tiles(t) > 0) {
-                    if (q_uses[t] > 0 && !all(wait(sh, &sh.q_free[t], (q_uses[t] - 1) & 1))) {
-                        ok = false;
-                        break;
-                    }
-                    ++q_uses[t];
-                    if (lane == 0) {
-                        mbar_expect_tx(&sh.q_full[t], q_bytes);
-                        for (int c = 0; c < NC; ++c)
-                            tma_load_4d(q_s + (t * NC + c) * CHUNK, &maps.q, c * 64, 0,
-                                        my.u.q0 + (my.u.m0 + t * p.tile_rows) / p.G, my.head, &sh.q_full[t]);
-                    }
-                    __syncwarp();
-                }
-            for (int i = 0; ok && i < x.n; ++i, ++j) {
+                    for (int c = 0; c < NC; ++c)
+                        tma_load_4d(dst + c * CHUNK, map, c * 64, my.head, at.y, at.x, full);
+                __syncwarp();
+                return true;
+            };
+            if (n > 0) look(0);
+            for (int i = 0; ok && i < n; ++i, ++j) {
                 const int2 to = box;
-                if (i + 1 < x.n) look(i + 1);
-                const uint32_t half = j & 1, before = ((j >> 1) - 1) & 1;
-                const uint32_t dst = ring + half * (Z::TILE * CHUNK) + lane * p.box_rows * 128;
-                if (j > 1 && !all(wait(sh, &sh.k_free[half], before))) {
-                    ok = false;
-                    break;
+                if (i + 1 < n) look(i + 1);
+                const uint32_t slot = j % RING;
+                ok = bring(&maps.k, &sh.k_full[slot], &sh.k_free[slot], 0, to);
+                if (ok && i == 0) {  // the queries, behind the first keys, which wait for less
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        if (my.nt[t] > 0) {
+                            ok = ok && (q_uses[t] == 0 || all(wait(sh, &sh.q_free[t], (q_uses[t] - 1) & 1)));
+                            if (!ok) break;
+                            ++q_uses[t];
+                            if (lane == 0) {
+                                mbar_expect_tx(&sh.q_full[t], q_bytes);
+                                for (int c = 0; c < NC; ++c)
+                                    tma_load_4d(q_s + (t * NC + c) * Q_CHUNK, &maps.q, c * 64, 0,
+                                                my.u.q0 + (my.u.m0 + t * p.tile_rows) / p.G, my.head, &sh.q_full[t]);
+                            }
+                            __syncwarp();
+                        }
                 }
-                if (lane == 0) mbar_expect_tx(&sh.k_full[half], NC * CHUNK);
-                __syncwarp();
-                if (lane < boxes)
-                    for (int c = 0; c < NC; ++c)
-                        tma_load_4d(dst + c * CHUNK, &maps.k, c * 64, my.head, to.y, to.x, &sh.k_full[half]);
-                __syncwarp();
-                if (j > 1 && !all(wait(sh, &sh.v_free[half], before))) {
-                    ++j;  // (its keys are on their way)
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) mbar_expect_tx(&sh.v_full[half], NC * CHUNK);
-                __syncwarp();
-                if (lane < boxes)
-                    for (int c = 0; c < NC; ++c)
-                        tma_load_4d(dst + (NC + c) * CHUNK, &maps.v, c * 64, my.head, to.y, to.x,
-                                    &sh.v_full[half]);
-                __syncwarp();
+                ok = ok && bring(&maps.v, &sh.v_full[slot], &sh.v_free[slot], NC, to);
             }
-            if (!ok || !all(!sh.abort)) break;
-            if (lane == 0) mbar_arrive(&sh.item_free[item & 1]);
-            if (!all(next_item(item))) break;
+            __syncwarp();  // (all lanes have read the item)
+            if (lane == 0) mbar_arrive(&sh.item_free[item % ITEMS]);
         }
         if (__any_sync(0xFFFFFFFFu, sh.abort)) {
-            // let the copies in flight land: the last two tiles' and the queries' (a fill that was
-            // cut off never completes: its wait runs to the limit)
-            for (uint32_t i = j > 2 ? j - 2 : 0; i < j; ++i) {
-                wait_out(&sh.k_full[i & 1], (i >> 1) & 1);
-                wait_out(&sh.v_full[i & 1], (i >> 1) & 1);
+            // let the copies in flight land: the last fills of every slot, and the queries' (a fill
+            // that was cut off never completes: its wait runs to the limit)
+            for (uint32_t i = j > RING ? j - RING : 0; i < j; ++i) {
+                wait_out(&sh.k_full[i % RING], (i / RING) & 1);
+                wait_out(&sh.v_full[i % RING], (i / RING) & 1);
             }
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < NT; ++t)
                 if (q_uses[t] > 0) wait_out(&sh.q_full[t], (q_uses[t] - 1) & 1);
         }
     } else if (warp == 1) {
         if (elect_one()) {
-            // ---- MMA issuer: a tile's products, then its next scores, in turn
-            constexpr uint32_t id_s = idesc_of<T>(TN, false);
-            constexpr uint32_t id_o = idesc_of<T>(NC * 64, true);
+            // ---- MMA issuer: a tile's products, then the scores of two tiles on, in turn
+            constexpr uint32_t id_s = idesc_of<T>(TN, false), id_o = idesc_of<T>(NC * 64, true);
             const uint64_t qd = smem_desc_sw128(q_s), kd = smem_desc_sw128(ring);
             const uint64_t vd = smem_desc_rows_k(ring) + NC * (CHUNK >> 4);
-            const auto scores = [&](uint32_t g, int t) {
-                const uint32_t d = tmem + S_COL + t * 128;
-                const uint64_t a_d = qd + t * (NC * (CHUNK >> 4));
-                const uint64_t b_d = kd + (g & 1) * (Z::TILE * (CHUNK >> 4));
+            uint32_t q_uses[2] = {0, 0}, tails = 0;
+            for (uint32_t item = 0; there_is(item); ++item) {
+                const Item my = sh.item[item % ITEMS];
+                const int n = my.tiles(), last = my.last();
+                // row tile t's scores against the item's tile j
+                const auto scores = [&](int t, int j) {
+                    const uint32_t g = my.g0 + j, b = (my.met[t] + j) & 1;
+                    if (!wait(sh, &sh.k_full[g % RING], (g / RING) & 1)) return;
+                    tc_fence_after();
+                    const uint32_t d = tmem + t * 128 + b * 64;
+                    const uint64_t a_d = qd + t * (NC * (Q_CHUNK >> 4)), b_d = kd + g % RING * (Z::TILE >> 4);
 #pragma unroll
-                for (int c = 0; c < NC; ++c)
+                    for (int c = 0; c < NC; ++c)
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        mma_bf16(d, a_d + c * (CHUNK >> 4) + 2 * u, b_d + c * (CHUNK >> 4) + 2 * u, id_s, (c | u) != 0);
-                mma_commit(&sh.s_full[t]);
-            };
-            const auto products = [&](uint32_t g, int t, int j) {
-                const uint32_t a_d = tmem + S_COL + t * 128, d = tmem + O_COL + t * 128;
-                const uint64_t b_d = vd + (g & 1) * (Z::TILE * (CHUNK >> 4));
+                        for (int u = 0; u < 4; ++u)
+                            mma_bf16(d, a_d + c * (Q_CHUNK >> 4) + 2 * u, b_d + c * (CHUNK >> 4) + 2 * u, id_s,
+                                     (c | u) != 0);
+                    mma_commit(&sh.s_full[t][b]);
+                    if (j + 1 == my.nt[t]) mma_commit(&sh.q_free[t]);
+                    if (t == last) mma_commit(&sh.k_free[g % RING]);
+                };
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    mma_ts(d, a_d + 8 * u, b_d + u * (2048 >> 4), id_o, (j | u) != 0);
-            };
-            // the tile's number through all items, and the numbers of tiles, items and cleared
-            // tails so far, as far as parities go
-            uint32_t g = 0, q_uses[2] = {0, 0}, p_uses[2] = {0, 0}, tails = 0;
-            for (uint32_t item = 0;; ++item) {
-                const Item my = sh.item[item & 1];
-                const Extent x(p, my);
-                const int last = x.last();
-                if (x.n > 0) {
-                    if (!wait(sh, &sh.k_full[g & 1], (g >> 1) & 1)) break;
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        if (x.tiles(t) > 0) {
-                            if (!wait(sh, &sh.q_full[t], q_uses[t] & 1)) break;
-                            ++q_uses[t];
-                            tc_fence_after();
-                            scores(g, t);
-                            if (x.tiles(t) == 1) mma_commit(&sh.q_free[t]);
+                    for (int t = 0; t < NT; ++t)
+                        if (j < my.nt[t] && !sh.abort) {
+                            if (j == 0 && !wait(sh, &sh.q_full[t], q_uses[t]++ & 1)) break;
+                            scores(t, j);
                         }
-                    mma_commit(&sh.k_free[g & 1]);
-                }
-                for (int j = 0; j < x.n && !sh.abort; ++j, ++g) {
-                    if (!wait(sh, &sh.v_full[g & 1], (g >> 1) & 1)) break;
-                    bool keys = false;  // tile j + 1's have been waited for
-                    if (j == x.tail && !wait(sh, &sh.v_clean, tails++ & 1)) break;
+                for (int j = 0; j < n && !sh.abort; ++j) {
+                    const uint32_t g = my.g0 + j;
+                    if (!wait(sh, &sh.v_full[g % RING], (g / RING) & 1)) break;
+                    if (j == my.tail && !wait(sh, &sh.v_clean, tails++ & 1)) break;
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const int nt = x.tiles(t);
-                        if (j >= nt) continue;
-                        if (!wait(sh, &sh.p_ready[t], p_uses[t]++ & 1)) break;
+                    for (int t = 0; t < NT; ++t) {
+                        if (j >= my.nt[t]) continue;
+                        const uint32_t step = my.met[t] + j, b = step & 1;
+                        if (!wait(sh, &sh.p_ready[t][b], (step >> 1) & 1)) break;
                         tc_fence_after();
-                        products(g, t, j);
-                        if (t == last) mma_commit(&sh.v_free[g & 1]);
-                        if (j + 1 == nt) mma_commit(&sh.o_done[t]);
-                        if (j + 1 < nt) {
-                            if (!keys && !wait(sh, &sh.k_full[(g + 1) & 1], ((g + 1) >> 1) & 1)) break;
-                            keys = true;
-                            scores(g + 1, t);
-                            if (j + 2 == nt) mma_commit(&sh.q_free[t]);
-                            if (t == last) mma_commit(&sh.k_free[(g + 1) & 1]);
-                        }
+                        const uint32_t a_d = tmem + t * 128 + b * 64, d = tmem + O_COL + t * 128;
+                        const uint64_t b_d = vd + g % RING * (Z::TILE >> 4);
+#pragma unroll
+                        for (int u = 0; u < TN / 16; ++u)
+                            mma_ts(d, a_d + 8 * u, b_d + u * (2048 >> 4), id_o, (j | u) != 0);
+                        mma_commit(&sh.pv_done[t][b]);
+                        if (t == last) mma_commit(&sh.v_free[g % RING]);
+                        if (j + 2 < my.nt[t]) scores(t, j + 2);
                     }
                 }
-                mbar_arrive(&sh.item_free[item & 1]);
-                if (sh.abort || !next_item(item)) break;
+                mbar_arrive(&sh.item_free[item % ITEMS]);
+                if (sh.abort) break;
             }
             mma_commit(&sh.drained);
             wait_out(&sh.drained, 0);
         }
     } else if (warp == 2) {
-        // ---- the items after the first, each as soon as the one two before it is left behind
+        // ---- the items after the first, each as soon as its place is left behind
         Item it = sh.item[0];
-        for (uint32_t item = 0;; ++item) {
-            const Extent was(p, it);
-            it.g0 += was.n;
+        for (uint32_t item = 1; it.head >= 0; ++item) {
+            it.g0 += it.tiles();
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                it.met[t] += was.tiles(t);
-                it.outputs[t] += was.tiles(t) > 0;
-            }
-            const bool more = next(it);
-            if (!more) it.head = -1;
-            if (!__all_sync(0xFFFFFFFFu, item == 0 || wait_far(sh, &sh.item_free[(item - 1) & 1],
-                                                               ((item - 1) >> 1) & 1)))
+            for (int t = 0; t < 2; ++t) it.met[t] += it.nt[t];
+            next(it);
+            if (!__all_sync(0xFFFFFFFFu, item < ITEMS || wait_far(sh, &sh.item_free[item % ITEMS],
+                                                                  (item / ITEMS - 1) & 1)))
                 break;
             if (lane == 0) {
-                sh.item[(item + 1) & 1] = it;
-                mbar_arrive(&sh.item_full[(item + 1) & 1]);
+                sh.item[item % ITEMS] = it;
+                mbar_arrive(&sh.item_full[item % ITEMS]);
             }
             __syncwarp();
-            if (!more) break;
         }
+        walk.close(p);
     }
-    if (warp == 2) walk.close(p);
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -574,56 +538,56 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
 struct Layout {
     size_t plan, part, lse, total;
 };
-Layout layout(int32_t D) {
+Layout layout(int NC) {
     const auto align256 = [](size_t n) { return (n + 255) & ~static_cast<size_t>(255); };
+    const size_t rows = static_cast<size_t>(2 * SMS) * TM * (NC <= 2 ? 2 : 1);
     Layout y;
     y.plan = 0;
     y.part = align256(SMS * sizeof(Plan));
-    y.lse = y.part + static_cast<size_t>(2 * SMS) * 2 * TM * ((D + 63) / 64 * 64) * 4;
-    y.total = y.lse + align256(static_cast<size_t>(2 * SMS) * 2 * TM * 4);
+    y.lse = y.part + rows * (64 * NC) * 4;
+    y.total = y.lse + align256(rows * 4);
     return y;
 }
 
 template <typename T, int NC>
-cudaError_t launch(const Maps &maps, const Params &p, cudaStream_t stream) {
-    constexpr int smem = Sizes<NC>::SMEM;
+cudaError_t launch(const HeadsAttnArgs &a, cudaStream_t stream) {
+    using Z = Sizes<NC>;
+    const Layout y = layout(NC);
+    const int G = a.Hq / a.Hkv;
+    Params p;
+    Maps maps;
+    if (!set_up(a, TM / G * G, Z::NT, TN, true, y.plan, y.part, y.lse, p, maps)) return cudaErrorInvalidValue;
     static AttrCache attr;
-    cudaError_t e = ensure_attr(k_heads_chunk<T, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem, attr);
+    cudaError_t e = ensure_attr(k_heads_chunk<T, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::SMEM, attr);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(SMS);
-    cfg.blockDim = dim3(NTHREADS);
-    cfg.dynamicSmemBytes = smem;
+    cfg.blockDim = dim3(Z::THREADS);
+    cfg.dynamicSmemBytes = Z::SMEM;
     cfg.stream = stream;
     cfg.attrs = pdl_attr();  // set up beside the end of whatever the stream runs before
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, k_heads_chunk<T, NC>, maps, p);
     if (e != cudaSuccess) return e;
     count_launches(1);
-    cfg.gridDim = dim3(2 * TM / JOIN_WARPS, SMS);
+    cfg.gridDim = dim3(Z::NT * TM / 32, SMS);
     cfg.blockDim = dim3(JOIN_THREADS);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, k_heads_join<T, NC, TM, 2>, p);
+    e = cudaLaunchKernelEx(&cfg, k_heads_join<T, NC, TM, Z::NT, false>, p);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
-
 template <typename T>
-cudaError_t pick(const Maps &maps, const Params &p, cudaStream_t stream) {
-    return p.D <= 64 ? launch<T, 1>(maps, p, stream) : launch<T, 2>(maps, p, stream);
+cudaError_t pick(const HeadsAttnArgs &a, cudaStream_t s) {
+    return a.D <= 64 ? launch<T, 1>(a, s) : a.D <= 128 ? launch<T, 2>(a, s) : launch<T, 4>(a, s);
 }
 
 }  // namespace hch
 
-size_t heads_chunk_workspace_bytes(int32_t D) { return hch::layout(D).total; }
+size_t heads_chunk_workspace_bytes(int32_t D) { return hch::layout(D <= 64 ? 1 : D <= 128 ? 2 : 4).total; }
 
 cudaError_t run_heads_chunk(const HeadsAttnArgs &a, int dtype, cudaStream_t stream) {
-    heads::Params p;
-    heads::Maps maps;
-    const int G = a.Hq / a.Hkv, tok = hch::TM / G;
-    const hch::Layout y = hch::layout(a.D);
-    if (!heads::set_up(a, tok * G, 2, hch::TN, y.plan, y.part, y.lse, p, maps)) return cudaErrorInvalidValue;
-    return dtype == MTPSPEC_BF16 ? hch::pick<Bf16>(maps, p, stream) : hch::pick<F16>(maps, p, stream);
+    return dtype == MTPSPEC_BF16 ? hch::pick<Bf16>(a, stream) : hch::pick<F16>(a, stream);
 }
 
 }  // namespace mtpspec

@@ -473,15 +473,14 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
             const bool real = r < rows, whole = i0 == 0 && my.i1 == my.n;
             const int tok = (m0 + r) / p.G, h = my.head * p.G + m0 + r - tok * p.G;
             const int64_t out_row = my.u.q0 + tok;
-            const int64_t part_row = static_cast<int64_t>(2 * blockIdx.x + (i0 > 0 ? 0 : 1)) * ROWS + r;
+            const int slot_out = 2 * blockIdx.x + (i0 > 0 ? 0 : 1);
             if (real && part == 0) {
                 if (!whole)
-                    p.part_lse[part_row] = lse2;
+                    p.part_lse[static_cast<int64_t>(slot_out) * ROWS + r] = lse2;
                 else if (p.lse)
                     p.lse[out_row * p.Hq + h] = lse2 * LN2;
             }
             uint16_t *dst = p.out + out_row * p.out_tok + h * p.out_head + part * W;
-            float *pdst = p.part + part_row * (64 * NC) + part * W;
             // 32 bytes a store, a whole sector, where the rows allow it
             const bool sectors = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
 #pragma unroll
@@ -511,12 +510,9 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
                         }
                     } else {
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            uint32_t y[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) y[i] = __float_as_uint(f[8 * k + i]);
-                            st_global_32B(pdst + c * 64 + v + 8 * k, y);
-                        }
+                        for (int k = 0; k < 16; k += 4)
+                            *part_at<NC, ROWS, 1>(p, slot_out, 0, c * 64 + part * W + v + k, r) =
+                                make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
                     }
                 }
             }
@@ -581,7 +577,7 @@ cudaError_t launch(const HeadsAttnArgs &a, cudaStream_t stream) {
     const Layout y = layout(ROWS, Z::CTAS, NC);
     Params p;
     Maps maps;
-    if (!set_up(a, ROWS, 1, Z::TN, y.plan, y.part, y.lse, p, maps)) return cudaErrorInvalidValue;
+    if (!set_up(a, ROWS, 1, Z::TN, false, y.plan, y.part, y.lse, p, maps)) return cudaErrorInvalidValue;
     static AttrCache attr;
     cudaError_t e = ensure_attr(k_heads_few<T, NC, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::SMEM, attr);
     if (e != cudaSuccess) return e;
@@ -595,10 +591,13 @@ cudaError_t launch(const HeadsAttnArgs &a, cudaStream_t stream) {
     e = cudaLaunchKernelEx(&cfg, k_heads_few<T, NC, ROWS>, maps, p);
     if (e != cudaSuccess) return e;
     count_launches(1);
-    cfg.gridDim = dim3(ROWS / JOIN_WARPS, Z::CTAS * SMS);
+    // few units are cut into many parts each
+    const bool spread = a.B * a.Hkv * 4 < Z::CTAS * SMS;
+    cfg.gridDim = dim3(ROWS / 32, Z::CTAS * SMS, spread ? JOIN_WARPS : 1);
     cfg.blockDim = dim3(JOIN_THREADS);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, k_heads_join<T, NC, ROWS, 1>, p);
+    e = spread ? cudaLaunchKernelEx(&cfg, k_heads_join<T, NC, ROWS, 1, true>, p)
+               : cudaLaunchKernelEx(&cfg, k_heads_join<T, NC, ROWS, 1, false>, p);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }

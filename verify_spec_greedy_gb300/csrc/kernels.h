@@ -321,7 +321,7 @@ struct HeadsAttnArgs {
 };
 size_t heads_attn_workspace_bytes(int64_t B, int64_t Tq, int32_t Hq, int32_t Hkv, int32_t D);
 cudaError_t run_heads_attn(const HeadsAttnArgs &a, int dtype, cudaStream_t stream);
-// Its forms: for rows of many tokens (heads_chunk.cu; D <= 128), and for rows of few (heads_few.cu).
+// Its forms: for rows of many tokens (heads_chunk.cu), and for rows of few (heads_few.cu).
 size_t heads_chunk_workspace_bytes(int32_t D);
 cudaError_t run_heads_chunk(const HeadsAttnArgs &a, int dtype, cudaStream_t stream);
 size_t heads_few_workspace_bytes(int32_t D, bool rows32);
