@@ -12,11 +12,10 @@
 // 128 / G tokens times G heads.  A unit of work is two such tiles (one, for heads of more than 128
 // elements), a thread a row in the softmax.
 //
-// Keys: tiles of 64.  A row tile has two score buffers of 64 columns in tensor memory (whose first
-// half becomes the weights, the left operand of the second product) beside its output: 512 columns
-// in all.  So the scores of a tile are there before the weights of the one before are, and no
-// row tile's chain scores - softmax - products is waited for from end to end.  (Tiles of 128 keys
-// with one buffer each: a round of both row tiles took 3,700 cycles for 2,048 of products.)
+// Keys: tiles of 128, and a score buffer a row tile, whose first half becomes the weights (the left
+// operand of the second product): while the tensor cores work on one row tile, the other's softmax
+// runs.  A single row tile has two buffers, of 64 keys, beside its 256 output columns: the scores of
+// a tile are there before the weights of the one before are.
 //
 // A tile is brought in boxes that stay within a page, a box a lane of the producing warp.  With a
 // window, a unit meets the tiles of the first tokens, then those of the window.
@@ -35,38 +34,53 @@ namespace hch {
 using namespace heads;
 
 constexpr int TM = 128;            // rows of a tile in tensor memory
-constexpr int TN = 64;             // keys of a tile
 constexpr int Q_CHUNK = TM * 128;  // bytes of a row tile x 64 columns of 16 bits
-constexpr int CHUNK = TN * 128;    // and of a key tile
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int O_COL = 256;         // row tile t's scores: 128 t + 64 (buffer), its output: 256 + 128 t
+constexpr int O_COL = 256;         // row tile t's scores: 128 t, its output: 256 + 128 t
 constexpr int ITEMS = 4;
 
 // An item of a CTA: tiles i0 .. i1 - 1 of a unit's list of n (at least 1); how many of them either
 // row tile meets, and which of them the row's keys end in, if that is not a whole tile; with the key
 // tiles before it, and the key tiles that either row tile met before.  head -1: no more.
+template <int TN>
 struct Item {
     Unit<TN> u;
     int row, head, i0, i1, n;
     int nt[2], tail;
     uint32_t g0, met[2];
     __device__ __forceinline__ int tiles() const { return max(nt[0], nt[1]); }
-    // the row tile that uses every chunk last
-    __device__ __forceinline__ int last() const { return nt[1] >= nt[0] ? 1 : 0; }
 };
 
 constexpr int MAX_RING = 8;
 // Barriers by row tile are doubled, a phase for every other key tile: who waits for a tile may be one
 // behind, and a parity cannot tell two phases from none.
+template <int TN>
 struct __align__(16) Shared {
     uint64_t k_full[MAX_RING], v_full[MAX_RING], k_free[MAX_RING], v_free[MAX_RING];  // by the tile's slot
-    uint64_t q_full[2], q_free[2], s_full[2][2], p_ready[2][2], pv_done[2][2], v_clean, drained;
+    uint64_t q_full[2], q_free[2], s_full[2][2], p_ready[2][2], pv_done[2][2], drained;
     uint64_t item_full[ITEMS], item_free[ITEMS];
-    Item item[ITEMS];
+    Item<TN> item[ITEMS];
     Scan scan;
     uint32_t tmem;
     volatile int abort;
+    float other[2][2][TM];  // what the two threads of a row tell each other, by tile and half
 };
+
+// Whether all of two warps that share rows say yes.  They meet at barrier `bar` in everything they
+// do, so that after a wait that gave up none may go on without the others.
+__device__ __forceinline__ bool both(bool yes, int bar) {
+    uint32_t all;
+    __syncwarp();
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %2, 0;\n\t"
+        "bar.red.and.pred p, %1, 64, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(all)
+        : "r"(bar), "r"(static_cast<uint32_t>(yes))
+        : "memory");
+    return all != 0;
+}
 
 // D[128, n] (+)= A[128, 16] B[16, n], A from tensor memory.
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
@@ -78,11 +92,11 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// A tile whose rows are the products' K axis and whose 64-column chunks are CHUNK apart.
-__device__ __forceinline__ uint64_t smem_desc_rows_k(uint32_t addr) {
+// A tile whose rows are the products' K axis and whose 64-column chunks are `chunk` bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_rows_k(uint32_t addr, uint32_t chunk) {
     uint64_t d = 0;
     d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(CHUNK >> 4) << 16;
+    d |= static_cast<uint64_t>(chunk >> 4) << 16;
     d |= static_cast<uint64_t>(1024 >> 4) << 32;
     d |= static_cast<uint64_t>(1) << 46;
     d |= static_cast<uint64_t>(2) << 61;
@@ -99,12 +113,16 @@ __host__ __device__ constexpr uint32_t idesc_of(int n, bool b_rows_k) {
 template <int NC>
 struct Sizes {
     static constexpr int NT = NC <= 2 ? 2 : 1;                      // row tiles of a unit
-    static constexpr int THREADS = 128 + 128 * NT;                  // warp 0 TMA, 1 MMA, 2 items, 3 TMEM; softmax
-    static constexpr int TILE = 2 * NC * CHUNK, RING = 16 / (2 * NC) < MAX_RING ? 16 / (2 * NC) : MAX_RING;
-    static constexpr int STAGE = 4096;                              // of a softmax warp: 32 rows x 64 columns
+    static constexpr int TN = NC <= 2 ? 128 : 64;                   // keys of a tile
+    static constexpr int SB = NC <= 2 ? 1 : 2;                      // score buffers of a row tile
+    static constexpr int CHUNK = TN * 128;                          // bytes of a key tile x 64 columns
+    static constexpr int HALVES = NT;                               // softmax threads of a row
+    static constexpr int THREADS = 128 + 128 * NT * HALVES;         // warp 0 TMA, 1 MMA, 2 items, 3 TMEM; softmax
+    static constexpr int TILE = 2 * NC * CHUNK, RING = 128 * 1024 / TILE;
+    static constexpr int STAGE = 2048;                              // of a softmax warp: 32 rows x 32 columns
     static constexpr int Q_BYTES = NT * NC * Q_CHUNK, STAGES = Q_BYTES + RING * TILE;
-    static constexpr int EXTRA = static_cast<int>(sizeof(Shared));
-    static constexpr int SMEM = STAGES + 4 * NT * STAGE + EXTRA;
+    static constexpr int EXTRA = static_cast<int>(sizeof(Shared<TN>));
+    static constexpr int SMEM = STAGES + (THREADS - 128) / 32 * STAGE + EXTRA;
     static_assert(SMEM <= 232448, "227 KB a CTA");
     static_assert(SMEM > 116 * 1024, "two CTAs, which take all tensor memory, may not share an SM");
 };
@@ -114,9 +132,10 @@ __global__ void __launch_bounds__(Sizes<NC>::THREADS, 1)
 k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
     extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's period
     using Z = Sizes<NC>;
-    constexpr int NT = Z::NT, RING = Z::RING;
+    constexpr int NT = Z::NT, HALVES = Z::HALVES, TN = Z::TN, C = TN / HALVES, SB = Z::SB, CHUNK = Z::CHUNK, RING = Z::RING;
+    using Item = hch::Item<TN>;
     const uint32_t q_s = smem_addr(smem), ring = q_s + Z::Q_BYTES;
-    Shared &sh = *reinterpret_cast<Shared *>(smem + Z::SMEM - Z::EXTRA);
+    Shared<TN> &sh = *reinterpret_cast<Shared<TN> *>(smem + Z::SMEM - Z::EXTRA);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -129,17 +148,16 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
         for (int t = 0; t < NT; ++t) {
             mbar_init(&sh.q_full[t], 1);
             mbar_init(&sh.q_free[t], 1);
-            for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < SB; ++b) {
                 mbar_init(&sh.s_full[t][b], 1);
-                mbar_init(&sh.p_ready[t][b], 128);
+                mbar_init(&sh.p_ready[t][b], 4 * HALVES);
                 mbar_init(&sh.pv_done[t][b], 1);
             }
         }
         for (int i = 0; i < ITEMS; ++i) {
             mbar_init(&sh.item_full[i], 1);
-            mbar_init(&sh.item_free[i], 2 + 4 * NT);  // the producer, the issuer, the softmax warps
+            mbar_init(&sh.item_free[i], 2 + 4 * NT * HALVES);  // the producer, the issuer, the softmax warps
         }
-        mbar_init(&sh.v_clean, 128);
         mbar_init(&sh.drained, 1);
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -191,17 +209,30 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
     };
 
     if (warp >= 4) {
-        // ---- softmax: a thread a row
-        const int t = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
+        // ---- softmax: a thread a row, or two, with 64 of a tile's 128 keys each
+        const int t = (warp - 4) / (4 * HALVES), half = (warp - 4) / 4 % HALVES, r = (warp & 3) * 32 + lane;
         const uint32_t lane_bits = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_t = tmem + lane_bits + t * 128, o_t = tmem + lane_bits + O_COL + t * 128;
         const int my_tok = r / p.G, last_tok = p.tile_rows / p.G - 1;  // within the tile
-        for (uint32_t item = 0; there_is(item); ++item) {
+        const int pair_bar = 1 + t * 4 + (warp & 3);
+        // the row's value from those of its threads
+        const auto meet = [&](float v, auto join) {
+            if constexpr (HALVES == 2) {
+                sh.other[t][half][r] = v;
+                asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+                v = join(v, sh.other[t][half ^ 1][r]);
+            }
+            return v;
+        };
+        const auto go_on = [&](uint32_t item) {
+            const bool yes = there_is(item);
+            return HALVES == 2 ? both(yes, pair_bar) : yes;
+        };
+        for (uint32_t item = 0; go_on(item); ++item) {
             // (what only the item's end needs stays in shared memory meanwhile)
             const volatile Item &my = sh.item[item % ITEMS];
             const int nt = my.nt[t], len = my.u.len, ns = my.u.ns, skip = my.u.w0 - ns, i0 = my.i0;
-            // the tile whose values are to be cleared
-            const int tail = t == (my.nt[1] >= my.nt[0] ? NT - 1 : 0) ? my.tail : -1;
+            const int tail = my.tail;  // the tile whose values are to be cleared
             const int tok = (my.u.m0 + t * p.tile_rows) / p.G + my_tok;
             const int limit = len - my.u.nq + tok + 1;  // one past the last key that this row sees,
             const int sure = limit - my_tok;            // and the least of the tile's rows
@@ -209,15 +240,15 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
             uint32_t met = my.met[t];  // the row tile's key tiles so far
             float m_ref = -INFINITY, l = 0.0f;
             for (int j = 0; j < nt; ++j, ++met) {
-                const uint32_t s_b = s_t + (met & 1) * 64;
-                wait_long(sh, &sh.s_full[t][met & 1], (met >> 1) & 1);
+                const uint32_t buffer = met % SB, phase = (met / SB) & 1, s_b = s_t + buffer * TN;
+                wait_long(sh, &sh.s_full[t][buffer], phase);
                 tc_fence_after();
-                uint32_t x[2][32];
-                tmem_ld32(s_b, x[0]);
-                tmem_ld32(s_b + 32, x[1]);
+                uint32_t x[C / 32][32];
+#pragma unroll
+                for (int c = 0; c < C / 32; ++c) tmem_ld32(s_b + half * C + 32 * c, x[c]);
                 if (__builtin_expect(j == tail, 0)) {
                     // value rows behind the row's last key: whatever lies there must not meet the
-                    // zero weights
+                    // zero weights.  (Either row tile clears them, before its own products.)
                     const uint32_t g = my.g0 + tail, slot = g % RING;
                     wait(sh, &sh.v_full[slot], (g / RING) & 1);
                     const int z0 = len % TN;
@@ -225,46 +256,45 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
                     for (int c = 0; c < NC; ++c) {
                         const uint32_t v = ring + slot * Z::TILE + (NC + c) * CHUNK + z0 * 128;
 #pragma unroll 1
-                        for (int i = r; i < (TN - z0) * 8; i += 128)
+                        for (int i = half * 128 + r; i < (TN - z0) * 8; i += 128 * HALVES)
                             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + i * 16), "r"(0)
                                          : "memory");
                     }
                     fence_async_smem();
-                    mbar_arrive(&sh.v_clean);
                 }
                 tmem_wait_ld();
                 const int key0 = (i0 + j < ns ? i0 + j : i0 + j + skip) * TN;
                 if (__builtin_expect(key0 + TN > sure, 0)) {  // more than every row sees
-                    const int seen = limit - key0;
+                    const int seen = limit - key0 - half * C;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        if (i >= seen) x[0][i] = 0xFF800000u;
-                        if (i + 32 >= seen) x[1][i] = 0xFF800000u;
-                    }
+                    for (int i = 0; i < C; ++i)
+                        if (i >= seen) x[i / 32][i % 32] = 0xFF800000u;
                 }
                 if (__builtin_expect(width && key0 < sure + last_tok - width, 0)) {  // not in every window
-                    const int first = max(p.sinks - key0, 0);
-                    const uint32_t gap = max(limit - width - key0 - first, 0);  // hidden keys from `first` on
+                    const int first = max(p.sinks - key0, 0) - half * C;
+                    const uint32_t gap = max(limit - width - key0 - half * C - first, 0);  // hidden from `first` on
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        if (static_cast<uint32_t>(i - first) < gap) x[0][i] = 0xFF800000u;
-                        if (static_cast<uint32_t>(i + 32 - first) < gap) x[1][i] = 0xFF800000u;
-                    }
+                    for (int i = 0; i < C; ++i)
+                        if (static_cast<uint32_t>(i - first) < gap) x[i / 32][i % 32] = 0xFF800000u;
                 }
                 float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    top4[i & 3] = max3(top4[i & 3], __uint_as_float(x[0][i]), __uint_as_float(x[1][i]));
-                const float top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]) * p.scale2;
+                for (int i = 0; i < C / 2; ++i)
+                    top4[i & 3] = max3(top4[i & 3], __uint_as_float(x[i / 32][i % 32]),
+                                       __uint_as_float(x[C / 64 + i / 32][i % 32]));
+                // (the second barrier of a tile is p_ready: nobody writes the next value before the
+                // products have taken both threads' weights)
+                const float top = meet(fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]),
+                                       [](float a, float b) { return fmaxf(a, b); }) * p.scale2;
                 const bool raise = top > m_ref + (LAZY + T::first_weight);
                 const float m_new = top - T::first_weight;
                 if (__builtin_expect(j > 0 && __any_sync(0xFFFFFFFFu, raise), 0)) {
-                    wait(sh, &sh.pv_done[t][(met - 1) & 1], ((met - 1) >> 1) & 1);  // the output is free
+                    wait(sh, &sh.pv_done[t][(met - 1) % SB], ((met - 1) / SB) & 1);  // the output is free
                     tc_fence_after();
                     const float f = raise ? ex2(m_ref - m_new) : 1.0f;
                     l *= f;
 #pragma unroll 1
-                    for (int c = 0; c < NC * 64; c += 16) {
+                    for (int c = half * (NC * 64 / HALVES); c < (half + 1) * (NC * 64 / HALVES); c += 16) {
                         uint32_t o[16];
                         tmem_ld16(o_t + c, o);
                         tmem_wait_ld();
@@ -278,7 +308,7 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
                 const uint64_t scale_2 = pack2(p.scale2, p.scale2), minus_m = pack2(-m_use, -m_use);
                 uint64_t part[2] = {0, 0};  // two pairs of sums
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
+                for (int c = 0; c < C / 32; ++c) {
                     uint32_t w[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -290,15 +320,22 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
                         part[i & 1] = add2(part[i & 1], pack2(e0, e1));
                         w[i] = T::narrow2(e0, e1);
                     }
-                    tmem_st16(s_b + 16 * c, w);
+                    tmem_st16(s_b + half * (C / 2) + 16 * c, w);
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&sh.p_ready[t][met & 1]);
+                // (an arrival a warp: 128 of them took the barriers' unit longer than the weights)
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.p_ready[t][buffer]);
                 float l0, l1;
                 unpack2(add2(part[0], part[1]), l0, l1);
                 l += l0 + l1;
             }
+            if (nt > 0) {
+                wait_long(sh, &sh.pv_done[t][(met - 1) % SB], ((met - 1) / SB) & 1);
+                tc_fence_after();
+            }
+            l = meet(l, [](float a, float b) { return a + b; });
             // (a sum of zero: nothing was seen; one that is NaN stays so)
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             const float lse2 = l == 0.0f ? -INFINITY : m_ref + log2f(l);
@@ -307,63 +344,55 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
             const bool whole = i0 == 0 && my.i1 == my.n;
             const int64_t out_row = my.u.q0 + tok;
             const int slot_out = 2 * blockIdx.x + (i0 > 0 ? 0 : 1);
-            if (real) {
+            if (real && half == 0) {
                 if (!whole)
                     p.part_lse[static_cast<int64_t>(slot_out) * (NT * TM) + t * TM + r] = lse2;
                 else if (p.lse)
                     p.lse[out_row * p.Hq + h] = lse2 * LN2;
             }
-            // A warp's 32 rows x 64 columns go through shared memory, so that eight lanes write a
-            // whole line of a row.
+            // A warp's 32 rows x 32 columns go through shared memory, so that four lanes write 64
+            // bytes of a row.
             const uint32_t stage = q_s + Z::STAGES + (warp - 4) * Z::STAGE;
             const int64_t mine = reinterpret_cast<int64_t>(p.out + out_row * p.out_tok + h * p.out_head);
-            if (nt > 0) {
-                wait_long(sh, &sh.pv_done[t][(met - 1) & 1], ((met - 1) >> 1) & 1);
-                tc_fence_after();
-            }
 #pragma unroll 1
-            for (int c = 0; c < NC; ++c) {
+            for (int col = half * (NC * 64 / HALVES); col < (half + 1) * (NC * 64 / HALVES); col += 32) {
+                uint32_t o[32];
+                tmem_ld32(o_t + col, o);
+                tmem_wait_ld();
+                // (where no key was met, the columns hold anything)
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t o[32];
-                    tmem_ld32(o_t + c * 64 + half * 32, o);
-                    tmem_wait_ld();
-                    // (where no key was met, the columns hold anything)
+                for (int i = 0; i < 32; ++i) o[i] = nt > 0 ? __float_as_uint(__uint_as_float(o[i]) * inv) : 0u;
+                if (!whole) {
+                    if (real)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = nt > 0 ? __float_as_uint(__uint_as_float(o[i]) * inv) : 0u;
-                    if (!whole) {
-                        if (real)
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4)
-                                *part_at<NC, TM, NT>(p, slot_out, t, c * 64 + half * 32 + i, r) =
-                                    make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]),
-                                                __uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
-                        continue;
-                    }
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        uint32_t y[4];
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            y[u] = T::narrow2(__uint_as_float(o[8 * v + 2 * u]), __uint_as_float(o[8 * v + 2 * u + 1]));
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                         stage + lane * 128 + (((half * 4 + v) ^ (lane & 7)) << 4)),
-                                     "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
-                                     : "memory");
-                    }
+                        for (int i = 0; i < 32; i += 4)
+                            *part_at<NC, TM, NT>(p, slot_out, t, col + i, r) =
+                                make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]),
+                                            __uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
+                    continue;
                 }
-                if (!whole) continue;
-                __syncwarp();
-                const bool in = c * 64 + (lane & 7) * 8 < p.D;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int row = k * 4 + lane / 8;
+                for (int v = 0; v < 4; ++v) {
+                    uint32_t y[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        y[u] = T::narrow2(__uint_as_float(o[8 * v + 2 * u]), __uint_as_float(o[8 * v + 2 * u + 1]));
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     stage + lane * 64 + ((v ^ ((lane >> 1) & 3)) << 4)),
+                                 "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+                                 : "memory");
+                }
+                __syncwarp();
+                const bool in = col + (lane & 3) * 8 < p.D;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int row = k * 8 + lane / 4;
                     uint4 y;
                     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                                  : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
-                                 : "r"(stage + row * 128 + (((lane & 7) ^ (row & 7)) << 4))
+                                 : "r"(stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4))
                                  : "memory");
-                    const int64_t to = __shfl_sync(0xFFFFFFFFu, mine, row) + c * 128 + (lane & 7) * 16;
+                    const int64_t to = __shfl_sync(0xFFFFFFFFu, mine, row) + (col + (lane & 3) * 8) * 2;
                     if (__shfl_sync(0xFFFFFFFFu, static_cast<int>(real), row) && in)
                         *reinterpret_cast<uint4 *>(to) = y;
                 }
@@ -382,6 +411,9 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
         const uint32_t q_bytes = NC * p.tile_rows * 128;
         uint32_t j = 0, q_uses[2] = {0, 0};
         const auto all = [](bool yes) { return __all_sync(0xFFFFFFFFu, yes) != 0; };
+        const auto wait_all = [&](uint64_t *bar, uint32_t parity) {  // one lane asks
+            return all(lane != 0 || wait(sh, bar, parity));
+        };
         bool ok = true;
         for (uint32_t item = 0; ok && all(there_is(item)); ++item) {
             const Item my = sh.item[item % ITEMS];
@@ -394,7 +426,7 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
             };
             // a tile's keys or values into their slot, once that is free
             const auto bring = [&](const CUtensorMap *map, uint64_t *full, uint64_t *free, int chunk, int2 at) {
-                if (j >= RING && !all(wait(sh, free, (j / RING - 1) & 1))) return false;
+                if (j >= RING && !wait_all(free, (j / RING - 1) & 1)) return false;
                 if (lane == 0) mbar_expect_tx(full, NC * CHUNK);
                 __syncwarp();
                 const uint32_t dst = ring + j % RING * Z::TILE + chunk * CHUNK + lane * p.box_rows * 128;
@@ -415,7 +447,7 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
                         if (my.nt[t] > 0) {
-                            ok = ok && (q_uses[t] == 0 || all(wait(sh, &sh.q_free[t], (q_uses[t] - 1) & 1)));
+                            ok = ok && (q_uses[t] == 0 || wait_all(&sh.q_free[t], (q_uses[t] - 1) & 1));
                             if (!ok) break;
                             ++q_uses[t];
                             if (lane == 0) {
@@ -444,57 +476,55 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
         }
     } else if (warp == 1) {
         if (elect_one()) {
-            // ---- MMA issuer: a tile's products, then the scores of two tiles on, in turn
+            // ---- MMA issuer: a tile's products, then the next scores of the same rows, in turn
             constexpr uint32_t id_s = idesc_of<T>(TN, false), id_o = idesc_of<T>(NC * 64, true);
             const uint64_t qd = smem_desc_sw128(q_s), kd = smem_desc_sw128(ring);
-            const uint64_t vd = smem_desc_rows_k(ring) + NC * (CHUNK >> 4);
-            uint32_t q_uses[2] = {0, 0}, tails = 0;
+            const uint64_t vd = smem_desc_rows_k(ring, CHUNK) + NC * (CHUNK >> 4);
+            // the numbers of the next key tile, and of the next one that a row tile meets, for the
+            // products and for the scores
+            uint32_t gv = 0, gk = 0, mv[2] = {0, 0}, mk[2] = {0, 0}, q_uses[2] = {0, 0};
             for (uint32_t item = 0; there_is(item); ++item) {
-                const Item my = sh.item[item % ITEMS];
-                const int n = my.tiles(), last = my.last();
-                // row tile t's scores against the item's tile j
-                const auto scores = [&](int t, int j) {
-                    const uint32_t g = my.g0 + j, b = (my.met[t] + j) & 1;
-                    if (!wait(sh, &sh.k_full[g % RING], (g / RING) & 1)) return;
-                    tc_fence_after();
-                    const uint32_t d = tmem + t * 128 + b * 64;
-                    const uint64_t a_d = qd + t * (NC * (Q_CHUNK >> 4)), b_d = kd + g % RING * (Z::TILE >> 4);
-#pragma unroll
-                    for (int c = 0; c < NC; ++c)
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            mma_bf16(d, a_d + c * (Q_CHUNK >> 4) + 2 * u, b_d + c * (CHUNK >> 4) + 2 * u, id_s,
-                                     (c | u) != 0);
-                    mma_commit(&sh.s_full[t][b]);
-                    if (j + 1 == my.nt[t]) mma_commit(&sh.q_free[t]);
-                    if (t == last) mma_commit(&sh.k_free[g % RING]);
-                };
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-                        if (j < my.nt[t] && !sh.abort) {
-                            if (j == 0 && !wait(sh, &sh.q_full[t], q_uses[t]++ & 1)) break;
-                            scores(t, j);
-                        }
-                for (int j = 0; j < n && !sh.abort; ++j) {
-                    const uint32_t g = my.g0 + j;
-                    if (!wait(sh, &sh.v_full[g % RING], (g / RING) & 1)) break;
-                    if (j == my.tail && !wait(sh, &sh.v_clean, tails++ & 1)) break;
+                const int nt[2] = {sh.item[item % ITEMS].nt[0], sh.item[item % ITEMS].nt[1]}, n = max(nt[0], nt[1]);
+                for (int j = -SB; j < n && !sh.abort; ++j) {
+                    const uint32_t vs = gv % RING, ks = gk % RING;
+                    if (j >= 0 && !wait(sh, &sh.v_full[vs], (gv / RING) & 1)) break;
+                    bool keys = false;  // tile j + SB's have been waited for
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        if (j >= my.nt[t]) continue;
-                        const uint32_t step = my.met[t] + j, b = step & 1;
-                        if (!wait(sh, &sh.p_ready[t][b], (step >> 1) & 1)) break;
-                        tc_fence_after();
-                        const uint32_t a_d = tmem + t * 128 + b * 64, d = tmem + O_COL + t * 128;
-                        const uint64_t b_d = vd + g % RING * (Z::TILE >> 4);
+                        if (j >= 0 && j < nt[t]) {
+                            if (!wait(sh, &sh.p_ready[t][mv[t] % SB], (mv[t] / SB) & 1)) break;
+                            tc_fence_after();
+                            const uint32_t a_d = tmem + t * 128 + mv[t] % SB * TN, d = tmem + O_COL + t * 128;
+                            const uint64_t b_d = vd + vs * (Z::TILE >> 4);
 #pragma unroll
-                        for (int u = 0; u < TN / 16; ++u)
-                            mma_ts(d, a_d + 8 * u, b_d + u * (2048 >> 4), id_o, (j | u) != 0);
-                        mma_commit(&sh.pv_done[t][b]);
-                        if (t == last) mma_commit(&sh.v_free[g % RING]);
-                        if (j + 2 < my.nt[t]) scores(t, j + 2);
+                            for (int u = 0; u < TN / 16; ++u)
+                                mma_ts(d, a_d + 8 * u, b_d + u * (2048 >> 4), id_o, (j | u) != 0);
+                            mma_commit(&sh.pv_done[t][mv[t] % SB]);
+                            ++mv[t];
+                        }
+                        if (t == NT - 1 && j >= 0) mma_commit(&sh.v_free[vs]);
+                        if (j + SB < nt[t]) {
+                            if (!keys && !wait(sh, &sh.k_full[ks], (gk / RING) & 1)) break;
+                            keys = true;
+                            if (j == -SB && !wait(sh, &sh.q_full[t], q_uses[t]++ & 1)) break;
+                            const uint32_t d = tmem + t * 128 + mk[t] % SB * TN;
+                            const uint64_t a_d = qd + t * (NC * (Q_CHUNK >> 4)), b_d = kd + ks * (Z::TILE >> 4);
+#pragma unroll
+                            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                                for (int u = 0; u < 4; ++u)
+                                    mma_bf16(d, a_d + c * (Q_CHUNK >> 4) + 2 * u, b_d + c * (CHUNK >> 4) + 2 * u, id_s,
+                                             (c | u) != 0);
+                            mma_commit(&sh.s_full[t][mk[t] % SB]);
+                            if (j + SB + 1 == nt[t]) mma_commit(&sh.q_free[t]);
+                            ++mk[t];
+                        }
                     }
+                    if (keys) {
+                        mma_commit(&sh.k_free[ks]);
+                        ++gk;
+                    }
+                    gv += j >= 0;
                 }
                 mbar_arrive(&sh.item_free[item % ITEMS]);
                 if (sh.abort) break;
@@ -556,7 +586,7 @@ cudaError_t launch(const HeadsAttnArgs &a, cudaStream_t stream) {
     const int G = a.Hq / a.Hkv;
     Params p;
     Maps maps;
-    if (!set_up(a, TM / G * G, Z::NT, TN, true, y.plan, y.part, y.lse, p, maps)) return cudaErrorInvalidValue;
+    if (!set_up(a, TM / G * G, Z::NT, Z::TN, true, y.plan, y.part, y.lse, p, maps)) return cudaErrorInvalidValue;
     static AttrCache attr;
     cudaError_t e = ensure_attr(k_heads_chunk<T, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::SMEM, attr);
     if (e != cudaSuccess) return e;

@@ -127,11 +127,11 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
         } else if (lane == 16) {
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&sh.s_full[i], 1);
-                mbar_init(&sh.q_full[i], 32);
+                mbar_init(&sh.q_full[i], 1);
                 mbar_init(&sh.item_full[i], 1);
                 mbar_init(&sh.item_free[i], 6);  // the producer, the issuer, four softmax warps
             }
-            mbar_init(&sh.p_ready, 128);
+            mbar_init(&sh.p_ready, 4);
             mbar_init(&sh.pv_done, 1);
             mbar_init(&sh.drained, 1);
             sh.abort = 0;
@@ -197,7 +197,7 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
                 if (i + 1 < my.tiles) look(i + 1);
 #pragma unroll
                 for (int c = 0; c < 2 * NC; ++c) {
-                    if (!all(wait(sh, &sh.empty[s], ph))) {
+                    if (!all(lane != 0 || wait_long(sh, &sh.empty[s], ph))) {
                         ok = false;
                         break;
                     }
@@ -211,6 +211,7 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
                     Z::step(s, ph, 1);
                 }
             }
+            __syncwarp();  // (all lanes have read the item)
             if (lane == 0) mbar_arrive(&sh.item_free[item & 1]);
             if (!ok || !all(next_item(item))) break;
         }
@@ -329,7 +330,8 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
             fence_async_smem();
-            mbar_arrive(&sh.q_full[item & 1]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.q_full[item & 1]);
             it.g0 += it.tiles;
             const bool more = next(it);
             if (!__all_sync(0xFFFFFFFFu, item == 0 || wait_far(sh, &sh.item_free[(item - 1) & 1],
@@ -459,7 +461,8 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
                 }
                 fence_async_smem();
                 tc_fence_before();
-                mbar_arrive(&sh.p_ready);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.p_ready);
             }
             // ---- epilogue
             l = meet(l, [](float a, float b) { return a + b; });
