@@ -648,9 +648,11 @@ def _pages(block_table, held, refs):
     """(table, held, refs pointers; B, max_pages, num_pages)."""
     if getattr(block_table, "ndim", 0) != 2:
         _refuse_axes(block_table=(block_table, 2))
+    if _INT is None:
+        _half_codes()
     B, max_pages = block_table.shape
-    return (_arg(block_table, "block_table", _I32), _arg(held, "held", _I32, B),
-            _arg(refs, "refs", _I32)), (B, max_pages, refs.numel())
+    return (_vec(block_table, "block_table", _INT, _I32), _vec(held, "held", _INT, _I32, B),
+            _vec(refs, "refs", _INT, _I32)), (B, max_pages, refs.numel())
 
 
 def mtp_pages_resize(keep, lens, block_table, held, refs, page_size: int, copies=None, status=None,
@@ -660,8 +662,8 @@ def mtp_pages_resize(keep, lens, block_table, held, refs, page_size: int, copies
     rows left for their own (see include/libmtpspec/pages.h)."""
     ptrs, sizes = _pages(block_table, held, refs)
     B = sizes[0]
-    _call("mtp_pages_resize", _arg(keep, "keep", _I32, B), _arg(lens, "lens", _I32, B), *ptrs, *sizes,
-          int(page_size), _arg(copies, "copies", _I32, 2 * B, optional=True),
+    _call("mtp_pages_resize", _vec(keep, "keep", _INT, _I32, B), _vec(lens, "lens", _INT, _I32, B), *ptrs,
+          *sizes, int(page_size), copies if copies is None else _vec(copies, "copies", _INT, _I32, 2 * B),
           _arg(status, "status", _I32, 1, optional=True), _stream(stream))
     return block_table
 
@@ -669,9 +671,9 @@ def mtp_pages_resize(keep, lens, block_table, held, refs, page_size: int, copies
 def mtp_pages_fork(src_rows, dst_rows, block_table, held, refs, status=None, stream=None):
     """Row dst_rows[i] gives back its pages and shares those of src_rows[i]."""
     ptrs, sizes = _pages(block_table, held, refs)
-    src = _arg(src_rows, "src_rows", _I32)
+    src = _vec(src_rows, "src_rows", _INT, _I32)
     n = src_rows.numel()
-    _call("mtp_pages_fork", src, _arg(dst_rows, "dst_rows", _I32, n), n, *ptrs, *sizes,
+    _call("mtp_pages_fork", src, _vec(dst_rows, "dst_rows", _INT, _I32, n), n, *ptrs, *sizes,
           _arg(status, "status", _I32, 1, optional=True), _stream(stream))
     return block_table
 
@@ -689,26 +691,32 @@ def mtp_pages_compact(block_table, held, refs, moves, n_moves, status=None, stre
 def mtp_pages_copy(caches, pairs, n_pairs=None, status=None, stream=None):
     """Page pairs[i][1] of every cache (tensors [pages, ...] of one shape and type, a page's
     elements contiguous) becomes a copy of its page pairs[i][0]."""
-    caches = list(caches)
-    if not caches:
-        raise ValueError("caches is empty")
-    first, ptrs = caches[0], []
+    tensor, ptrs, first = _kinds()["tensor"], [], None
     for c in caches:
-        if not isinstance(c, _kinds()["tensor"]):
+        if not isinstance(c, tensor):
             raise TypeError("caches must be torch tensors")
         if not c.is_cuda:
             raise ValueError("caches must live on a CUDA device")
-        if c.dim() < 2 or c.shape[0] < 1 or not c[0].is_contiguous():
-            raise ValueError("a cache must be [pages, ...] with contiguous pages")
-        if c.shape != first.shape or c.dtype != first.dtype or c.stride() != first.stride():
+        if first is None:
+            first, shape, strides, dtype = c, c.shape, c.stride(), c.dtype
+            page = 1  # a page's elements, which must follow one another
+            for n, st in zip(reversed(shape[1:]), reversed(strides[1:])):
+                if n != 1 and st != page:
+                    page = 0
+                    break
+                page *= n
+            if len(shape) < 2 or page == 0 or shape[0] < 1:
+                raise ValueError("a cache must be [pages, ...] with contiguous pages")
+        elif c.shape != shape or c.dtype != dtype or c.stride() != strides:
             raise ValueError("caches must have one shape, type and layout")
         ptrs.append(c.data_ptr())
-    size = first.element_size()
-    page = first[0].numel() * size
-    stride = first.stride(0) * size if first.shape[0] > 1 else page
+    if first is None:
+        raise ValueError("caches is empty")
+    page *= first.element_size()
+    stride = strides[0] * first.element_size() if shape[0] > 1 else page
     p = _arg(pairs, "pairs", _I32)
     if pairs.dim() != 2 or pairs.shape[1] != 2:
         raise ValueError(f"pairs must be [n, 2], got {tuple(pairs.shape)}")
-    _call("mtp_pages_copy", (C.c_void_p * len(ptrs))(*ptrs), len(ptrs), first.shape[0], page, stride, p,
+    _call("mtp_pages_copy", (C.c_void_p * len(ptrs))(*ptrs), len(ptrs), shape[0], page, stride, p,
           pairs.shape[0], _arg(n_pairs, "n_pairs", _I32, 1, optional=True),
           _arg(status, "status", _I32, 1, optional=True), _stream(stream))

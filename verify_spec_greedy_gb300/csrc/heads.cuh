@@ -310,20 +310,25 @@ __device__ __forceinline__ void wait_out(uint64_t *bar, uint32_t parity) {
         if (mbar_test(bar, parity)) return;
 }
 
-// A tile of keys in boxes that stay within a page, one a lane: where this lane's box of the tile
-// lies.  Beyond the row's length, and where the table has no such page, TMA fills zeros.
-__device__ __forceinline__ int2 find_box(const Params &p, const int32_t *table, int key, int len, bool mine) {
-    const int pi = key / p.page_size, slot = key - pi * p.page_size;
-    int page = p.num_pages;
-    if (mine && key < len) {
-        page = table[pi];
-        if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) {
-            page = p.num_pages;
-            if (p.status) atomicOr(p.status, MTPSPEC_STATUS_BAD_PARAM);
-        }
+// A tile of keys in boxes that stay within a page, one a lane: where this lane's box of the tile lies.
+// Its page's number is asked for by look() and looked at by settle(), a tile later, so that nothing
+// waits for the answer.
+struct Box {
+    int page, slot;
+    bool mine;
+    __device__ __forceinline__ void look(const Params &p, const int32_t *table, int key, int len, bool lane_has) {
+        const int pi = key / p.page_size;
+        slot = key - pi * p.page_size;
+        mine = lane_has && key < len;
+        if (mine) page = table[pi];
     }
-    return make_int2(page, slot);
-}
+    // (page, row of it): beyond the row's length, and where the table has no such page, TMA fills zeros
+    __device__ __forceinline__ int2 settle(const Params &p) const {
+        const bool good = mine && static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages);
+        if (mine && !good && p.status) atomicOr(p.status, MTPSPEC_STATUS_BAD_PARAM);
+        return make_int2(good ? page : p.num_pages, slot);
+    }
+};
 
 // Partial outputs lie by fours of columns, the rows side by side (a thread that has a row's columns
 // writes beside its neighbours): float4 number ((slot * TILES + tile) * 16 NC + column / 4) * TM + row.
@@ -435,9 +440,9 @@ inline bool set_up(const HeadsAttnArgs &a, int tile_rows, int tiles, int TN, boo
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
     const auto u = [](int64_t x) { return static_cast<cuuint64_t>(x); };
-    const cuuint64_t cd[4] = {u(a.D), u(a.Hkv), u(a.page_size), u(a.num_pages)},
-                     cs[3] = {u(head * 2), u(slot * 2), u(page * 2)};
-    const cuuint32_t cb[4] = {64, 1, static_cast<cuuint32_t>(p.box_rows), 1};
+    const cuuint64_t cd[4] = {u(a.D), u(a.page_size), u(a.Hkv), u(a.num_pages)},
+                     cs[3] = {u(slot * 2), u(head * 2), u(page * 2)};
+    const cuuint32_t cb[4] = {64, static_cast<cuuint32_t>(p.box_rows), 1, 1};
     if (!encode(&maps.k, a.k_cache, cd, cs, cb) || !encode(&maps.v, a.v_cache, cd, cs, cb)) return false;
     if (q_map) {
         const cuuint64_t qd[4] = {u(a.D), u(p.G), u(a.Tq), u(a.Hkv)},

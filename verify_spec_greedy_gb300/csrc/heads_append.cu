@@ -16,37 +16,12 @@ namespace hap {
 
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
-constexpr int U = 4;  // groups of heads that a warp has in flight
 
-template <typename T, bool PAIRS>
-__global__ void __launch_bounds__(THREADS)
-k_heads_append(const HeadsAppendArgs a, const int lpv, const int heads, const int runs) {
-    const int lane = threadIdx.x & 31;
-    const int64_t warp = static_cast<int64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5);
-    const int64_t t = warp / runs;
-    if (t >= a.T) return;
-    const int run = static_cast<int>(warp - t * runs);
-    const int per = 32 / lpv, sub = lane / lpv, vec = lane - sub * lpv;
-    const bool in = vec * 8 < a.D;
-    const int nq = a.q ? a.Hq : 0;
-    // the values are loaded before the token's position is known: the two chains overlap
-    uint4 x[U];
-    int h[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        h[u] = (run * U + u) * per + sub;
-        x[u] = make_uint4(0, 0, 0, 0);
-        if (!in || h[u] >= heads) {
-            h[u] = -1;
-            continue;
-        }
-        const int g = h[u] - nq;
-        const uint16_t *src = g < 0          ? a.q + t * a.q_tok + h[u] * a.q_head
-                              : g < a.Hkv ? a.k + t * a.k_tok + g * a.k_head
-                                          : a.v + t * a.v_tok + (g - a.Hkv) * a.v_head;
-        x[u] = *reinterpret_cast<const uint4 *>(src + vec * 8);
-    }
-    const int row = a.tok_row[t], pos = a.positions[t];
+// A run of U groups of heads of token t, whose values x are on their way.
+template <typename T, bool PAIRS, int U>
+__device__ __forceinline__ void append_run(const HeadsAppendArgs &a, const uint4 (&x)[U], const int (&h)[U],
+                                           int64_t t, int run, int row, int pos, int lpv, int vec, bool in, int nq) {
+    const int lane = threadIdx.x & 31, per = 32 / lpv;
     const bool good = row >= 0 && row < a.B && pos >= 0 && pos < a.pos_end;
     int page = -1, off = 0;
     if (good) {
@@ -87,6 +62,12 @@ k_heads_append(const HeadsAppendArgs a, const int lpv, const int heads, const in
     for (int u = 0; u < U; ++u) {
         const int g = h[u] - nq;
         const bool query = g < 0, value = g >= a.Hkv;
+        if (__all_sync(0xFFFFFFFFu, value || h[u] < 0)) {  // a group of values: as they are
+            if (h[u] >= 0 && page >= 0)
+                *reinterpret_cast<uint4 *>(a.v_cache + page * a.page_stride + off * a.slot_stride +
+                                           (g - a.Hkv) * a.head_stride + vec * 8) = x[u];
+            continue;
+        }
         float f[8];
         half8_to_float<T>(x[u], f);
         // (all lanes take part in the shuffles, whatever they hold)
@@ -127,26 +108,64 @@ k_heads_append(const HeadsAppendArgs a, const int lpv, const int heads, const in
     }
 }
 
-template <typename T>
-cudaError_t launch(const HeadsAppendArgs &a, cudaStream_t stream) {
-    int lpv = 2;
-    while (lpv * 8 < a.D) lpv *= 2;
-    const int heads = (a.q ? a.Hq : 0) + 2 * a.Hkv;
+// A warp a run of U groups.
+template <typename T, bool PAIRS, int U>
+__global__ void __launch_bounds__(THREADS, U <= 4 ? 4 : 3)
+k_heads_append(const HeadsAppendArgs a, const uint32_t lpv, const uint32_t heads, const uint32_t runs) {
+    const uint32_t lane = threadIdx.x & 31, warp = blockIdx.x * WARPS + (threadIdx.x >> 5);
+    const uint32_t tok = warp / runs, run = warp - tok * runs;  // (at most 2^20 tokens x 768 runs)
+    const int64_t t = tok;
+    if (t >= a.T) return;
+    const int per = 32 / lpv, sub = lane / lpv, vec = lane - sub * lpv;
+    const bool in = vec * 8 < a.D;
+    const int nq = a.q ? a.Hq : 0;
+    // the values are loaded before the token's position is known: the two chains overlap
+    uint4 x[U];
+    int h[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        h[u] = (run * U + u) * per + sub;
+        x[u] = make_uint4(0, 0, 0, 0);
+        if (!in || h[u] >= static_cast<int>(heads)) {
+            h[u] = -1;
+            continue;
+        }
+        const int g = h[u] - nq;
+        const uint16_t *src = g < 0          ? a.q + t * a.q_tok + h[u] * a.q_head
+                              : g < a.Hkv ? a.k + t * a.k_tok + g * a.k_head
+                                          : a.v + t * a.v_tok + (g - a.Hkv) * a.v_head;
+        x[u] = *reinterpret_cast<const uint4 *>(src + vec * 8);
+    }
+    append_run<T, PAIRS, U>(a, x, h, t, run, a.tok_row[t], a.positions[t], lpv, vec, in, nq);
+}
+
+template <typename T, int U>
+cudaError_t launch(const HeadsAppendArgs &a, int lpv, int heads, cudaStream_t stream) {
     const int run = U * (32 / lpv), runs = (heads + run - 1) / run;
     const unsigned grid = static_cast<unsigned>((a.T * runs + WARPS - 1) / WARPS);
     if (a.interleaved)
-        k_heads_append<T, true><<<grid, THREADS, 0, stream>>>(a, lpv, heads, runs);
+        k_heads_append<T, true, U><<<grid, THREADS, 0, stream>>>(a, lpv, heads, runs);
     else
-        k_heads_append<T, false><<<grid, THREADS, 0, stream>>>(a, lpv, heads, runs);
+        k_heads_append<T, false, U><<<grid, THREADS, 0, stream>>>(a, lpv, heads, runs);
     const cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) count_launches(1);
     return e;
+}
+template <typename T>
+cudaError_t pick(const HeadsAppendArgs &a, cudaStream_t s) {
+    int lpv = 2;
+    while (lpv * 8 < a.D) lpv *= 2;
+    const int heads = (a.q ? a.Hq : 0) + 2 * a.Hkv;
+    // few heads in all are spread over as many warps as there are, many keep four groups a warp in
+    // flight
+    const int64_t groups = (static_cast<int64_t>(heads) * lpv + 31) / 32 * a.T;
+    return groups >= 4 * 152 * 24 ? launch<T, 4>(a, lpv, heads, s) : launch<T, 1>(a, lpv, heads, s);
 }
 
 }  // namespace hap
 
 cudaError_t run_heads_append(const HeadsAppendArgs &a, int dtype, cudaStream_t stream) {
-    return dtype == MTPSPEC_BF16 ? hap::launch<Bf16>(a, stream) : hap::launch<F16>(a, stream);
+    return dtype == MTPSPEC_BF16 ? hap::pick<Bf16>(a, stream) : hap::pick<F16>(a, stream);
 }
 
 }  // namespace mtpspec

@@ -420,9 +420,9 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
             const int n = my.tiles();
             // the page of this lane's box of the item's tile i
             const int32_t *table = p.block_table + static_cast<int64_t>(my.row) * p.max_pages;
-            int2 box = {};
+            Box box = {};
             const auto look = [&](int i) {
-                box = find_box(p, table, my.u.key_tile(my.i0 + i) * TN + lane * p.box_rows, my.u.len, lane < boxes);
+                box.look(p, table, my.u.key_tile(my.i0 + i) * TN + lane * p.box_rows, my.u.len, lane < boxes);
             };
             // a tile's keys or values into their slot, once that is free
             const auto bring = [&](const CUtensorMap *map, uint64_t *full, uint64_t *free, int chunk, int2 at) {
@@ -433,13 +433,13 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
                 if (lane < boxes)
 #pragma unroll
                     for (int c = 0; c < NC; ++c)
-                        tma_load_4d(dst + c * CHUNK, map, c * 64, my.head, at.y, at.x, full);
+                        tma_load_4d(dst + c * CHUNK, map, c * 64, at.y, my.head, at.x, full);
                 __syncwarp();
                 return true;
             };
             if (n > 0) look(0);
             for (int i = 0; ok && i < n; ++i, ++j) {
-                const int2 to = box;
+                const int2 to = box.settle(p);
                 if (i + 1 < n) look(i + 1);
                 const uint32_t slot = j % RING;
                 ok = bring(&maps.k, &sh.k_full[slot], &sh.k_free[slot], 0, to);

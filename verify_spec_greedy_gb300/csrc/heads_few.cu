@@ -37,6 +37,7 @@ struct __align__(16) Shared {
     uint64_t s_full[2], p_ready, pv_done, q_full[2], item_full[2], item_free[2], drained;
     Item<TN> item[2];
     Scan scan;
+    int2 box[2][16];  // boxes of a tile, in turn
     uint32_t tmem;
     volatile int abort;
     float other[2][128 / ROWS][ROWS];  // what the threads of a row tell each other
@@ -178,7 +179,7 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
     if (sh.item[0].head < 0) {
         // nothing: fewer tiles than CTAs
     } else if (warp == 0) {
-        // ---- producer: a box of a tile a lane
+        // ---- producer: a lane finds a box of a tile, and one thread issues all copies
         const int boxes = TN / p.box_rows;
         const auto all = [](bool yes) { return __all_sync(0xFFFFFFFFu, yes) != 0; };
         int s = 0, filled = 0;
@@ -187,29 +188,38 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
         for (uint32_t item = 0;; ++item) {
             const Item<TN> my = sh.item[item & 1];
             const int32_t *table = p.block_table + static_cast<int64_t>(my.row) * p.max_pages;
-            int2 box = {};
+            Box box = {};
             const auto look = [&](int i) {
-                box = find_box(p, table, my.u.key_tile(my.i0 + i) * TN + lane * p.box_rows, my.u.len, lane < boxes);
+                box.look(p, table, my.u.key_tile(my.i0 + i) * TN + lane * p.box_rows, my.u.len, lane < boxes);
             };
             if (my.tiles > 0) look(0);
             for (int i = 0; ok && i < my.tiles; ++i) {
-                const int2 to = box;
+                int2 *at = sh.box[i & 1];
+                if (lane < boxes) at[lane] = box.settle(p);
                 if (i + 1 < my.tiles) look(i + 1);
+                __syncwarp();
+                if (elect_one()) {
+                    int slot = s;
+                    uint32_t phase = ph;
 #pragma unroll
-                for (int c = 0; c < 2 * NC; ++c) {
-                    if (!all(lane != 0 || wait_long(sh, &sh.empty[s], ph))) {
-                        ok = false;
-                        break;
+                    for (int c = 0; c < 2 * NC; ++c) {
+                        ok = ok && wait(sh, &sh.empty[slot], phase);
+                        if (!ok) break;
+                        mbar_expect_tx(&sh.full[slot], CHUNK);
+                        uint32_t dst = ring + slot * CHUNK;
+#pragma unroll 4
+                        for (int k = 0; k < boxes; ++k) {
+                            const int2 x = at[k];
+                            tma_load_4d(dst, c < NC ? &maps.k : &maps.v, c % NC * 64, x.y, my.head, x.x, &sh.full[slot]);
+                            dst += p.box_rows * 128;
+                        }
+                        Z::step(slot, phase, 1);
                     }
-                    ++filled;
-                    if (lane == 0) mbar_expect_tx(&sh.full[s], CHUNK);
-                    __syncwarp();
-                    if (lane < boxes)
-                        tma_load_4d(ring + s * CHUNK + lane * p.box_rows * 128, c < NC ? &maps.k : &maps.v,
-                                    c % NC * 64, my.head, to.y, to.x, &sh.full[s]);
-                    __syncwarp();
-                    Z::step(s, ph, 1);
                 }
+                __syncwarp();
+                ok = all(ok);
+                filled += 2 * NC;
+                Z::step(s, ph, 2 * NC);
             }
             __syncwarp();  // (all lanes have read the item)
             if (lane == 0) mbar_arrive(&sh.item_free[item & 1]);
