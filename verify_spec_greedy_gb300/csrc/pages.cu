@@ -50,26 +50,33 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *sums, int64_t 
     return at - v + (warp == 0 ? 0 : before);
 }
 
-// Which pages of the window [base, base + WINDOW) a predicate holds for, in order of their
-// numbers: calls put(rank in the window, page) for each, and returns how many there are.  Thread
-// i looks at pages base + 1024 j + i, so that loads are whole lines.  `counts` is shared.
+// The counts of a window's pages, as thread i looks at them: pages base + 1024 j + i, so that loads are
+// whole lines.
+struct Window {
+    int32_t ref[PER];
+    __device__ __forceinline__ void load(const int32_t *refs, int64_t base, int64_t end) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int64_t p = base + j * THREADS + threadIdx.x;
+            ref[j] = p < end ? __ldcg(refs + p) : 0;
+        }
+    }
+};
+// Which pages of the window [base, base + WINDOW) a predicate holds for, in order of their numbers:
+// calls put(rank in the window, page) for each, and returns how many there are.  `w` is the window,
+// and then the one after it, on its way meanwhile.  `counts` is shared.
 template <typename P, typename F>
-__device__ __forceinline__ int window_ranks(int64_t base, int64_t end, int (*counts)[WARPS],
-                                            const P &holds, const F &put) {
+__device__ __forceinline__ int window_ranks(const int32_t *refs, Window &w, int64_t base, int64_t end,
+                                            int (*counts)[WARPS], const P &holds, const F &put) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     unsigned has[PER];
-    int32_t ref[PER];
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
         const int64_t p = base + j * THREADS + threadIdx.x;
-        ref[j] = p < end ? holds.load(p) : 0;
-    }
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        const int64_t p = base + j * THREADS + threadIdx.x;
-        has[j] = __ballot_sync(ALL, p < end && holds(ref[j]));
+        has[j] = __ballot_sync(ALL, p < end && holds(w.ref[j]));
         if (lane == 0) counts[j][warp] = __popc(has[j]);
     }
+    w.load(refs, base + WINDOW, end);
     __syncthreads();
     // every warp adds up all counts, a column of eight a lane, and keeps its own places
     int total = 0, mine[PER];
@@ -94,13 +101,9 @@ __device__ __forceinline__ int window_ranks(int64_t base, int64_t end, int (*cou
 }
 
 struct IsFree {
-    const int32_t *refs;
-    __device__ int32_t load(int64_t p) const { return __ldcg(refs + p); }
     __device__ bool operator()(int32_t r) const { return r == 0; }
 };
 struct IsLive {
-    const int32_t *refs;
-    __device__ int32_t load(int64_t p) const { return __ldcg(refs + p); }
     __device__ bool operator()(int32_t r) const { return r > 0; }
 };
 
@@ -137,6 +140,17 @@ __global__ void __launch_bounds__(THREADS) k_pages_resize(const PagesResizeArgs 
     __shared__ int counts[PER][WARPS];
     __shared__ unsigned leaving[16384 / 32];  // the rows that leave their last page
     const int tid = threadIdx.x;
+    // (a thread's first row, which is its only one up to 1024 rows, stays in registers)
+    Row mine = {};
+    int32_t my_last = -1;
+    if (tid < a.B) {
+        mine = row_of(a, tid);
+        if (mine.partly) my_last = a.block_table[tid * a.max_pages + mine.kept - 1];
+    }
+    const auto row = [&](int64_t b) { return b == tid ? mine : row_of(a, b); };
+    const auto last_page = [&](int64_t b, const Row &r) {
+        return b == tid ? my_last : r.partly ? a.block_table[b * a.max_pages + r.kept - 1] : -1;
+    };
     // ---- 1. pages given back
     for (int64_t b = tid / LANES; b < a.B; b += THREADS / LANES) {
         const int keep = a.keep[b];
@@ -155,24 +169,25 @@ __global__ void __launch_bounds__(THREADS) k_pages_resize(const PagesResizeArgs 
     for (int i = tid; i < 16384 / 32; i += THREADS) leaving[i] = 0;
     __syncthreads();
     // ---- 2. who leaves a page that others hold too
-    const auto last_page = [&](int64_t b, const Row &r) {
-        return r.partly ? a.block_table[b * a.max_pages + r.kept - 1] : -1;
-    };
-    if (a.copies) {
+    bool shared = false;
+    if (a.copies)
         for (int64_t b = tid; b < a.B; b += THREADS) {
-            const int32_t p = last_page(b, row_of(a, b));
-            if (is_page(a, p) && (__ldcg(a.refs + p) & 0xFFFF) > 1) atomicAdd(a.refs + p, 1 << 16);
+            const int32_t p = last_page(b, row(b));
+            if (is_page(a, p) && (__ldcg(a.refs + p) & 0xFFFF) > 1) {
+                atomicAdd(a.refs + p, 1 << 16);
+                shared = true;
+            }
         }
-        __syncthreads();
+    if (__syncthreads_or(shared)) {
         for (int64_t b = tid; b < a.B; b += THREADS) {
-            const int32_t p = last_page(b, row_of(a, b));
+            const int32_t p = last_page(b, row(b));
             if (!is_page(a, p)) continue;
             const int32_t v = __ldcg(a.refs + p);
             if (v < 0 || (v >> 16 > 0 && v >> 16 == (v & 0xFFFF))) atomicMin(a.refs + p, code_of(a, b));
         }
         __syncthreads();
         for (int64_t b = tid; b < a.B; b += THREADS) {
-            const int32_t p = last_page(b, row_of(a, b));
+            const int32_t p = last_page(b, row(b));
             if (!is_page(a, p)) continue;
             const int32_t v = __ldcg(a.refs + p);
             if (v < 0 ? v != code_of(a, b) : v >> 16 > 0)
@@ -180,7 +195,7 @@ __global__ void __launch_bounds__(THREADS) k_pages_resize(const PagesResizeArgs 
         }
         __syncthreads();
         for (int64_t b = tid; b < a.B; b += THREADS) {  // the counts again, without those who leave
-            const int32_t p = last_page(b, row_of(a, b));
+            const int32_t p = last_page(b, row(b));
             if (!is_page(a, p)) continue;
             const bool leaves = leaving[b >> 5] >> (b & 31) & 1;
             const int32_t v = __ldcg(a.refs + p);
@@ -192,19 +207,21 @@ __global__ void __launch_bounds__(THREADS) k_pages_resize(const PagesResizeArgs 
         __syncthreads();
     }
     // ---- 3. what the rows need, a run of rows a thread
+    Window window;
+    window.load(a.refs, 0, a.num_pages);
     const int64_t run = (a.B + THREADS - 1) / THREADS, b0 = tid * run, b1 = min(b0 + run, a.B);
     const auto need_of = [&](int64_t b, const Row &r) {
         return max(r.want - r.kept, int64_t{0}) + (leaving[b >> 5] >> (b & 31) & 1);
     };
     int64_t need = 0, total;
-    for (int64_t b = b0; b < b1; ++b) need += need_of(b, row_of(a, b));
+    for (int64_t b = b0; b < b1; ++b) need += need_of(b, row(b));
     const int64_t at = block_scan(need, sums, total);
     start[tid] = at;
     __syncthreads();
     // ---- free pages, lowest first, each to the row that it falls to
     int64_t found = 0;
     for (int64_t base = 0; base < a.num_pages && found < total; base += WINDOW) {
-        found += window_ranks(base, a.num_pages, counts, IsFree{a.refs}, [&](int rank, int64_t page) {
+        found += window_ranks(a.refs, window, base, a.num_pages, counts, IsFree{}, [&](int rank, int64_t page) {
             int64_t k = found + rank;
             if (k >= total) return;
             int lo = 0, hi = THREADS - 1;  // the last thread whose rows start at or before k
@@ -241,7 +258,7 @@ __global__ void __launch_bounds__(THREADS) k_pages_resize(const PagesResizeArgs 
     int64_t end = at;
     bool none = false;
     for (int64_t b = b0; b < b1; ++b) {
-        const Row r = row_of(a, b);
+        const Row r = row(b);
         const int64_t n = need_of(b, r), first = end;
         end += n;
         const bool leaves = leaving[b >> 5] >> (b & 31) & 1;
@@ -303,17 +320,24 @@ __global__ void __launch_bounds__(FORK_THREADS) k_pages_fork(const PagesForkArgs
 __global__ void __launch_bounds__(THREADS) k_pages_compact(const PagesCompactArgs a) {
     __shared__ int64_t sums[WARPS];
     __shared__ int counts[PER][WARPS];
-    const IsLive live{a.refs};
+    const IsLive live;
+    Window window;
     int64_t mine = 0, L;
-    for (int64_t p = threadIdx.x; p < a.num_pages; p += THREADS) mine += live(live.load(p));
+    for (int64_t base = 0; base < a.num_pages; base += WINDOW) {
+        window.load(a.refs, base, a.num_pages);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) mine += live(window.ref[j]);
+    }
     block_scan(mine, sums, L);
     int n = 0, m = 0;
+    window.load(a.refs, 0, L);
     for (int64_t base = 0; base < L; base += WINDOW)
-        n += window_ranks(base, L, counts, IsFree{a.refs}, [&](int rank, int64_t p) {
+        n += window_ranks(a.refs, window, base, L, counts, IsFree{}, [&](int rank, int64_t p) {
             a.moves[2 * (static_cast<int64_t>(n) + rank) + 1] = static_cast<int32_t>(p);
         });
+    window.load(a.refs, L, a.num_pages);
     for (int64_t base = L; base < a.num_pages && m < n; base += WINDOW)
-        m += window_ranks(base, a.num_pages, counts, live, [&](int rank, int64_t p) {
+        m += window_ranks(a.refs, window, base, a.num_pages, counts, live, [&](int rank, int64_t p) {
             a.moves[2 * (static_cast<int64_t>(m) + rank)] = static_cast<int32_t>(p);
         });
     // (a negative count, which no row holds, is neither live nor free: then the two may differ)
@@ -322,7 +346,7 @@ __global__ void __launch_bounds__(THREADS) k_pages_compact(const PagesCompactArg
     for (int64_t i = threadIdx.x; i < a.num_pages / 2; i += THREADS) {
         int32_t *pair = a.moves + 2 * i;
         if (i < n) {
-            const int32_t from = pair[0], to = pair[1];
+            const int32_t from = pair[0], to = pair[1];  // (put there by this block, behind a barrier)
             a.refs[to] = a.refs[from];
             a.refs[from] = 0;
         } else {
