@@ -386,7 +386,7 @@ const char *mtpspec_status_string(int code);
  *            scope);
  *   which 1  the chunked verifier's counter poll in global memory (which also raises its
  *            abort flag);
- *   which 2  the tcgen05 kernels' waits: the GEMM's stage wait, the latent attention's polled
+ *   which 2  the tcgen05 kernels' waits: the GEMM's stage wait, both attentions' polled
  *            and suspended forms, and the decision by which two of its warps leave together.
  * Each wait must give up; then MTPSPEC_STATUS_TIMEOUT is OR-ed into *status (device memory,
  * int32 [1], not cleared by the call).  1 <= limit <= 2^20.  The pages have no counterpart;

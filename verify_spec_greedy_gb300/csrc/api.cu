@@ -75,6 +75,7 @@ MTPSPEC_API int mtpspec_selftest_wait_timeout(int which, uint32_t limit, int32_t
                                  : mtpspec::run_wait_selftest_gemm(limit, status, s);
     if (which == 2 && e == cudaSuccess) e = mtpspec::run_wait_selftest_latent_attn(limit, status, s);
     if (which == 2 && e == cudaSuccess) e = mtpspec::run_wait_selftest_latent_prefill(limit, status, s);
+    if (which == 2 && e == cudaSuccess) e = mtpspec::run_wait_selftest_heads(limit, status, s);
     return launched(e);
 }
 

@@ -1,5 +1,5 @@
 // Attention with grouped heads over the paged cache: which of its two kernels a call takes.
-#include "kernels.h"
+#include "heads.cuh"
 
 namespace mtpspec {
 namespace {
@@ -16,6 +16,37 @@ Form form_of(int64_t B, int64_t Tq, int32_t Hq, int32_t Hkv) {
 }
 
 }  // namespace
+
+// Diagnostic of the bounded waits, as the other kernels': on a barrier of two arrivals that got one,
+// both forms must give up after `limit` polls and raise the abort flag; if not, the timeout is taken
+// out of the status word.
+namespace heads {
+struct WaitShared {
+    uint64_t never;
+    volatile int abort;
+};
+__global__ void k_wait_selftest(uint32_t limit, int32_t *status) {
+    __shared__ WaitShared sh;
+    if (threadIdx.x != 0) return;
+    mbar_init(&sh.never, 2);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    mbar_arrive(&sh.never);
+    bool ok = true;
+    for (int form = 0; form < 2; ++form) {
+        sh.abort = 0;
+        const bool got = form == 0 ? wait(sh, &sh.never, 0, limit) : wait_long(sh, &sh.never, 0, limit);
+        ok &= !got && sh.abort;
+    }
+    if (!ok) atomicAnd(status, ~MTPSPEC_STATUS_TIMEOUT);
+}
+}  // namespace heads
+
+cudaError_t run_wait_selftest_heads(uint32_t limit, int32_t *status, cudaStream_t stream) {
+    heads::k_wait_selftest<<<1, 32, 0, stream>>>(limit, status);
+    const cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) count_launches(1);
+    return e;
+}
 
 size_t heads_attn_workspace_bytes(int64_t B, int64_t Tq, int32_t Hq, int32_t Hkv, int32_t D) {
     const Form f = form_of(B, Tq, Hq, Hkv);
