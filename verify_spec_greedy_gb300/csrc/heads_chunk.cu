@@ -8,14 +8,16 @@
 // sums the unrounded ones in fp32.  (In fp16 m lies 2^7 below that maximum, so that fewer weights
 // are subnormal: half_types.cuh.)
 //
-// Rows: the G = Hq / Hkv query heads of a key head meet the same keys, so a tile's 128 rows are
-// 128 / G tokens times G heads.  A unit of work is two such tiles (one, for heads of more than 128
-// elements), a thread a row in the softmax.
+// Rows: the G = Hq / Hkv query heads of a key head meet the same keys, so a unit's 128 rows are
+// 128 / G tokens times G heads.  Two threads a row in the softmax.
 //
-// Keys: tiles of 128, and a score buffer a row tile, whose first half becomes the weights (the left
-// operand of the second product): while the tensor cores work on one row tile, the other's softmax
-// runs.  A single row tile has two buffers, of 64 keys, beside its 256 output columns: the scores of
-// a tile are there before the weights of the one before are.
+// Keys: tiles of 128.  Tensor memory holds the output and two score buffers, whose first halves
+// become the weights (the left operand of the second product): the tensor cores compute the
+// scores two tiles ahead, across units as well, so that a softmax waits for nothing but the softmax
+// before.  (With two row tiles of one buffer each a round took what the chain scores - softmax -
+// products of a row tile takes, 4,200 cycles for 2,300 of products; keys and values are now read
+// twice as often, from L2.)  They stream through two rings of chunks (128 keys x 64 columns),
+// released one by one.
 //
 // A tile is brought in boxes that stay within a page, a box a lane of the producing warp.  With a
 // window, a unit meets the tiles of the first tokens, then those of the window.
@@ -33,37 +35,36 @@ namespace hch {
 
 using namespace heads;
 
-constexpr int TM = 128;            // rows of a tile in tensor memory
-constexpr int Q_CHUNK = TM * 128;  // bytes of a row tile x 64 columns of 16 bits
+constexpr int TM = 128;            // rows of a unit
+constexpr int Q_CHUNK = TM * 128;  // bytes of a unit's rows x 64 columns of 16 bits
+constexpr int THREADS = 448;       // warps 0, 3, 12, 13 TMA, 1 MMA, 2 items; 4-11 softmax
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int O_COL = 256;         // row tile t's scores: 128 t, its output: 256 + 128 t
+constexpr int O_COL = 256;         // the output; the score buffers lie at 0 and 128
+constexpr int AHEAD = 2;           // key tiles that the scores are ahead of the products
 constexpr int ITEMS = 4;
+constexpr int MAX_SLOTS = 4;       // tiles of either ring
 
-// An item of a CTA: tiles i0 .. i1 - 1 of a unit's list of n (at least 1); how many of them either
-// row tile meets, and which of them the row's keys end in, if that is not a whole tile; with the key
-// tiles before it, and the key tiles that either row tile met before.  head -1: no more.
+// An item of a CTA: tiles i0 .. i1 - 1 of a unit's list of n, and the key tiles before it.  Its
+// `tiles` are at least one.  head -1: no more.
 template <int TN>
 struct Item {
     Unit<TN> u;
-    int row, head, i0, i1, n;
-    int nt[2], tail;
-    uint32_t g0, met[2];
-    __device__ __forceinline__ int tiles() const { return max(nt[0], nt[1]); }
+    int row, head, i0, i1, n, tiles;
+    uint32_t g0;
 };
 
-constexpr int MAX_RING = 8;
-// Barriers by row tile are doubled, a phase for every other key tile: who waits for a tile may be one
-// behind, and a parity cannot tell two phases from none.
+// Barriers by tile are doubled, a phase for every other tile: who waits for a tile may be one behind,
+// and a parity cannot tell two phases from none.
 template <int TN>
 struct __align__(16) Shared {
-    uint64_t k_full[MAX_RING], v_full[MAX_RING], k_free[MAX_RING], v_free[MAX_RING];  // by the tile's slot
-    uint64_t q_full[2], q_free[2], s_full[2][2], p_ready[2][2], pv_done[2][2], drained;
+    uint64_t k_full[MAX_SLOTS], k_free[MAX_SLOTS], v_full[MAX_SLOTS], v_free[MAX_SLOTS];
+    uint64_t q_full[2], q_free[2], s_full[2], p_ready[2], pv_done[2], drained;
     uint64_t item_full[ITEMS], item_free[ITEMS];
     Item<TN> item[ITEMS];
-    Scan scan;
     uint32_t tmem;
     volatile int abort;
-    float other[2][2][TM];  // what the two threads of a row tell each other, by tile and half
+    int2 box[4][8];         // boxes of a tile, by producer
+    float other[2][2][TM];  // what the two threads of a row tell each other, in turn, by half
 };
 
 // Whether all of two warps that share rows say yes.  They meet at barrier `bar` in everything they
@@ -92,7 +93,7 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// A tile whose rows are the products' K axis and whose 64-column chunks are `chunk` bytes apart.
+// Chunks side by side whose rows are the products' K axis.
 __device__ __forceinline__ uint64_t smem_desc_rows_k(uint32_t addr, uint32_t chunk) {
     uint64_t d = 0;
     d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
@@ -112,51 +113,45 @@ __host__ __device__ constexpr uint32_t idesc_of(int n, bool b_rows_k) {
 // NC: the 64-column chunks of a head.
 template <int NC>
 struct Sizes {
-    static constexpr int NT = NC <= 2 ? 2 : 1;                      // row tiles of a unit
-    static constexpr int TN = NC <= 2 ? 128 : 64;                   // keys of a tile
-    static constexpr int SB = NC <= 2 ? 1 : 2;                      // score buffers of a row tile
-    static constexpr int CHUNK = TN * 128;                          // bytes of a key tile x 64 columns
-    static constexpr int HALVES = NT;                               // softmax threads of a row
-    static constexpr int THREADS = 128 + 128 * NT * HALVES;         // warp 0 TMA, 1 MMA, 2 items, 3 TMEM; softmax
-    static constexpr int TILE = 2 * NC * CHUNK, RING = 128 * 1024 / TILE;
-    static constexpr int STAGE = 2048;                              // of a softmax warp: 32 rows x 32 columns
-    static constexpr int Q_BYTES = NT * NC * Q_CHUNK, STAGES = Q_BYTES + RING * TILE;
+    static constexpr int TN = NC <= 2 ? 128 : 64;          // keys of a tile
+    static constexpr int CHUNK = TN * 128, TILE = NC * CHUNK;
+    static constexpr int QS = NC <= 2 ? 2 : 1;             // units whose queries are there
+    static constexpr int KS = NC == 1 ? 4 : 2, VS = NC == 1 ? 4 : 3;  // tiles of the keys' and the values' ring
+    static constexpr int Q_BYTES = NC * Q_CHUNK;
     static constexpr int EXTRA = static_cast<int>(sizeof(Shared<TN>));
-    static constexpr int SMEM = STAGES + (THREADS - 128) / 32 * STAGE + EXTRA;
+    static constexpr int SMEM = QS * Q_BYTES + (KS + VS) * TILE + EXTRA;
     static_assert(SMEM <= 232448, "227 KB a CTA");
     static_assert(SMEM > 116 * 1024, "two CTAs, which take all tensor memory, may not share an SM");
 };
 
 template <typename T, int NC>
-__global__ void __launch_bounds__(Sizes<NC>::THREADS, 1)
+__global__ void __launch_bounds__(THREADS, 1)
 k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
     extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's period
     using Z = Sizes<NC>;
-    constexpr int NT = Z::NT, HALVES = Z::HALVES, TN = Z::TN, C = TN / HALVES, SB = Z::SB, CHUNK = Z::CHUNK, RING = Z::RING;
+    constexpr int TN = Z::TN, C = TN / 2, CHUNK = Z::CHUNK, TILE = Z::TILE, KS = Z::KS, VS = Z::VS, QS = Z::QS;
     using Item = hch::Item<TN>;
-    const uint32_t q_s = smem_addr(smem), ring = q_s + Z::Q_BYTES;
+    const uint32_t q_s = smem_addr(smem), k_s = q_s + QS * Z::Q_BYTES, v_s = k_s + KS * TILE;
     Shared<TN> &sh = *reinterpret_cast<Shared<TN> *>(smem + Z::SMEM - Z::EXTRA);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < RING; ++i) {
+        for (int i = 0; i < MAX_SLOTS; ++i) {
             mbar_init(&sh.k_full[i], 1);
-            mbar_init(&sh.v_full[i], 1);
             mbar_init(&sh.k_free[i], 1);
+            mbar_init(&sh.v_full[i], 1);
             mbar_init(&sh.v_free[i], 1);
         }
-        for (int t = 0; t < NT; ++t) {
-            mbar_init(&sh.q_full[t], 1);
-            mbar_init(&sh.q_free[t], 1);
-            for (int b = 0; b < SB; ++b) {
-                mbar_init(&sh.s_full[t][b], 1);
-                mbar_init(&sh.p_ready[t][b], 4 * HALVES);
-                mbar_init(&sh.pv_done[t][b], 1);
-            }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.q_full[i], 1);
+            mbar_init(&sh.q_free[i], 1);
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.p_ready[i], 8);
+            mbar_init(&sh.pv_done[i], 1);
         }
         for (int i = 0; i < ITEMS; ++i) {
             mbar_init(&sh.item_full[i], 1);
-            mbar_init(&sh.item_free[i], 2 + 4 * NT * HALVES);  // the producer, the issuer, the softmax warps
+            mbar_init(&sh.item_free[i], 13);  // the producers, the issuer, eight softmax warps
         }
         mbar_init(&sh.drained, 1);
         sh.abort = 0;
@@ -177,19 +172,25 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
     }
     // ---- where this CTA starts, and its first item
     Walk<TN> walk;
-    const Cut cut = find_start<TN, Z::THREADS>(p, sh.scan, 2, walk);
+    const Cut cut = find_start<TN, THREADS>(p, *reinterpret_cast<Scan *>(smem), 2, walk);  // (before any copy)
+    // the next item with tiles to meet; a unit that sees no key is done with at once
     const auto next = [&](Item &it) {
-        const bool more = walk.next(p, cut, it.u, it.i0, it.i1, it.n);
-        it.row = walk.row;
-        it.head = more ? walk.head : -1;
-        it.nt[0] = it.nt[1] = 0;
-        if (more) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-                it.nt[t] = max(0, min(it.i1, it.u.tiles(p, it.u.m0 + t * p.tile_rows, p.tile_rows)) - it.i0);
-            it.tail = it.u.tail() - it.i0;
+        it.head = -1;
+        while (walk.next(p, cut, it.u, it.i0, it.i1, it.n)) {
+            it.tiles = min(it.i1, it.u.tiles(p)) - it.i0;
+            if (it.tiles > 0) {
+                it.row = walk.row;
+                it.head = walk.head;
+                return;
+            }
+            const int rows = min(TM, it.u.nq * p.G - it.u.m0);
+            for (int r = 0; r < min(rows, p.tile_rows); ++r) {
+                const int m = it.u.m0 + r, tok = m / p.G, h = walk.head * p.G + m - tok * p.G;
+                uint16_t *dst = p.out + (it.u.q0 + tok) * p.out_tok + h * p.out_head;
+                for (int d = lane * 8; d < p.D; d += 256) *reinterpret_cast<uint4 *>(dst + d) = make_uint4(0, 0, 0, 0);
+                if (lane == 0 && p.lse) p.lse[static_cast<int64_t>(it.u.q0 + tok) * p.Hq + h] = -INFINITY;
+            }
         }
-        return more;
     };
     if (warp == 2) {
         Item it = {};
@@ -199,6 +200,7 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
             mbar_arrive(&sh.item_full[0]);
         }
     }
+    fence_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -208,55 +210,52 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
         return wait_far(sh, &sh.item_full[item % ITEMS], (item / ITEMS) & 1) && sh.item[item % ITEMS].head >= 0;
     };
 
-    if (warp >= 4) {
-        // ---- softmax: a thread a row, or two, with 64 of a tile's 128 keys each
-        const int t = (warp - 4) / (4 * HALVES), half = (warp - 4) / 4 % HALVES, r = (warp & 3) * 32 + lane;
+    if (warp >= 4 && warp < 12) {
+        // ---- softmax: two threads a row, half of a tile's keys each
+        const int half = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lane_bits = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t s_t = tmem + lane_bits + t * 128, o_t = tmem + lane_bits + O_COL + t * 128;
-        const int my_tok = r / p.G, last_tok = p.tile_rows / p.G - 1;  // within the tile
-        const int pair_bar = 1 + t * 4 + (warp & 3);
+        const uint32_t o_t = tmem + lane_bits + O_COL;
+        const int my_tok = r / p.G, last_tok = p.tile_rows / p.G - 1;  // within the unit
+        const int pair_bar = 1 + (warp & 3);
+        int turn = 0;
         // the row's value from those of its threads
         const auto meet = [&](float v, auto join) {
-            if constexpr (HALVES == 2) {
-                sh.other[t][half][r] = v;
-                asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
-                v = join(v, sh.other[t][half ^ 1][r]);
-            }
+            sh.other[turn][half][r] = v;
+            asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+            v = join(v, sh.other[turn][half ^ 1][r]);
+            turn ^= 1;
             return v;
         };
-        const auto go_on = [&](uint32_t item) {
-            const bool yes = there_is(item);
-            return HALVES == 2 ? both(yes, pair_bar) : yes;
-        };
-        for (uint32_t item = 0; go_on(item); ++item) {
+        uint32_t g = 0;  // the tile's number
+        for (uint32_t item = 0; both(there_is(item), pair_bar); ++item) {
             // (what only the item's end needs stays in shared memory meanwhile)
             const volatile Item &my = sh.item[item % ITEMS];
-            const int nt = my.nt[t], len = my.u.len, ns = my.u.ns, skip = my.u.w0 - ns, i0 = my.i0;
-            const int tail = my.tail;  // the tile whose values are to be cleared
-            const int tok = (my.u.m0 + t * p.tile_rows) / p.G + my_tok;
+            const int tiles = my.tiles, len = my.u.len, ns = my.u.ns, skip = my.u.w0 - ns, i0 = my.i0;
+            // the tile that the row's keys end in, if that is not a whole one
+            const int tail = (len % TN != 0 ? ns + len / TN - my.u.w0 : -1) - i0;
+            const int tok = my.u.m0 / p.G + my_tok;
             const int limit = len - my.u.nq + tok + 1;  // one past the last key that this row sees,
-            const int sure = limit - my_tok;            // and the least of the tile's rows
+            const int sure = limit - my_tok;            // and the least of the unit's rows
             const int width = p.window > 0 && p.window < len ? p.window : 0;
-            uint32_t met = my.met[t];  // the row tile's key tiles so far
             float m_ref = -INFINITY, l = 0.0f;
-            for (int j = 0; j < nt; ++j, ++met) {
-                const uint32_t buffer = met % SB, phase = (met / SB) & 1, s_b = s_t + buffer * TN;
-                wait_long(sh, &sh.s_full[t][buffer], phase);
+            for (int j = 0; j < tiles; ++j, ++g) {
+                const uint32_t b = g & 1, s_b = tmem + lane_bits + b * TN;
+                wait_long(sh, &sh.s_full[b], (g >> 1) & 1);
                 tc_fence_after();
                 uint32_t x[C / 32][32];
 #pragma unroll
                 for (int c = 0; c < C / 32; ++c) tmem_ld32(s_b + half * C + 32 * c, x[c]);
                 if (__builtin_expect(j == tail, 0)) {
                     // value rows behind the row's last key: whatever lies there must not meet the
-                    // zero weights.  (Either row tile clears them, before its own products.)
-                    const uint32_t g = my.g0 + tail, slot = g % RING;
-                    wait(sh, &sh.v_full[slot], (g / RING) & 1);
+                    // zero weights
                     const int z0 = len % TN;
+                    const uint32_t slot = g % VS;
+                    wait(sh, &sh.v_full[slot], (g / VS) & 1);
 #pragma unroll 1
                     for (int c = 0; c < NC; ++c) {
-                        const uint32_t v = ring + slot * Z::TILE + (NC + c) * CHUNK + z0 * 128;
+                        const uint32_t v = v_s + slot * TILE + c * CHUNK + z0 * 128;
 #pragma unroll 1
-                        for (int i = half * 128 + r; i < (TN - z0) * 8; i += 128 * HALVES)
+                        for (int i = half * 128 + r; i < (TN - z0) * 8; i += 256)
                             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + i * 16), "r"(0)
                                          : "memory");
                     }
@@ -279,22 +278,20 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
                 }
                 float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int i = 0; i < C / 2; ++i)
-                    top4[i & 3] = max3(top4[i & 3], __uint_as_float(x[i / 32][i % 32]),
-                                       __uint_as_float(x[C / 64 + i / 32][i % 32]));
-                // (the second barrier of a tile is p_ready: nobody writes the next value before the
-                // products have taken both threads' weights)
+                for (int i = 0; i < C; i += 2)
+                    top4[(i >> 1) & 3] = max3(top4[(i >> 1) & 3], __uint_as_float(x[i / 32][i % 32]),
+                                              __uint_as_float(x[i / 32][i % 32 + 1]));
                 const float top = meet(fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]),
                                        [](float a, float b) { return fmaxf(a, b); }) * p.scale2;
                 const bool raise = top > m_ref + (LAZY + T::first_weight);
                 const float m_new = top - T::first_weight;
                 if (__builtin_expect(j > 0 && __any_sync(0xFFFFFFFFu, raise), 0)) {
-                    wait(sh, &sh.pv_done[t][(met - 1) % SB], ((met - 1) / SB) & 1);  // the output is free
+                    wait(sh, &sh.pv_done[b ^ 1], ((g - 1) >> 1) & 1);  // the output is free
                     tc_fence_after();
                     const float f = raise ? ex2(m_ref - m_new) : 1.0f;
                     l *= f;
 #pragma unroll 1
-                    for (int c = half * (NC * 64 / HALVES); c < (half + 1) * (NC * 64 / HALVES); c += 16) {
+                    for (int c = half * (NC * 32); c < (half + 1) * (NC * 32); c += 16) {
                         uint32_t o[16];
                         tmem_ld16(o_t + c, o);
                         tmem_wait_ld();
@@ -320,22 +317,20 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
                         part[i & 1] = add2(part[i & 1], pack2(e0, e1));
                         w[i] = T::narrow2(e0, e1);
                     }
+                    // (both threads of the row have read their scores: they have met since)
                     tmem_st16(s_b + half * (C / 2) + 16 * c, w);
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                // (an arrival a warp: 128 of them took the barriers' unit longer than the weights)
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_ready[t][buffer]);
+                if (lane == 0) mbar_arrive(&sh.p_ready[b]);
                 float l0, l1;
                 unpack2(add2(part[0], part[1]), l0, l1);
                 l += l0 + l1;
             }
-            if (nt > 0) {
-                wait_long(sh, &sh.pv_done[t][(met - 1) % SB], ((met - 1) / SB) & 1);
-                tc_fence_after();
-            }
             l = meet(l, [](float a, float b) { return a + b; });
+            wait_long(sh, &sh.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
+            tc_fence_after();
             // (a sum of zero: nothing was seen; one that is NaN stays so)
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             const float lse2 = l == 0.0f ? -INFINITY : m_ref + log2f(l);
@@ -346,57 +341,45 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
             const int slot_out = 2 * blockIdx.x + (i0 > 0 ? 0 : 1);
             if (real && half == 0) {
                 if (!whole)
-                    p.part_lse[static_cast<int64_t>(slot_out) * (NT * TM) + t * TM + r] = lse2;
+                    p.part_lse[static_cast<int64_t>(slot_out) * TM + r] = lse2;
                 else if (p.lse)
                     p.lse[out_row * p.Hq + h] = lse2 * LN2;
             }
-            // A warp's 32 rows x 32 columns go through shared memory, so that four lanes write 64
-            // bytes of a row.
-            const uint32_t stage = q_s + Z::STAGES + (warp - 4) * Z::STAGE;
-            const int64_t mine = reinterpret_cast<int64_t>(p.out + out_row * p.out_tok + h * p.out_head);
+            uint16_t *dst = p.out + out_row * p.out_tok + h * p.out_head;
+            // 32 bytes a store, a whole sector, where the rows allow it
+            const bool sectors = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
 #pragma unroll 1
-            for (int col = half * (NC * 64 / HALVES); col < (half + 1) * (NC * 64 / HALVES); col += 32) {
+            for (int col = half * (NC * 32); col < (half + 1) * (NC * 32); col += 32) {
                 uint32_t o[32];
+                __syncwarp();
                 tmem_ld32(o_t + col, o);
                 tmem_wait_ld();
-                // (where no key was met, the columns hold anything)
+                if (!real) continue;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = nt > 0 ? __float_as_uint(__uint_as_float(o[i]) * inv) : 0u;
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
                 if (!whole) {
-                    if (real)
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *part_at<NC, TM, NT>(p, slot_out, t, col + i, r) =
-                                make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]),
-                                            __uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
+                    for (int i = 0; i < 32; i += 4)
+                        *part_at<NC, TM, 1>(p, slot_out, 0, col + i, r) =
+                            make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]),
+                                        __uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
                     continue;
                 }
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    uint32_t y[4];
+                for (int v = 0; v < 2; ++v) {
+                    if (col + v * 16 >= p.D) break;
+                    uint32_t y[8];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        y[u] = T::narrow2(__uint_as_float(o[8 * v + 2 * u]), __uint_as_float(o[8 * v + 2 * u + 1]));
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                     stage + lane * 64 + ((v ^ ((lane >> 1) & 3)) << 4)),
-                                 "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
-                                 : "memory");
+                    for (int u = 0; u < 8; ++u)
+                        y[u] = T::narrow2(__uint_as_float(o[16 * v + 2 * u]), __uint_as_float(o[16 * v + 2 * u + 1]));
+                    uint16_t *d = dst + col + v * 16;
+                    if (sectors) {
+                        st_global_32B(d, y);
+                    } else {
+                        *reinterpret_cast<uint4 *>(d) = make_uint4(y[0], y[1], y[2], y[3]);
+                        *reinterpret_cast<uint4 *>(d + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+                    }
                 }
-                __syncwarp();
-                const bool in = col + (lane & 3) * 8 < p.D;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int row = k * 8 + lane / 4;
-                    uint4 y;
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
-                                 : "r"(stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4))
-                                 : "memory");
-                    const int64_t to = __shfl_sync(0xFFFFFFFFu, mine, row) + (col + (lane & 3) * 8) * 2;
-                    if (__shfl_sync(0xFFFFFFFFu, static_cast<int>(real), row) && in)
-                        *reinterpret_cast<uint4 *>(to) = y;
-                }
-                __syncwarp();
             }
             // The next item's products overwrite this output once its first weights are there,
             // which come after these reads.
@@ -404,127 +387,117 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
             __syncwarp();  // the whole warp is done with the item
             if (lane == 0) mbar_arrive(&sh.item_free[item % ITEMS]);
         }
-    } else if (warp == 0) {
-        // ---- producer: a box of a tile a lane.  Tiles are numbered through all items of the CTA,
-        // and tile j takes slot j mod RING.
-        const int boxes = TN / p.box_rows;
-        const uint32_t q_bytes = NC * p.tile_rows * 128;
-        uint32_t j = 0, q_uses[2] = {0, 0};
+    } else if (warp == 0 || warp == 3 || warp >= 12) {
+        // ---- producers: two of the keys and two of the values, half of a tile's boxes each (a copy takes
+        // a thread some 75 cycles, and a tile of 128 keys in pages of 16 is 16 of them for its keys
+        // alone).  A lane finds a box, and one thread issues.
+        const int what = warp == 3 || warp == 13, part = warp >= 12;  // values or keys; which boxes
+        const int boxes = TN / p.box_rows, mine = part ? boxes / 2 : (boxes + 1) / 2, first = part ? (boxes + 1) / 2 : 0;
         const auto all = [](bool yes) { return __all_sync(0xFFFFFFFFu, yes) != 0; };
-        const auto wait_all = [&](uint64_t *bar, uint32_t parity) {  // one lane asks
-            return all(lane != 0 || wait(sh, bar, parity));
-        };
+        const uint32_t N = what ? VS : KS, ring = what ? v_s : k_s;
+        const CUtensorMap *map = what ? &maps.v : &maps.k;
+        uint64_t *full = what ? sh.v_full : sh.k_full, *free = what ? sh.v_free : sh.k_free;
+        int2 *at = sh.box[what * 2 + part];
+        uint32_t slot = 0, phase = 1, fills = 0, q_uses = 0;
         bool ok = true;
         for (uint32_t item = 0; ok && all(there_is(item)); ++item) {
-            const Item my = sh.item[item % ITEMS];
-            const int n = my.tiles();
-            // the page of this lane's box of the item's tile i
+            const Item &my = sh.item[item % ITEMS];
             const int32_t *table = p.block_table + static_cast<int64_t>(my.row) * p.max_pages;
-            Box box = {};
+            const int tiles = my.tiles, i0 = my.i0, head = my.head, len = my.u.len, ns = my.u.ns, skip = my.u.w0 - ns;
+            const int q_tok = my.u.q0 + my.u.m0 / p.G;
+            Box box = {};  // of the next tile
             const auto look = [&](int i) {
-                box.look(p, table, my.u.key_tile(my.i0 + i) * TN + lane * p.box_rows, my.u.len, lane < boxes);
+                const int key = (i0 + i < ns ? i0 + i : i0 + i + skip) * TN;
+                box.look(p, table, key + (first + lane) * p.box_rows, len, lane < mine);
             };
-            // a tile's keys or values into their slot, once that is free
-            const auto bring = [&](const CUtensorMap *map, uint64_t *full, uint64_t *free, int chunk, int2 at) {
-                if (j >= RING && !wait_all(free, (j / RING - 1) & 1)) return false;
-                if (lane == 0) mbar_expect_tx(full, NC * CHUNK);
+            look(0);
+            for (int i = 0; ok && i < tiles; ++i) {
+                if (lane < mine) at[lane] = box.settle(p);
+                if (i + 1 < tiles) look(i + 1);
                 __syncwarp();
-                const uint32_t dst = ring + j % RING * Z::TILE + chunk * CHUNK + lane * p.box_rows * 128;
-                if (lane < boxes)
+                if (elect_one()) {
+                    ok = wait(sh, &free[slot], phase);
+                    if (ok) {
+                        if (part == 0) mbar_expect_tx(&full[slot], TILE);
+                        const uint32_t dst = ring + slot * TILE + first * p.box_rows * 128;
+#pragma unroll 4
+                        for (int x = 0; x < mine; ++x) {
+                            const int2 to = at[x];
 #pragma unroll
-                    for (int c = 0; c < NC; ++c)
-                        tma_load_4d(dst + c * CHUNK, map, c * 64, at.y, my.head, at.x, full);
-                __syncwarp();
-                return true;
-            };
-            if (n > 0) look(0);
-            for (int i = 0; ok && i < n; ++i, ++j) {
-                const int2 to = box.settle(p);
-                if (i + 1 < n) look(i + 1);
-                const uint32_t slot = j % RING;
-                ok = bring(&maps.k, &sh.k_full[slot], &sh.k_free[slot], 0, to);
-                if (ok && i == 0) {  // the queries, behind the first keys, which wait for less
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-                        if (my.nt[t] > 0) {
-                            ok = ok && (q_uses[t] == 0 || wait_all(&sh.q_free[t], (q_uses[t] - 1) & 1));
-                            if (!ok) break;
-                            ++q_uses[t];
-                            if (lane == 0) {
-                                mbar_expect_tx(&sh.q_full[t], q_bytes);
-                                for (int c = 0; c < NC; ++c)
-                                    tma_load_4d(q_s + (t * NC + c) * Q_CHUNK, &maps.q, c * 64, 0,
-                                                my.u.q0 + (my.u.m0 + t * p.tile_rows) / p.G, my.head, &sh.q_full[t]);
-                            }
-                            __syncwarp();
+                            for (int c = 0; c < NC; ++c)
+                                tma_load_4d(dst + c * CHUNK + x * p.box_rows * 128, map, c * 64, to.y, head, to.x, &full[slot]);
                         }
+                    }
+                    if (ok && i == 0 && what == 0 && part == 0) {  // the queries, behind the first keys, which wait for less
+                        const uint32_t s = item % QS;
+                        ok = wait_long(sh, &sh.q_free[s], (item / QS + 1) & 1);
+                        if (ok) {
+                            mbar_expect_tx(&sh.q_full[s], NC * p.tile_rows * 128);
+                            for (int c = 0; c < NC; ++c)
+                                tma_load_4d(q_s + s * Z::Q_BYTES + c * Q_CHUNK, &maps.q, c * 64, 0, q_tok, head,
+                                            &sh.q_full[s]);
+                        }
+                    }
                 }
-                ok = ok && bring(&maps.v, &sh.v_full[slot], &sh.v_free[slot], NC, to);
+                __syncwarp();
+                ok = all(ok);
+                ++fills;
+                if (++slot == N) {
+                    slot = 0;
+                    phase ^= 1;
+                }
             }
+            ++q_uses;
             __syncwarp();  // (all lanes have read the item)
             if (lane == 0) mbar_arrive(&sh.item_free[item % ITEMS]);
         }
         if (__any_sync(0xFFFFFFFFu, sh.abort)) {
-            // let the copies in flight land: the last fills of every slot, and the queries' (a fill
-            // that was cut off never completes: its wait runs to the limit)
-            for (uint32_t i = j > RING ? j - RING : 0; i < j; ++i) {
-                wait_out(&sh.k_full[i % RING], (i / RING) & 1);
-                wait_out(&sh.v_full[i % RING], (i / RING) & 1);
-            }
-            for (int t = 0; t < NT; ++t)
-                if (q_uses[t] > 0) wait_out(&sh.q_full[t], (q_uses[t] - 1) & 1);
+            // let the copies in flight land: the last fill of every slot, and the queries' (a fill that
+            // was cut off never completes: its wait runs to the limit)
+            for (uint32_t s = 0; s < N; ++s)
+                if (fills > s) wait_out(&full[s], ((fills + N - 1 - s) / N - 1) & 1);
+            for (uint32_t s = 0; s < QS; ++s)
+                if (what == 0 && part == 0 && q_uses > s) wait_out(&sh.q_full[s], ((q_uses + QS - 1 - s) / QS - 1) & 1);
         }
     } else if (warp == 1) {
         if (elect_one()) {
-            // ---- MMA issuer: a tile's products, then the next scores of the same rows, in turn
-            constexpr uint32_t id_s = idesc_of<T>(TN, false), id_o = idesc_of<T>(NC * 64, true);
-            const uint64_t qd = smem_desc_sw128(q_s), kd = smem_desc_sw128(ring);
-            const uint64_t vd = smem_desc_rows_k(ring, CHUNK) + NC * (CHUNK >> 4);
-            // the numbers of the next key tile, and of the next one that a row tile meets, for the
-            // products and for the scores
-            uint32_t gv = 0, gk = 0, mv[2] = {0, 0}, mk[2] = {0, 0}, q_uses[2] = {0, 0};
+            // ---- MMA issuer: a tile's products, then the scores of the tile two on. 
+            constexpr uint32_t id_s = idesc_of<T>(TN, false), id_o = idesc_of<T>(64 * NC, true);
+            const uint64_t qd = smem_desc_sw128(q_s), kd = smem_desc_sw128(k_s), vd = smem_desc_rows_k(v_s, CHUNK);
+            uint32_t gk = 0, gv = 0;  // the numbers of the next tiles
             for (uint32_t item = 0; there_is(item); ++item) {
-                const int nt[2] = {sh.item[item % ITEMS].nt[0], sh.item[item % ITEMS].nt[1]}, n = max(nt[0], nt[1]);
-                for (int j = -SB; j < n && !sh.abort; ++j) {
-                    const uint32_t vs = gv % RING, ks = gk % RING;
-                    if (j >= 0 && !wait(sh, &sh.v_full[vs], (gv / RING) & 1)) break;
-                    bool keys = false;  // tile j + SB's have been waited for
+                const int tiles = sh.item[item % ITEMS].tiles;
+                const uint32_t q = item % QS;
+                if (!wait(sh, &sh.q_full[q], (item / QS) & 1)) break;
+                for (int j = -AHEAD; j < tiles && !sh.abort; ++j) {
+                    if (j >= 0) {
+                        const uint32_t b = gv & 1, slot = gv % VS;
+                        if (!wait(sh, &sh.v_full[slot], (gv / VS) & 1)) break;
+                        if (!wait(sh, &sh.p_ready[b], (gv >> 1) & 1)) break;
+                        tc_fence_after();
+                        const uint64_t b_d = vd + slot * (TILE >> 4);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        if (j >= 0 && j < nt[t]) {
-                            if (!wait(sh, &sh.p_ready[t][mv[t] % SB], (mv[t] / SB) & 1)) break;
-                            tc_fence_after();
-                            const uint32_t a_d = tmem + t * 128 + mv[t] % SB * TN, d = tmem + O_COL + t * 128;
-                            const uint64_t b_d = vd + vs * (Z::TILE >> 4);
-#pragma unroll
-                            for (int u = 0; u < TN / 16; ++u)
-                                mma_ts(d, a_d + 8 * u, b_d + u * (2048 >> 4), id_o, (j | u) != 0);
-                            mma_commit(&sh.pv_done[t][mv[t] % SB]);
-                            ++mv[t];
-                        }
-                        if (t == NT - 1 && j >= 0) mma_commit(&sh.v_free[vs]);
-                        if (j + SB < nt[t]) {
-                            if (!keys && !wait(sh, &sh.k_full[ks], (gk / RING) & 1)) break;
-                            keys = true;
-                            if (j == -SB && !wait(sh, &sh.q_full[t], q_uses[t]++ & 1)) break;
-                            const uint32_t d = tmem + t * 128 + mk[t] % SB * TN;
-                            const uint64_t a_d = qd + t * (NC * (Q_CHUNK >> 4)), b_d = kd + ks * (Z::TILE >> 4);
-#pragma unroll
-                            for (int c = 0; c < NC; ++c)
-#pragma unroll
-                                for (int u = 0; u < 4; ++u)
-                                    mma_bf16(d, a_d + c * (Q_CHUNK >> 4) + 2 * u, b_d + c * (CHUNK >> 4) + 2 * u, id_s,
-                                             (c | u) != 0);
-                            mma_commit(&sh.s_full[t][mk[t] % SB]);
-                            if (j + SB + 1 == nt[t]) mma_commit(&sh.q_free[t]);
-                            ++mk[t];
-                        }
+                        for (int u = 0; u < TN / 16; ++u)
+                            mma_ts(tmem + O_COL, tmem + b * TN + 8 * u, b_d + u * (2048 >> 4), id_o, (j | u) != 0);
+                        mma_commit(&sh.pv_done[b]);
+                        mma_commit(&sh.v_free[slot]);
+                        ++gv;
                     }
-                    if (keys) {
-                        mma_commit(&sh.k_free[ks]);
+                    if (j + AHEAD < tiles) {
+                        const uint32_t b = gk & 1, slot = gk % KS;
+                        if (!wait(sh, &sh.k_full[slot], (gk / KS) & 1)) break;
+                        const uint64_t a_d = qd + q * (Z::Q_BYTES >> 4), b_d = kd + slot * (TILE >> 4);
+#pragma unroll
+                        for (int c = 0; c < NC; ++c)
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                mma_bf16(tmem + b * TN, a_d + c * (Q_CHUNK >> 4) + 2 * u, b_d + c * (CHUNK >> 4) + 2 * u, id_s,
+                                         (c | u) != 0);
+                        mma_commit(&sh.s_full[b]);
+                        mma_commit(&sh.k_free[slot]);
+                        if (j + AHEAD + 1 == tiles) mma_commit(&sh.q_free[q]);
                         ++gk;
                     }
-                    gv += j >= 0;
                 }
                 mbar_arrive(&sh.item_free[item % ITEMS]);
                 if (sh.abort) break;
@@ -536,9 +509,7 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
         // ---- the items after the first, each as soon as its place is left behind
         Item it = sh.item[0];
         for (uint32_t item = 1; it.head >= 0; ++item) {
-            it.g0 += it.tiles();
-#pragma unroll
-            for (int t = 0; t < 2; ++t) it.met[t] += it.nt[t];
+            it.g0 += it.tiles;
             next(it);
             if (!__all_sync(0xFFFFFFFFu, item < ITEMS || wait_far(sh, &sh.item_free[item % ITEMS],
                                                                   (item / ITEMS - 1) & 1)))
@@ -570,7 +541,7 @@ struct Layout {
 };
 Layout layout(int NC) {
     const auto align256 = [](size_t n) { return (n + 255) & ~static_cast<size_t>(255); };
-    const size_t rows = static_cast<size_t>(2 * SMS) * TM * (NC <= 2 ? 2 : 1);
+    const size_t rows = static_cast<size_t>(2 * SMS) * TM;
     Layout y;
     y.plan = 0;
     y.part = align256(SMS * sizeof(Plan));
@@ -586,13 +557,13 @@ cudaError_t launch(const HeadsAttnArgs &a, cudaStream_t stream) {
     const int G = a.Hq / a.Hkv;
     Params p;
     Maps maps;
-    if (!set_up(a, TM / G * G, Z::NT, Z::TN, true, y.plan, y.part, y.lse, p, maps)) return cudaErrorInvalidValue;
+    if (!set_up(a, TM / G * G, 1, Z::TN, true, y.plan, y.part, y.lse, p, maps)) return cudaErrorInvalidValue;
     static AttrCache attr;
     cudaError_t e = ensure_attr(k_heads_chunk<T, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::SMEM, attr);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(SMS);
-    cfg.blockDim = dim3(Z::THREADS);
+    cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = Z::SMEM;
     cfg.stream = stream;
     cfg.attrs = pdl_attr();  // set up beside the end of whatever the stream runs before
@@ -600,10 +571,10 @@ cudaError_t launch(const HeadsAttnArgs &a, cudaStream_t stream) {
     e = cudaLaunchKernelEx(&cfg, k_heads_chunk<T, NC>, maps, p);
     if (e != cudaSuccess) return e;
     count_launches(1);
-    cfg.gridDim = dim3(Z::NT * TM / 32, SMS);
+    cfg.gridDim = dim3(TM / 32, SMS);
     cfg.blockDim = dim3(JOIN_THREADS);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, k_heads_join<T, NC, TM, Z::NT, false>, p);
+    e = cudaLaunchKernelEx(&cfg, k_heads_join<T, NC, TM, 1, false>, p);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
