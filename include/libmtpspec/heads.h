@@ -96,8 +96,9 @@ int mtp_heads_append(const void *k, int64_t k_tok_stride, int64_t k_head_stride,
  *            (taken as the nearest in range), a bound out of range or out of order (taken as the
  *            nearest good one: in range, and not below the bounds before it) or a page id out of
  *            range (its positions are read as zeros); MTPSPEC_STATUS_TIMEOUT if a wait gave up.
- * 1 <= B <= 65536, 0 <= Tq <= 2^24, Tq * Hq <= 2^30, scale finite and above 0.  The results do
- * not depend on timing.
+ * 1 <= B <= 65536, 0 <= Tq <= 2^24, Tq * Hq <= 2^30, scale finite and above 0.  Two launches; the
+ * results do not depend on timing.  They may differ in their last bits with the batch that a row is
+ * in, since the work is cut among multiprocessors by the lengths of all rows.
  */
 int mtp_heads_attn(const void *q, int64_t q_tok_stride, int64_t q_head_stride, const void *k_cache,
                    const void *v_cache, int64_t num_pages, int32_t page_size, int64_t page_stride,

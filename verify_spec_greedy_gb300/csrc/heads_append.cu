@@ -7,6 +7,12 @@
 // shuffles; the rotation's partner is in the same lane (neighbouring pairs) or R / 16 lanes on
 // (pairs of the two halves: eight shuffles).  All heads of a token, queries, keys and values, are
 // one list that warps take in runs, so the angles and the weights are loaded once a run.
+//
+// What bounds it (in a graph): 11,994 tokens, 16 / 4 heads of 256 of which 64 elements are turned, 298 MB:
+// 73 us, 4.1 TB/s, 0.60 of the copy rate.  The issue slots are 76 % taken, by conversions, sums and
+// addresses; loads ahead through registers or shared memory made it slower (84 and 104 us), runs of
+// eight groups the same, of two 91 us.  1024 tokens, 32 / 8 heads of 128: 10.8 us.  One token: 2.7 us, the
+// launch.
 #include "common.cuh"
 #include "half_types.cuh"
 #include "kernels.h"

@@ -9,23 +9,35 @@
 // are subnormal: half_types.cuh.)
 //
 // Rows: the G = Hq / Hkv query heads of a key head meet the same keys, so a unit's 128 rows are
-// 128 / G tokens times G heads.  Two threads a row in the softmax.
+// 128 / G tokens times G heads, two threads a row in the softmax.  (Four threads a row: 313 -> 349 us
+// in the second case below.)
 //
-// Keys: tiles of 128.  Tensor memory holds the output and two score buffers, whose first halves
-// become the weights (the left operand of the second product): the tensor cores compute the
-// scores two tiles ahead, across units as well, so that a softmax waits for nothing but the softmax
-// before.  (With two row tiles of one buffer each a round took what the chain scores - softmax -
-// products of a row tile takes, 4,200 cycles for 2,300 of products; keys and values are now read
-// twice as often, from L2.)  They stream through two rings of chunks (128 keys x 64 columns),
-// released one by one.
+// Keys: tiles of 128, or of 64 for heads of more than 128 elements.  Tensor memory holds the output
+// and two score buffers, whose first halves become the weights (the left operand of the second
+// product): the tensor cores compute the scores two tiles ahead, so that a softmax waits for little
+// but the softmax before.  (Two row tiles of one buffer each beside two outputs: 340 us in that case; a
+// round took what the chain scores - softmax - products of a row tile takes, 4,100 cycles for 2,300
+// of products.)  Keys and values have a ring of tiles each.
 //
-// A tile is brought in boxes that stay within a page, a box a lane of the producing warp.  With a
-// window, a unit meets the tiles of the first tokens, then those of the window.
+// A tile is brought in boxes that stay within a page; a copy takes the thread that issues it some 75
+// cycles, so there are four such threads.  With a window, a unit meets the tiles of the first tokens,
+// then those of the window.
 //
 // Work: all units laid end to end, a unit's length its key tiles and a constant for its start and
 // end, and cut evenly over 152 CTAs, one a multiprocessor, whatever the lengths; every CTA finds
 // its start from a scan of the rows.  A unit cut among CTAs leaves fp32 partial outputs, which a
 // second small kernel joins.
+//
+// What bounds it (HBM copy 6.8 TB/s, products 1885 TFLOP/s measured; in a graph):
+//   8 prompts of 77-1500 tokens, 32 / 4 heads of 128, pages of 16, bf16, 66 GFLOP: 95 us, 0.70 PFLOP/s.
+//     Units have six tiles on average, and their starts and ends, some 5,000 cycles each, are not
+//     covered by anything (tensor pipe 31 %).
+//   6 rows of 1-1000 tokens behind up to 7001 keys, 40 / 8 heads of 128, pages of 48, fp16, 365 GFLOP:
+//     300 us, 1.22 PFLOP/s, 0.64.  A tile takes some 1,800 cycles, the softmax of 128 x 128 scores by
+//     eight warps, for 1,150 of products (tensor pipe 55 %).
+//   8192 tokens, 16 / 2 heads of 256, pages of 128, bf16, 550 GFLOP: 465 us, 1.18 PFLOP/s, 0.63.  Scores
+//     of 64 columns take the tensor cores as long as 128 would (tensor pipe 50 %), and tiles of 128
+//     keys of such heads do not fit twice.
 #include <algorithm>
 
 #include "heads.cuh"
@@ -461,7 +473,7 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
         }
     } else if (warp == 1) {
         if (elect_one()) {
-            // ---- MMA issuer: a tile's products, then the scores of the tile two on. 
+            // ---- MMA issuer: a tile's products, then the scores of the tile two on
             constexpr uint32_t id_s = idesc_of<T>(TN, false), id_o = idesc_of<T>(64 * NC, true);
             const uint64_t qd = smem_desc_sw128(q_s), kd = smem_desc_sw128(k_s), vd = smem_desc_rows_k(v_s, CHUNK);
             uint32_t gk = 0, gv = 0;  // the numbers of the next tiles
