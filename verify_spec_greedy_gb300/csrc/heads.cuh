@@ -29,8 +29,7 @@ struct Params {
     int max_len;         // the table's positions, up to 2^31 - 256
     int num_pages, page_size, box_rows;
     int B, Tq, Hq, Hkv, G, D, window, sinks;
-    int tile_rows;       // (token, head) rows that a row tile holds
-    int unit_rows;       // and a unit, of one or two tiles
+    int unit_rows;       // (token, head) rows that a unit holds
     float scale2;        // scale * log2(e), above 0
     const uint16_t *q;
     int64_t q_tok, q_head;
@@ -331,11 +330,11 @@ struct Box {
 };
 
 // Partial outputs lie by fours of columns, the rows side by side (a thread that has a row's columns
-// writes beside its neighbours): float4 number ((slot * TILES + tile) * 16 NC + column / 4) * TM + row.
-template <int NC, int TM, int TILES>
-__device__ __forceinline__ float4 *part_at(const Params &p, int slot, int tile, int column, int row) {
+// writes beside its neighbours): float4 number (slot * 16 NC + column / 4) * TM + row.
+template <int NC, int TM>
+__device__ __forceinline__ float4 *part_at(const Params &p, int slot, int column, int row) {
     return reinterpret_cast<float4 *>(p.part) +
-           (static_cast<int64_t>(slot * TILES + tile) * (16 * NC) + column / 4) * TM + row;
+           (static_cast<int64_t>(slot) * (16 * NC) + column / 4) * TM + row;
 }
 
 // Units cut among CTAs: each row's partial outputs, weighted by their sums, become the output.  A
@@ -344,23 +343,23 @@ __device__ __forceinline__ float4 *part_at(const Params &p, int slot, int tile, 
 // eighth of the parts each, and blockIdx.z the columns.
 constexpr int JOIN_THREADS = 256, JOIN_WARPS = JOIN_THREADS / 32;
 
-template <typename T, int NC, int TM, int TILES, bool SPREAD>
+template <typename T, int NC, int TM, bool SPREAD>
 __global__ void __launch_bounds__(JOIN_THREADS) k_heads_join(const Params p) {
     constexpr int COLS = 8 * NC, QUADS = 2 * NC;  // of a warp
     __shared__ float shared[SPREAD ? JOIN_WARPS : 1][SPREAD ? 32 : 1][COLS + 2];
     pdl_wait_primary();
     const Plan u = p.plan[blockIdx.y];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rr = blockIdx.x * 32 + lane, tile = rr / TM, r = rr % TM, in = tile * p.tile_rows + r;
+    const int r = blockIdx.x * 32 + lane;
     // (what an aborted call left there is checked)
     if (u.parts < 2 || u.parts > static_cast<int>(gridDim.y - blockIdx.y) || u.q0 < 0 || u.m0 < 0 ||
         u.q0 + (u.m0 + u.rows - 1) / p.G >= p.Tq || u.head < 0 || u.head >= p.Hkv ||
-        blockIdx.x * 32 / TM * p.tile_rows + blockIdx.x * 32 % TM >= u.rows)
+        static_cast<int>(blockIdx.x) * 32 >= u.rows)
         return;
     // a CTA's partial: the second slot where the unit starts, else the first
     const auto slot = [&](int i) { return static_cast<int>(2 * (blockIdx.y + i) + (i == 0)); };
-    const auto lse2 = [&](int i) { return p.part_lse[static_cast<int64_t>(slot(i)) * (TILES * TM) + rr]; };
-    const bool real = r < p.tile_rows && in < u.rows;
+    const auto lse2 = [&](int i) { return p.part_lse[static_cast<int64_t>(slot(i)) * TM + r]; };
+    const bool real = r < u.rows;
     const int col = (SPREAD ? blockIdx.z : warp) * COLS;
     float top = -INFINITY, sum = 0.0f;
     float acc[COLS] = {};
@@ -373,7 +372,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_heads_join(const Params p) {
             const float w = exp2f(lse2(i) - ref);
             float4 v[QUADS];
 #pragma unroll
-            for (int k = 0; k < QUADS; ++k) v[k] = *part_at<NC, TM, TILES>(p, slot(i), tile, col + 4 * k, r);
+            for (int k = 0; k < QUADS; ++k) v[k] = *part_at<NC, TM>(p, slot(i), col + 4 * k, r);
             sum += w;
 #pragma unroll
             for (int k = 0; k < QUADS; ++k) {
@@ -399,7 +398,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_heads_join(const Params p) {
     }
     if (!real) return;
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int m = u.m0 + in, tok = m / p.G, head = u.head * p.G + m - tok * p.G;
+    const int m = u.m0 + r, tok = m / p.G, head = u.head * p.G + m - tok * p.G;
     const int64_t out_row = u.q0 + tok;
     uint16_t *dst = p.out + out_row * p.out_tok + head * p.out_head + col;
 #pragma unroll
@@ -413,17 +412,34 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_heads_join(const Params p) {
     if (p.lse && col == 0) p.lse[out_row * p.Hq + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * LN2;
 }
 
-// The parameters and tensor maps of a call whose row tiles hold `tile_rows` rows and whose units
-// `tiles` of them; the workspace's parts lie at the given offsets.  The queries' map, if it is asked
-// for, brings a whole tile of them, as tile_rows / G tokens of G heads.
-inline bool set_up(const HeadsAttnArgs &a, int tile_rows, int tiles, int TN, bool q_map, size_t plan,
+// The joining kernel behind one that was launched with `cfg`.
+template <typename T, int NC, int TM>
+cudaError_t launch_join(cudaLaunchConfig_t cfg, const Params &p, cudaStream_t stream) {
+    const unsigned ctas = cfg.gridDim.x;
+    // very few units are cut into very many parts each (where they are eight in 19 parts, either way takes
+    // the same; five parts are slower when spread, by 1.5 us)
+    const int64_t units = static_cast<int64_t>(p.B) * p.Hkv + static_cast<int64_t>(p.Tq) * p.Hq / p.unit_rows;
+    const bool spread = units * 32 < static_cast<int64_t>(ctas);
+    cfg.gridDim = dim3(TM / 32, ctas, spread ? JOIN_WARPS : 1);
+    cfg.blockDim = dim3(JOIN_THREADS);
+    cfg.dynamicSmemBytes = 0;
+    cfg.stream = stream;
+    const cudaError_t e = spread ? cudaLaunchKernelEx(&cfg, k_heads_join<T, NC, TM, true>, p)
+                                 : cudaLaunchKernelEx(&cfg, k_heads_join<T, NC, TM, false>, p);
+    if (e == cudaSuccess) count_launches(1);
+    return e;
+}
+
+// The parameters and tensor maps of a call whose units hold `unit_rows` rows; the workspace's parts lie
+// at the given offsets.  The queries' map, if it is asked for, brings a unit's, as unit_rows / G tokens
+// of G heads.
+inline bool set_up(const HeadsAttnArgs &a, int unit_rows, int TN, bool q_map, size_t plan,
                    size_t part, size_t lse, Params &p, Maps &maps) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     p = {};
     p.G = a.Hq / a.Hkv;
-    p.tile_rows = tile_rows;
-    p.unit_rows = tiles * tile_rows;
+    p.unit_rows = unit_rows;
     // boxes of the largest power of two (up to a tile) that divides the page: a box never leaves
     // its page, and its rows start at a multiple of eight, the swizzle's period
     const int two = a.page_size & -a.page_size;
@@ -447,7 +463,7 @@ inline bool set_up(const HeadsAttnArgs &a, int tile_rows, int tiles, int TN, boo
     if (q_map) {
         const cuuint64_t qd[4] = {u(a.D), u(p.G), u(a.Tq), u(a.Hkv)},
                          qs[3] = {u(q_head * 2), u(q_tok * 2), u(q_head * p.G * 2)};
-        const cuuint32_t qb[4] = {64, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(tile_rows / p.G), 1};
+        const cuuint32_t qb[4] = {64, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(unit_rows / p.G), 1};
         if (!encode(&maps.q, a.q, qd, qs, qb)) return false;
     } else {
         maps.q = maps.k;

@@ -4,15 +4,15 @@
 namespace mtpspec {
 namespace {
 
-// How a call goes.  A row has Tq / B tokens on average and G = Hq / Hkv rows of work a token and
-// key head.  What fits 32 or 64 rows is bound by the cache's bytes, which heads_few.cu streams with
-// few threads a row; more rows are bound by products, for which heads_chunk.cu has pairs of
-// 128-row tiles.
-enum class Form { few32, few64, chunk };
-Form form_of(int64_t B, int64_t Tq, int32_t Hq, int32_t Hkv) {
-    const int64_t rows = Tq * (Hq / Hkv);
-    if (rows <= 32 * B) return Form::few32;
-    return rows <= 64 * B ? Form::few64 : Form::chunk;
+// How a call goes.  heads_chunk.cu takes any: its units of 128 rows keep up with the cache's bytes
+// even where a row of the batch has a token and a key head eight queries.  Where heads have at most 64
+// elements, a tile of keys is 32 KB, and the smaller units of heads_few.cu, two CTAs an SM, get from tile
+// to tile faster: up to 32 rows of work a row of the batch and key head (64 rows, a window of 1024,
+// pages of 16: 43 us, not 49; 2000-4000 keys 102, not 107; from two units a row on its bytes double).
+// Heads of 128 elements take the same time in both (256 rows x 4 tokens 378 and 378 us; 256 rows of
+// 50-1000 keys in pages of 16 106 here, 143 there), heads of 256 133 here and 202 there.
+bool few(int64_t B, int64_t Tq, int32_t Hq, int32_t Hkv, int32_t D) {
+    return D <= 64 && Tq * (Hq / Hkv) <= 32 * B;
 }
 
 }  // namespace
@@ -49,14 +49,11 @@ cudaError_t run_wait_selftest_heads(uint32_t limit, int32_t *status, cudaStream_
 }
 
 size_t heads_attn_workspace_bytes(int64_t B, int64_t Tq, int32_t Hq, int32_t Hkv, int32_t D) {
-    const Form f = form_of(B, Tq, Hq, Hkv);
-    return f == Form::chunk ? heads_chunk_workspace_bytes(D) : heads_few_workspace_bytes(D, f == Form::few32);
+    return few(B, Tq, Hq, Hkv, D) ? heads_few_workspace_bytes() : heads_chunk_workspace_bytes(D);
 }
 
 cudaError_t run_heads_attn(const HeadsAttnArgs &a, int dtype, cudaStream_t stream) {
-    const Form f = form_of(a.B, a.Tq, a.Hq, a.Hkv);
-    return f == Form::chunk ? run_heads_chunk(a, dtype, stream)
-                            : run_heads_few(a, f == Form::few32, dtype, stream);
+    return few(a.B, a.Tq, a.Hq, a.Hkv, a.D) ? run_heads_few(a, dtype, stream) : run_heads_chunk(a, dtype, stream);
 }
 
 }  // namespace mtpspec

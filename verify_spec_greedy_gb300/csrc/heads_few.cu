@@ -1,24 +1,20 @@
-// Attention with grouped heads over the paged cache, for rows of few tokens: draft steps and
-// verifications.  What bounds them is the cache's bytes.
+// Attention with grouped heads over the paged cache, for rows of few tokens and heads of up to 64
+// elements: draft steps and verifications.  What bounds them is the cache's bytes and, at 32 KB a tile
+// of keys and values, the way from one tile to the next.
 //
 // One pass over the keys with the running maximum m and sum l of a softmax, as in heads_chunk.cu.
-// A unit's rows, the (token, head) rows of a key head, are ROWS = 32 or 64, whose accumulators are
-// folded into all 128 lanes of tensor memory: NQ = 128 / ROWS threads share a row, so that with few
-// rows every thread of the four softmax warps has work, TN / NQ keys of a tile each.
+// A unit's rows, the (token, head) rows of a key head, are 32, whose accumulators are folded into all
+// 128 lanes of tensor memory: four threads share a row, so that with few rows every thread of the
+// four softmax warps has work, 32 keys of a tile each.
 //
-// Keys and values stream through a ring of chunks (TN tokens x 64 columns), released one by one.
+// Keys and values stream through a ring of chunks (128 tokens x 64 columns), released one by one.
 // The scores of a tile are computed ahead of the weights of the tile before, across units as well.
-// With 32 rows and heads of up to 128 elements two CTAs share an SM: while one is in a
-// softmax, the other's copies and products go on.
+// Two CTAs share an SM: while one is in a softmax, the other's copies and products go on.
 //
-// What bounds it (HBM copy 6.8 TB/s measured; in a graph):
-//   256 rows of 4 tokens over 500-4000 keys, 32 / 8 heads of 128, pages of 64, bf16, 2.39 GB: 378 us, 6.3
-//     TB/s, 0.93 of the copy rate (as pairs of 128-row tiles in the other kernel 421 us).
-//   64 rows of a token, 64 / 8 heads of 64, pages of 16, a window of 1024 and four first tokens, fp16,
-//     136 MB: 43 us, 3.1 TB/s.  512 units of ten tiles on 304 CTAs: starts, ends and joins of units cut
-//     once or twice each.  (Two producers, two buffers of weights: the same.)
-//   A token of one row over 600 keys, 32 / 8 heads of 128: 13 us, two launches and one tile's way from
-//     page table to output.
+// What bounds it (HBM copy 6.8 TB/s measured; in a graph): 64 rows of a token, 64 / 8 heads of 64, pages of
+// 16, a window of 1024 and four first tokens, fp16, 136 MB: 43 us, 3.1 TB/s (in the other kernel 49).
+// 512 units of ten tiles on 304 CTAs: starts, ends and joins of units cut once or twice each.  (Two
+// producers, two buffers of weights: the same.)
 #include <algorithm>
 
 #include "heads.cuh"
@@ -28,59 +24,50 @@ namespace hfw {
 
 using namespace heads;
 
+constexpr int ROWS = 32, TN = 128;  // rows of a unit, keys of a tile
+constexpr int NQ = 128 / ROWS;       // threads of a row
+constexpr int C = TN / NQ;           // keys of a tile that a thread has
+constexpr int W = 64 / NQ;           // and columns of the output
+constexpr int CHUNK = TN * 128;      // bytes of a tile's keys, or values
+constexpr int Q_BYTES = ROWS * 128;
+constexpr int P_BYTES = TN / 64 * ROWS * 128;
+constexpr int CTAS = 2;              // of an SM
+constexpr int S_COL = 0, O_COL = 2 * C;
+constexpr uint32_t TMEM_COLS = 128;
+static_assert(O_COL + W <= static_cast<int>(TMEM_COLS), "tensor memory");
 constexpr int NTHREADS = 224;  // warp 0 TMA, 1 MMA and TMEM, 2-5 softmax, 6 items and queries
 constexpr int SOFTMAX0 = 64;   // the first softmax thread
-constexpr int MAX_SLOTS = 16;
+constexpr int SLOTS = 5;             // chunks of the ring
 
 // Tiles i0 .. i1 - 1 of a unit's n (at least 1); g0: the CTA's tiles before it.  head -1: no more.
-template <int TN>
 struct Item {
     Unit<TN> u;
     int row, head, i0, i1, n, tiles;
     uint32_t g0;
 };
 
-template <int TN, int ROWS>
 struct __align__(16) Shared {
-    uint64_t full[MAX_SLOTS], empty[MAX_SLOTS];
+    uint64_t full[SLOTS], empty[SLOTS];
     uint64_t s_full[2], p_ready, pv_done, q_full[2], item_full[2], item_free[2], drained;
-    Item<TN> item[2];
+    Item item[2];
     Scan scan;
     int2 box[2][16];  // boxes of a tile, in turn
     uint32_t tmem;
     volatile int abort;
-    float other[2][128 / ROWS][ROWS];  // what the threads of a row tell each other
+    float other[2][NQ][ROWS];  // what the threads of a row tell each other
 };
 
-template <int NC, int ROWS>
-struct Sizes {
-    static constexpr int TN = NC <= 2 ? 128 : 64;   // keys of a tile
-    static constexpr int NQ = 128 / ROWS;           // threads of a row
-    static constexpr int C = TN / NQ;               // keys of a tile that a thread has
-    static constexpr int W = 64 / NQ;               // and columns of an output chunk
-    static constexpr int CHUNK = TN * 128;
-    static constexpr int Q_CHUNK = ROWS * 128, Q_BYTES = NC * Q_CHUNK;
-    static constexpr int P_BYTES = TN / 64 * ROWS * 128;
-    static constexpr int CTAS = ROWS == 32 && NC <= 2 ? 2 : 1;  // of an SM
-    static constexpr int EXTRA = static_cast<int>(sizeof(Shared<TN, ROWS>));
-    static constexpr int LEFT = (CTAS == 2 ? 113 : 227) * 1024 - EXTRA - 2 * Q_BYTES - P_BYTES;
-    static constexpr int SLOTS = LEFT / CHUNK < MAX_SLOTS ? LEFT / CHUNK : MAX_SLOTS;
-    static constexpr int NEED = 2 * Q_BYTES + P_BYTES + SLOTS * CHUNK + EXTRA;
-    // (a CTA alone on its SM takes more than half of the SM's)
-    static constexpr int SMEM = CTAS == 1 && NEED < 120 * 1024 ? 120 * 1024 : NEED;
-    static constexpr int S_COL = 0, O_COL = 2 * C;
-    static constexpr int COLS = O_COL + NC * W <= 128 ? 128 : 256;
-    static_assert(SLOTS > 2 * NC, "a tile's keys and values and the start of the next");
-    static_assert(O_COL + NC * W <= 256, "tensor memory");
-    // the slot n chunks on (at most SLOTS), and whether that is around the end
-    static __device__ __forceinline__ void step(int &s, uint32_t &ph, int n) {
-        s += n;
-        if (s >= SLOTS) {
-            s -= SLOTS;
-            ph ^= 1;
-        }
+constexpr int EXTRA = static_cast<int>(sizeof(Shared));
+constexpr int SMEM = 2 * Q_BYTES + P_BYTES + SLOTS * CHUNK + EXTRA;
+static_assert(SMEM <= 113 * 1024 && SMEM > 75 * 1024, "two CTAs an SM, and no more: they take a quarter of its tensor memory");
+// The slot n chunks on, and its phase.
+__device__ __forceinline__ void step(int &s, uint32_t &ph, int n) {
+    s += n;
+    if (s >= SLOTS) {
+        s -= SLOTS;
+        ph ^= 1;
     }
-};
+}
 
 // D[ROWS, n] (+)= A[ROWS, 16] B[16, n], the accumulator folded into 128 lanes: lanes q * ROWS ..
 // hold the columns q * n / NQ ..
@@ -109,29 +96,16 @@ __host__ __device__ constexpr uint32_t idesc_of(int m, int n, bool b_rows_k) {
            (static_cast<uint32_t>(b_rows_k) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
            (static_cast<uint32_t>(m >> 4) << 24);
 }
-// N columns of this thread's lane (no wait), and back.
-template <int N>
-__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t *x) {
-    if constexpr (N == 16) {
-        tmem_ld16(addr, *reinterpret_cast<uint32_t(*)[16]>(x));
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; i += 32) tmem_ld32(addr + i, *reinterpret_cast<uint32_t(*)[32]>(x + i));
-    }
-}
-
-template <typename T, int NC, int ROWS>
-__global__ void __launch_bounds__(NTHREADS, Sizes<NC, ROWS>::CTAS)
+template <typename T>
+__global__ void __launch_bounds__(NTHREADS, CTAS)
 k_heads_few(const __grid_constant__ Maps maps, const Params p) {
     extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's period
-    using Z = Sizes<NC, ROWS>;
-    constexpr int TN = Z::TN, NQ = Z::NQ, C = Z::C, W = Z::W, CHUNK = Z::CHUNK;
-    const uint32_t q_s = smem_addr(smem), p_s = q_s + 2 * Z::Q_BYTES, ring = p_s + Z::P_BYTES;
-    Shared<TN, ROWS> &sh = *reinterpret_cast<Shared<TN, ROWS> *>(smem + Z::SMEM - Z::EXTRA);
+    const uint32_t q_s = smem_addr(smem), p_s = q_s + 2 * Q_BYTES, ring = p_s + P_BYTES;
+    Shared &sh = *reinterpret_cast<Shared *>(smem + SMEM - EXTRA);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (warp == 0) {
-        if (lane < MAX_SLOTS) {
+        if (lane < SLOTS) {
             mbar_init(&sh.full[lane], 1);
             mbar_init(&sh.empty[lane], 1);
         } else if (lane == 16) {
@@ -157,13 +131,13 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_addr(&sh.tmem)),
-                     "r"(static_cast<uint32_t>(Z::COLS))
+                     "r"(TMEM_COLS)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     Walk<TN> walk;
     const Cut cut = find_start<TN, NTHREADS>(p, sh.scan, 6, walk);
-    const auto next = [&](Item<TN> &it) {
+    const auto next = [&](Item &it) {
         const bool more = walk.next(p, cut, it.u, it.i0, it.i1, it.n);
         it.row = walk.row;
         it.head = more ? walk.head : -1;
@@ -171,7 +145,7 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
         return more;
     };
     if (warp == 6) {
-        Item<TN> it = {};
+        Item it = {};
         next(it);
         if (lane == 0) sh.item[0] = it;
     }
@@ -195,7 +169,7 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
         uint32_t ph = 1;  // phase of the slot's release
         bool ok = true;
         for (uint32_t item = 0;; ++item) {
-            const Item<TN> my = sh.item[item & 1];
+            const Item my = sh.item[item & 1];
             const int32_t *table = p.block_table + static_cast<int64_t>(my.row) * p.max_pages;
             Box box = {};
             const auto look = [&](int i) {
@@ -211,7 +185,7 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
                     int slot = s;
                     uint32_t phase = ph;
 #pragma unroll
-                    for (int c = 0; c < 2 * NC; ++c) {
+                    for (int c = 0; c < 2; ++c) {  // the keys, then the values
                         ok = ok && wait(sh, &sh.empty[slot], phase);
                         if (!ok) break;
                         mbar_expect_tx(&sh.full[slot], CHUNK);
@@ -219,16 +193,16 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
 #pragma unroll 4
                         for (int k = 0; k < boxes; ++k) {
                             const int2 x = at[k];
-                            tma_load_4d(dst, c < NC ? &maps.k : &maps.v, c % NC * 64, x.y, my.head, x.x, &sh.full[slot]);
+                            tma_load_4d(dst, c == 0 ? &maps.k : &maps.v, 0, x.y, my.head, x.x, &sh.full[slot]);
                             dst += p.box_rows * 128;
                         }
-                        Z::step(slot, phase, 1);
+                        step(slot, phase, 1);
                     }
                 }
                 __syncwarp();
                 ok = all(ok);
-                filled += 2 * NC;
-                Z::step(s, ph, 2 * NC);
+                filled += 2;
+                step(s, ph, 2);
             }
             __syncwarp();  // (all lanes have read the item)
             if (lane == 0) mbar_arrive(&sh.item_free[item & 1]);
@@ -236,8 +210,8 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
         }
         if (__any_sync(0xFFFFFFFFu, sh.abort)) {
             // let the copies in flight land (the last fill of each barrier)
-            for (int k = 0; k < Z::SLOTS; ++k) {
-                const int fills = (filled + Z::SLOTS - 1 - k) / Z::SLOTS;
+            for (int k = 0; k < SLOTS; ++k) {
+                const int fills = (filled + SLOTS - 1 - k) / SLOTS;
                 if (fills > 0) wait_out(&sh.full[k], (fills - 1) & 1);
             }
         }
@@ -249,38 +223,24 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
             constexpr uint32_t id_s = idesc_of<T>(ROWS, TN, false), id_o = idesc_of<T>(ROWS, 64, true);
             const uint64_t qd = smem_desc_sw128(q_s), pd = smem_desc_sw128(p_s);
             const uint64_t kd = smem_desc_sw128(ring), vd = smem_desc_rows_k(ring);
-            int sa = 0, sb = NC;            // the next slots of tile a's keys and tile b's values
+            int sa = 0, sb = 1;            // the next slots of tile a's keys and tile b's values
             uint32_t pa = 0, pb = 0;        // their phases
             uint32_t ga = 0, gb = 0;        // the numbers of tiles a and b
             uint32_t ahead = 0, firsts = 0, idle = 0;  // tiles between; which are their item's first
             const auto products = [&]() {
-                bool there = ahead > 0 && mbar_poll(&sh.p_ready, gb & 1);
-                {
-                    int k = sb;
-                    uint32_t ph = pb;
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        there = there && mbar_poll(&sh.full[k], ph);
-                        Z::step(k, ph, 1);
-                    }
-                }
-                if (!there) {
+                if (ahead == 0 || !mbar_poll(&sh.p_ready, gb & 1) || !mbar_poll(&sh.full[sb], pb)) {
                     if (++idle > POLL_LIMIT) sh.abort = 1;
                     return;
                 }
                 tc_fence_after();
+                const uint64_t v = vd + sb * (CHUNK >> 4);
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const uint64_t v = vd + sb * (CHUNK >> 4);
-#pragma unroll
-                    for (int u = 0; u < TN / 16; ++u)
-                        mma_ws(tmem + Z::O_COL + c * W, pd + (u >> 2) * (Z::Q_CHUNK >> 4) + 2 * (u & 3),
-                               v + u * (2048 >> 4), id_o, !(firsts & 1) || u > 0);
-                    mma_commit(&sh.empty[sb]);
-                    Z::step(sb, pb, 1);
-                }
+                for (int u = 0; u < TN / 16; ++u)
+                    mma_ws(tmem + O_COL, pd + (u >> 2) * (Q_BYTES >> 4) + 2 * (u & 3), v + u * (2048 >> 4), id_o,
+                           !(firsts & 1) || u > 0);
+                mma_commit(&sh.empty[sb]);
                 mma_commit(&sh.pv_done);
-                Z::step(sb, pb, NC);
+                step(sb, pb, 2);
                 ++gb;
                 --ahead;
                 firsts >>= 1;
@@ -298,24 +258,17 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
             for (uint32_t item = 0;; ++item) {
                 const int tiles = sh.item[item & 1].tiles;
                 mbar_arrive(&sh.item_free[item & 1]);
-                const uint64_t q = qd + (item & 1) * (Z::Q_BYTES >> 4);
+                const uint64_t q = qd + (item & 1) * (Q_BYTES >> 4);
                 if (!filled(&sh.q_full[item & 1], (item >> 1) & 1)) break;
                 for (int i = 0; i < tiles && !sh.abort; ++i) {
                     while (ahead > 1 && !sh.abort) products();  // the scores' buffer is free
-                    const uint32_t d = tmem + Z::S_COL + (ga & 1) * C;
+                    const uint32_t d = tmem + S_COL + (ga & 1) * C;
+                    if (!filled(&sh.full[sa], pa)) break;
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        if (!filled(&sh.full[sa], pa)) break;
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            mma_ws(d, q + c * (Z::Q_CHUNK >> 4) + 2 * u, kd + sa * (CHUNK >> 4) + 2 * u, id_s,
-                                   (c | u) != 0);
-                        mma_commit(&sh.empty[sa]);
-                        Z::step(sa, pa, 1);
-                    }
-                    if (sh.abort) break;
+                    for (int u = 0; u < 4; ++u) mma_ws(d, q + 2 * u, kd + sa * (CHUNK >> 4) + 2 * u, id_s, u != 0);
+                    mma_commit(&sh.empty[sa]);
                     mma_commit(&sh.s_full[ga & 1]);
-                    Z::step(sa, pa, NC);
+                    step(sa, pa, 2);
                     firsts |= static_cast<uint32_t>(i == 0) << ahead;
                     ++ga;
                     ++ahead;
@@ -333,17 +286,17 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
         }
     } else if (warp == 6) {
         // ---- the items, each published when the one two before it is left behind, and their queries
-        Item<TN> it = sh.item[0];
+        Item it = sh.item[0];
         for (uint32_t item = 0;; ++item) {
-            const uint32_t to = q_s + (item & 1) * Z::Q_BYTES;
+            const uint32_t to = q_s + (item & 1) * Q_BYTES;
             const int rows = it.u.nq * p.G - it.u.m0;
 #pragma unroll 8
-            for (int v = lane; v < ROWS * NC * 8; v += 32) {
-                const int r = v / (NC * 8), cv = v % (NC * 8), m = it.u.m0 + r, tok = m / p.G;
+            for (int v = lane; v < ROWS * 8; v += 32) {
+                const int r = v / 8, cv = v % 8, m = it.u.m0 + r, tok = m / p.G;
                 const bool real = r < rows && cv * 8 < p.D;
                 const uint16_t *src = p.q + (it.u.q0 + tok) * p.q_tok + (it.head * p.G + m - tok * p.G) * p.q_head + cv * 8;
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                                 to + (cv >> 3) * Z::Q_CHUNK + r * 128 + (((cv & 7) ^ (r & 7)) << 4)),
+                                 to + r * 128 + ((cv ^ (r & 7)) << 4)),
                              "l"(real ? src : p.q), "r"(real ? 16 : 0)
                              : "memory");
             }
@@ -372,10 +325,7 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
         // the threads of a row meet, and each sees the others' values
         const auto meet = [&](float v, auto join) {
             sh.other[slot][part][r] = v;
-            if constexpr (ROWS == 64)
-                asm volatile("bar.sync %0, 64;" ::"r"(1 + (wq & 1)) : "memory");
-            else
-                asm volatile("bar.sync 1, 128;" ::: "memory");
+            asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
             for (int k = 1; k < NQ; ++k) v = join(v, sh.other[slot][(part + k) % NQ][r]);
             slot ^= 1;
@@ -383,7 +333,7 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
         };
         uint32_t g = 0;
         for (uint32_t item = 0;; ++item) {
-            const volatile Item<TN> &my = sh.item[item & 1];
+            const volatile Item &my = sh.item[item & 1];
             const int tiles = my.tiles, i0 = my.i0, ns = my.u.ns, skip = my.u.w0 - ns, len = my.u.len;
             const int m0 = my.u.m0, base = len - my.u.nq, rows = my.u.nq * p.G - m0;
             const int tail = (len % TN != 0 ? ns + len / TN - my.u.w0 : -1) - i0;
@@ -396,7 +346,7 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
                 wait_long(sh, &sh.s_full[g & 1], (g >> 1) & 1);
                 tc_fence_after();
                 uint32_t x[C];
-                tmem_load<C>(trow + Z::S_COL + (g & 1) * C, x);
+                tmem_ld32(trow + S_COL + (g & 1) * C, x);
                 tmem_wait_ld();
                 const int key0 = (i0 + j < ns ? i0 + j : i0 + j + skip) * TN;
                 if (__builtin_expect(key0 + TN > sure || (width && key0 < most - width), 0)) {
@@ -441,15 +391,12 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
                     tc_fence_after();
                     const float f = raise ? ex2(m_old - m_ref) : 1.0f;
                     l *= f;
-#pragma unroll 1
-                    for (int c = 0; c < NC * W; c += 16) {
-                        uint32_t o[16];
-                        tmem_ld16(trow + Z::O_COL + c, o);
-                        tmem_wait_ld();
+                    uint32_t o[W];
+                    tmem_ld16(trow + O_COL, o);
+                    tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        tmem_st16(trow + Z::O_COL + c, o);
-                    }
+                    for (int i = 0; i < W; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                    tmem_st16(trow + O_COL, o);
                     tmem_wait_st();
                 }
                 float l0, l1;
@@ -459,7 +406,7 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
                 for (int v = 0; v < C / 8; ++v) {
                     const int at = part * (C / 8) + v;  // 16 bytes of the row's 2 TN
                     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                     p_s + (at >> 3) * Z::Q_CHUNK + r * 128 + (((at & 7) ^ (r & 7)) << 4)),
+                                     p_s + (at >> 3) * Q_BYTES + r * 128 + (((at & 7) ^ (r & 7)) << 4)),
                                  "r"(weights[v].x), "r"(weights[v].y), "r"(weights[v].z), "r"(weights[v].w)
                                  : "memory");
                 }
@@ -467,16 +414,13 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
                     // value rows behind the row's last key: whatever lies there must not meet the
                     // zero weights
                     const int z0 = len % TN;
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        const uint32_t n = g * (2 * NC) + NC + c, at = n % Z::SLOTS;
-                        wait(sh, &sh.full[at], (n / Z::SLOTS) & 1);
-                        for (int i = tid; i < (TN - z0) * 8; i += 128)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                             ring + at * CHUNK + z0 * 128 + i * 16),
-                                         "r"(0)
-                                         : "memory");
-                    }
+                    const uint32_t n = 2 * g + 1, at = n % SLOTS;
+                    wait(sh, &sh.full[at], (n / SLOTS) & 1);
+                    for (int i = tid; i < (TN - z0) * 8; i += 128)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                         ring + at * CHUNK + z0 * 128 + i * 16),
+                                     "r"(0)
+                                     : "memory");
                 }
                 fence_async_smem();
                 tc_fence_before();
@@ -505,36 +449,29 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
             uint16_t *dst = p.out + out_row * p.out_tok + h * p.out_head + part * W;
             // 32 bytes a store, a whole sector, where the rows allow it
             const bool sectors = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
+            uint32_t o[W] = {};
+            if (tiles > 0) {
+                tmem_ld16(trow + O_COL, o);
+                tmem_wait_ld();
+            }
+            if (real) {
+                float f[W];
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                uint32_t o[W] = {};
-                if (tiles > 0) {
-                    tmem_load<W>(trow + Z::O_COL + c * W, o);
-                    tmem_wait_ld();
-                }
-                if (!real) continue;
+                for (int i = 0; i < W; ++i) f[i] = tiles > 0 ? __uint_as_float(o[i]) * inv : 0.0f;
+                if (!whole) {
 #pragma unroll
-                for (int v = 0; v < W; v += 16) {
-                    float f[16];
+                    for (int k = 0; k < W; k += 4)
+                        *part_at<1, ROWS>(p, slot_out, part * W + k, r) =
+                            make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+                } else if (part * W < p.D) {
+                    uint32_t y[8];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) f[i] = tiles > 0 ? __uint_as_float(o[v + i]) * inv : 0.0f;
-                    if (whole) {
-                        if (c * 64 + part * W + v >= p.D) continue;
-                        uint32_t y[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) y[i] = T::narrow2(f[2 * i], f[2 * i + 1]);
-                        uint16_t *d = dst + c * 64 + v;
-                        if (sectors) {
-                            st_global_32B(d, y);
-                        } else {
-                            *reinterpret_cast<uint4 *>(d) = make_uint4(y[0], y[1], y[2], y[3]);
-                            *reinterpret_cast<uint4 *>(d + 8) = make_uint4(y[4], y[5], y[6], y[7]);
-                        }
+                    for (int i = 0; i < 8; ++i) y[i] = T::narrow2(f[2 * i], f[2 * i + 1]);
+                    if (sectors) {
+                        st_global_32B(dst, y);
                     } else {
-#pragma unroll
-                        for (int k = 0; k < 16; k += 4)
-                            *part_at<NC, ROWS, 1>(p, slot_out, 0, c * 64 + part * W + v + k, r) =
-                                make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+                        *reinterpret_cast<uint4 *>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
+                        *reinterpret_cast<uint4 *>(dst + 8) = make_uint4(y[4], y[5], y[6], y[7]);
                     }
                 }
             }
@@ -547,20 +484,12 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
             bool more = next_item(item);
             uint32_t every;
             __syncwarp();
-            if constexpr (ROWS == 64)
-                asm volatile(
-                    "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
-                    "bar.red.and.pred p, %1, 64, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                    : "=r"(every)
-                    : "r"(1 + (wq & 1)), "r"(static_cast<uint32_t>(more))
-                    : "memory");
-            else
-                asm volatile(
-                    "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-                    "bar.red.and.pred p, 1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                    : "=r"(every)
-                    : "r"(static_cast<uint32_t>(more))
-                    : "memory");
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+                "bar.red.and.pred p, 1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(every)
+                : "r"(static_cast<uint32_t>(more))
+                : "memory");
             if (!every) break;
         }
     }
@@ -574,7 +503,7 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                     "r"(static_cast<uint32_t>(Z::COLS))
+                     "r"(TMEM_COLS)
                      : "memory");
     }
 }
@@ -582,63 +511,45 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
 struct Layout {
     size_t plan, part, lse, total;
 };
-Layout layout(int rows, int ctas, int NC) {
+Layout layout() {
     const auto align256 = [](size_t n) { return (n + 255) & ~static_cast<size_t>(255); };
-    const size_t slots = static_cast<size_t>(2) * ctas * SMS;
+    constexpr size_t slots = static_cast<size_t>(2) * CTAS * SMS;
     Layout y;
     y.plan = 0;
     y.part = align256(slots * sizeof(Plan));
-    y.lse = y.part + slots * rows * (64 * NC) * 4;
-    y.total = y.lse + align256(slots * rows * 4);
+    y.lse = y.part + slots * ROWS * 64 * 4;
+    y.total = y.lse + align256(slots * ROWS * 4);
     return y;
 }
 
-template <typename T, int NC, int ROWS>
+template <typename T>
 cudaError_t launch(const HeadsAttnArgs &a, cudaStream_t stream) {
-    using Z = Sizes<NC, ROWS>;
-    const Layout y = layout(ROWS, Z::CTAS, NC);
+    const Layout y = layout();
     Params p;
     Maps maps;
-    if (!set_up(a, ROWS, 1, Z::TN, false, y.plan, y.part, y.lse, p, maps)) return cudaErrorInvalidValue;
+    if (!set_up(a, ROWS, TN, false, y.plan, y.part, y.lse, p, maps)) return cudaErrorInvalidValue;
     static AttrCache attr;
-    cudaError_t e = ensure_attr(k_heads_few<T, NC, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::SMEM, attr);
+    cudaError_t e = ensure_attr(k_heads_few<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM, attr);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(Z::CTAS * SMS);
+    cfg.gridDim = dim3(CTAS * SMS);
     cfg.blockDim = dim3(NTHREADS);
-    cfg.dynamicSmemBytes = Z::SMEM;
+    cfg.dynamicSmemBytes = SMEM;
     cfg.stream = stream;
     cfg.attrs = pdl_attr();  // set up beside the end of whatever the stream runs before
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, k_heads_few<T, NC, ROWS>, maps, p);
+    e = cudaLaunchKernelEx(&cfg, k_heads_few<T>, maps, p);
     if (e != cudaSuccess) return e;
     count_launches(1);
-    // few units are cut into many parts each
-    const bool spread = a.B * a.Hkv * 4 < Z::CTAS * SMS;
-    cfg.gridDim = dim3(ROWS / 32, Z::CTAS * SMS, spread ? JOIN_WARPS : 1);
-    cfg.blockDim = dim3(JOIN_THREADS);
-    cfg.dynamicSmemBytes = 0;
-    e = spread ? cudaLaunchKernelEx(&cfg, k_heads_join<T, NC, ROWS, 1, true>, p)
-               : cudaLaunchKernelEx(&cfg, k_heads_join<T, NC, ROWS, 1, false>, p);
-    if (e == cudaSuccess) count_launches(1);
-    return e;
-}
-template <typename T, int ROWS>
-cudaError_t pick(const HeadsAttnArgs &a, cudaStream_t s) {
-    return a.D <= 64 ? launch<T, 1, ROWS>(a, s) : a.D <= 128 ? launch<T, 2, ROWS>(a, s) : launch<T, 4, ROWS>(a, s);
+    return launch_join<T, 1, ROWS>(cfg, p, stream);
 }
 
 }  // namespace hfw
 
-size_t heads_few_workspace_bytes(int32_t D, bool rows32) {
-    const int NC = D <= 64 ? 1 : D <= 128 ? 2 : 4;
-    return hfw::layout(rows32 ? 32 : 64, rows32 && NC <= 2 ? 2 : 1, NC).total;
-}
+size_t heads_few_workspace_bytes() { return hfw::layout().total; }
 
-cudaError_t run_heads_few(const HeadsAttnArgs &a, bool rows32, int dtype, cudaStream_t stream) {
-    if (dtype == MTPSPEC_BF16)
-        return rows32 ? hfw::pick<Bf16, 32>(a, stream) : hfw::pick<Bf16, 64>(a, stream);
-    return rows32 ? hfw::pick<F16, 32>(a, stream) : hfw::pick<F16, 64>(a, stream);
+cudaError_t run_heads_few(const HeadsAttnArgs &a, int dtype, cudaStream_t stream) {
+    return dtype == MTPSPEC_BF16 ? hfw::launch<Bf16>(a, stream) : hfw::launch<F16>(a, stream);
 }
 
 }  // namespace mtpspec

@@ -322,11 +322,12 @@ struct HeadsAttnArgs {
 };
 size_t heads_attn_workspace_bytes(int64_t B, int64_t Tq, int32_t Hq, int32_t Hkv, int32_t D);
 cudaError_t run_heads_attn(const HeadsAttnArgs &a, int dtype, cudaStream_t stream);
-// Its forms: for rows of many tokens (heads_chunk.cu), and for rows of few (heads_few.cu).
+// Its kernels: for all calls (heads_chunk.cu), and for rows of few tokens and heads of up to 64
+// elements (heads_few.cu).
 size_t heads_chunk_workspace_bytes(int32_t D);
 cudaError_t run_heads_chunk(const HeadsAttnArgs &a, int dtype, cudaStream_t stream);
-size_t heads_few_workspace_bytes(int32_t D, bool rows32);
-cudaError_t run_heads_few(const HeadsAttnArgs &a, bool rows32, int dtype, cudaStream_t stream);
+size_t heads_few_workspace_bytes();
+cudaError_t run_heads_few(const HeadsAttnArgs &a, int dtype, cudaStream_t stream);
 
 // The pages of a draft head's cache (pages.cu).
 struct PagesResizeArgs {
