@@ -181,3 +181,32 @@ def test_pages_past_32_bit_offsets():
     x.table = torch.where(x.table >= 0, x.table + (pages - n), x.table)
     x.run(lib)
     x.check(heads=[0, 15])
+
+
+# Heads of up to 64 elements with few (token, head) rows a row: units of 32 rows.
+SMALL = [
+    (4, 4, 64, 16, BF), (64, 8, 64, 16, F16), (10, 2, 48, 24, BF), (32, 1, 64, 64, F16), (40, 1, 16, 8, BF),
+    (128, 1, 64, 128, BF), (12, 4, 32, 48, F16),
+]
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,P,dtype", SMALL)
+@pytest.mark.parametrize("rows", [
+    [(1, 1)], [(1, 5000)], [(1, 1), (0, 40), (1, 128), (0, 0), (1, 129), (1, 1000), (0, 3), (0, 1)],
+    [(1, n) for n in range(1, 150)], [(2, 3), (0, 8), (0, 9), (5, 700)] + [(0, 1)] * 40, [(0, 5)] * 3 + [(1, 2)],
+])
+def test_few_rows_of_small_heads(Hq, Hkv, D, P, dtype, rows):
+    x = Batch(rows, Hq, Hkv, D, P, dtype, seed=len(rows) + D)
+    x.run(lib)
+    x.check(heads=sorted({0, Hq // 2, Hq - 1}))
+
+
+@pytest.mark.parametrize("window,sinks", [
+    (1, 0), (1, 1), (5, 3), (127, 4), (128, 128), (129, 200), (300, 4), (1, 5000), (2 ** 31 - 1, 2 ** 31 - 1),
+    (130, 100000)])
+@pytest.mark.parametrize("Hq,Hkv,D,P,dtype", SMALL[:3])
+def test_windows_of_few_rows_of_small_heads(window, sinks, Hq, Hkv, D, P, dtype):
+    rows = [(1, 1), (1, 1000), (3, 1300), (3, 128), (1, 520), (2, 257), (0, 9), (4, 4), (1, 129)]
+    x = Batch(rows, Hq, Hkv, D, P, dtype, seed=window % 1000 + sinks)
+    x.run(lib, window, sinks)
+    x.check(window, sinks, heads=[0, Hq - 1])
