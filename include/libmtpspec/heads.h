@@ -18,8 +18,9 @@
  * come in any order, but no two of its elements may share a place: each stride is at least what
  * the axes of smaller strides span.
  *
- * Cache entries below a row's length are finite; whatever lies at or beyond it (an unwritten part
- * of a page, NaN and infinities among it) has no effect.
+ * Cache entries below a row's length, in the pages that its visible positions need, are finite;
+ * whatever lies at or beyond the length (an unwritten part of a page, NaN and infinities among it), or
+ * in other pages, has no effect.
  */
 #ifndef LIBMTPSPEC_HEADS_H
 #define LIBMTPSPEC_HEADS_H

@@ -65,9 +65,13 @@ struct Unit {
         : q0(q0_), nq(nq_), len(len_), m0(unit * p.unit_rows) {
         w0 = ns = 0;
         if (p.window > 0 && p.window < len) {
-            w0 = max(0, len - nq + m0 / p.G - p.window + 1) / TN;
+            w0 = window(p) / TN;
             ns = min(p.sinks / TN + (p.sinks % TN != 0), w0);
         }
+    }
+    // The first key of its first row's window: none of its rows sees one before it but the first tokens.
+    __device__ __forceinline__ int window(const Params &p) const {
+        return p.window > 0 && p.window < len ? max(0, len - nq + m0 / p.G - p.window + 1) : 0;
     }
     // Key tiles that `rows` rows from row m on meet.
     __device__ __forceinline__ int tiles(const Params &p, int m, int rows) const {
@@ -311,17 +315,19 @@ __device__ __forceinline__ void wait_out(uint64_t *bar, uint32_t parity) {
 
 // A tile of keys in boxes that stay within a page, one a lane: where this lane's box of the tile lies.
 // Its page's number is asked for by look() and looked at by settle(), a tile later, so that nothing
-// waits for the answer.
+// waits for the answer.  Of a box between the first tokens and the window, which no row of the unit
+// sees, neither the table's entry nor the page is read: the entry may be gone, and the page another's.
 struct Box {
     int page, slot;
     bool mine;
-    __device__ __forceinline__ void look(const Params &p, const int32_t *table, int key, int len, bool lane_has) {
+    __device__ __forceinline__ void look(const Params &p, const int32_t *table, int key, int len, int window,
+                                         bool lane_has) {
         const int pi = key / p.page_size;
         slot = key - pi * p.page_size;
-        mine = lane_has && key < len;
+        mine = lane_has && key < len && (key + p.box_rows > window || key < p.sinks);
         if (mine) page = table[pi];
     }
-    // (page, row of it): beyond the row's length, and where the table has no such page, TMA fills zeros
+    // (page, row of it): where nothing is seen, and where the table has no such page, TMA fills zeros
     __device__ __forceinline__ int2 settle(const Params &p) const {
         const bool good = mine && static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages);
         if (mine && !good && p.status) atomicOr(p.status, MTPSPEC_STATUS_BAD_PARAM);

@@ -418,11 +418,11 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
             const Item &my = sh.item[item % ITEMS];
             const int32_t *table = p.block_table + static_cast<int64_t>(my.row) * p.max_pages;
             const int tiles = my.tiles, i0 = my.i0, head = my.head, len = my.u.len, ns = my.u.ns, skip = my.u.w0 - ns;
-            const int q_tok = my.u.q0 + my.u.m0 / p.G;
+            const int q_tok = my.u.q0 + my.u.m0 / p.G, window = my.u.window(p);
             Box box = {};  // of the next tile
             const auto look = [&](int i) {
                 const int key = (i0 + i < ns ? i0 + i : i0 + i + skip) * TN;
-                box.look(p, table, key + (first + lane) * p.box_rows, len, lane < mine);
+                box.look(p, table, key + (first + lane) * p.box_rows, len, window, lane < mine);
             };
             look(0);
             for (int i = 0; ok && i < tiles; ++i) {

@@ -171,9 +171,10 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
         for (uint32_t item = 0;; ++item) {
             const Item my = sh.item[item & 1];
             const int32_t *table = p.block_table + static_cast<int64_t>(my.row) * p.max_pages;
+            const int window = my.u.window(p);
             Box box = {};
             const auto look = [&](int i) {
-                box.look(p, table, my.u.key_tile(my.i0 + i) * TN + lane * p.box_rows, my.u.len, lane < boxes);
+                box.look(p, table, my.u.key_tile(my.i0 + i) * TN + lane * p.box_rows, my.u.len, window, lane < boxes);
             };
             if (my.tiles > 0) look(0);
             for (int i = 0; ok && i < my.tiles; ++i) {
