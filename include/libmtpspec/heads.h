@@ -110,7 +110,8 @@ int mtp_heads_attn(const void *q, int64_t q_tok_stride, int64_t q_head_stride, c
                    float *lse, int dtype, void *workspace, size_t workspace_bytes, int32_t *status,
                    void *stream);
 
-/* Bytes of device workspace mtp_heads_attn needs; 0 for sizes it would reject, and for Tq == 0. */
+/* Bytes of device workspace mtp_heads_attn needs; 0 for sizes it would reject, and for Tq == 0.  It
+ * depends on D alone: a workspace serves any batch of such heads. */
 size_t mtp_heads_attn_workspace_bytes(int64_t B, int64_t Tq, int32_t Hq, int32_t Hkv, int32_t D);
 
 #ifdef __cplusplus

@@ -784,7 +784,7 @@ bool heads_attn_sizes(int64_t B, int64_t Tq, int32_t Hq, int32_t Hkv, int32_t D)
 MTPSPEC_API size_t mtp_heads_attn_workspace_bytes(int64_t B, int64_t Tq, int32_t Hq, int32_t Hkv,
                                                   int32_t D) {
     if (!heads_attn_sizes(B, Tq, Hq, Hkv, D) || Tq == 0) return 0;
-    return mtpspec::heads_attn_workspace_bytes(B, Tq, Hq, Hkv, D);
+    return mtpspec::heads_attn_workspace_bytes(D);
 }
 
 MTPSPEC_API int mtp_heads_attn(const void *q, int64_t q_tok_stride, int64_t q_head_stride,
@@ -811,7 +811,7 @@ MTPSPEC_API int mtp_heads_attn(const void *q, int64_t q_tok_stride, int64_t q_he
         !aligned(block_table, 4) || !aligned(cu_q, 4) || !aligned(kv_len, 4) || !aligned(lse, 4) ||
         !aligned(status, 4))
         return MTPSPEC_ERR_ARG;
-    if (!workspace || workspace_bytes < mtpspec::heads_attn_workspace_bytes(B, Tq, Hq, Hkv, D))
+    if (!workspace || workspace_bytes < mtpspec::heads_attn_workspace_bytes(D))
         return MTPSPEC_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return MTPSPEC_ERR_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

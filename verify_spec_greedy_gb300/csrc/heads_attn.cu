@@ -48,8 +48,11 @@ cudaError_t run_wait_selftest_heads(uint32_t limit, int32_t *status, cudaStream_
     return e;
 }
 
-size_t heads_attn_workspace_bytes(int64_t B, int64_t Tq, int32_t Hq, int32_t Hkv, int32_t D) {
-    return few(B, Tq, Hq, Hkv, D) ? heads_few_workspace_bytes() : heads_chunk_workspace_bytes(D);
+// What either kernel needs, so that a workspace for a batch is one for any smaller batch too, whichever
+// kernel that takes.
+size_t heads_attn_workspace_bytes(int32_t D) {
+    const size_t chunk = heads_chunk_workspace_bytes(D), few = heads_few_workspace_bytes();
+    return D <= 64 && few > chunk ? few : chunk;
 }
 
 cudaError_t run_heads_attn(const HeadsAttnArgs &a, int dtype, cudaStream_t stream) {

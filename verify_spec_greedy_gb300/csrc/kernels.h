@@ -320,7 +320,7 @@ struct HeadsAttnArgs {
     void *workspace;
     int32_t *status;
 };
-size_t heads_attn_workspace_bytes(int64_t B, int64_t Tq, int32_t Hq, int32_t Hkv, int32_t D);
+size_t heads_attn_workspace_bytes(int32_t D);
 cudaError_t run_heads_attn(const HeadsAttnArgs &a, int dtype, cudaStream_t stream);
 // Its kernels: for all calls (heads_chunk.cu), and for rows of few tokens and heads of up to 64
 // elements (heads_few.cu).
