@@ -40,7 +40,7 @@ extern "C" {
  *      none: they hold what they kept, and MTPSPEC_STATUS_NO_PAGES is OR-ed in.
  * A row with keep[b] < 0 is left as it is.  So is one with a length that does not fit (keep above
  * what is held, lens below keep or above the table); MTPSPEC_STATUS_BAD_PARAM is OR-ed in for it,
- * as for a page id out of range, which is passed over.
+ * as for a page id out of range among those of steps 1 and 2, which is passed over.
  *   keep, lens int32 [B]     copies int32 [B, 2], or NULL: step 2 is left out
  *   status     int32 [1] or NULL
  * One launch.

@@ -176,8 +176,11 @@ __global__ void __launch_bounds__(THREADS) k_pages_resize(const PagesResizeArgs 
     bool shared = false;
     if (a.copies)
         for (int64_t b = tid; b < a.B; b += THREADS) {
-            const int32_t p = last_page(b, row(b));
-            if (is_page(a, p) && (__ldcg(a.refs + p) & 0xFFFF) > 1) {
+            const Row r = row(b);
+            const int32_t p = last_page(b, r);
+            if (!is_page(a, p)) {
+                if (r.partly) flag(a.status, MTPSPEC_STATUS_BAD_PARAM);
+            } else if ((__ldcg(a.refs + p) & 0xFFFF) > 1) {
                 atomicAdd(a.refs + p, 1 << 16);
                 shared = true;
             }
