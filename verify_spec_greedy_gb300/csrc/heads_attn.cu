@@ -4,15 +4,24 @@
 namespace mtpspec {
 namespace {
 
-// How a call goes.  heads_chunk.cu takes any: its units of 128 rows keep up with the cache's bytes
-// even where a row of the batch has a token and a key head eight queries.  Where heads have at most 64
-// elements, a tile of keys is 32 KB, and the smaller units of heads_few.cu, two CTAs an SM, get from tile
-// to tile faster: up to 32 rows of work a row of the batch and key head (64 rows, a window of 1024,
-// pages of 16: 43 us, not 49; 2000-4000 keys 102, not 107; from two units a row on its bytes double).
-// Heads of 128 elements take the same time in both (256 rows x 4 tokens 378 and 378 us; 256 rows of
-// 50-1000 keys in pages of 16 106 here, 143 there), heads of 256 133 here and 202 there.
+// How a call goes.  heads_chunk.cu takes any: units of 128 rows.  Where heads have at most 64 elements,
+// a tile of keys is 32 KB, and the units of 32 rows of heads_few.cu, two CTAs an SM, get from tile to
+// tile faster as long as a row of the batch and key head fills one or two.  In us, heads of 64, eight key
+// heads, few / chunk:
+//   1 token a row, a window of 1024 and 4: 4 rows 14.4 / 15.5, 16 rows 18 / 20, 64 rows 37 / 49, 256 rows
+//   131 / 154; a window of 128: 64 rows 17 / 26, 256 rows 40 / 75; 256 rows over 50-100 keys 32 / 47, over
+//   500-1000 90 / 104, over 2000-4000 371 / 366; 4 tokens a row over 2000-4000 377 / 370
+// (heads of 128 elements over 500-4000 keys take the same time in both, heads of 256 more in it).
+//
+// The host knows how many tokens a row has on average only.  A batch of drafts or verifications has the
+// same number in every row, so its tokens are a multiple of the rows; in one that mixes prompts with
+// drafts, or with rows of no tokens, each of the prompt's units of 32 rows reads all its keys:
+//   a prompt of 64 / 256 / 700 / 4000 tokens in a table of 1024 rows of none: 13 / 25 / 66 / 662, in
+//   heads_chunk.cu 11 / 15 / 29 / 233; of 700 beside 255 drafts over 1000 keys 167 / 140
+//   256 rows of 1-4 tokens over 100-200 keys: 47 / 69, over 500-1000 91 / 105
+// So other batches are taken up to the tokens that 256 such rows have, 640 and two deviations.
 bool few(int64_t B, int64_t Tq, int32_t Hq, int32_t Hkv, int32_t D) {
-    return D <= 64 && Tq * (Hq / Hkv) <= 32 * B;
+    return D <= 64 && Tq * (Hq / Hkv) <= 32 * B && (Tq <= 680 || Tq % B == 0);
 }
 
 }  // namespace

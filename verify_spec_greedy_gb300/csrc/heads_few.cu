@@ -1,5 +1,6 @@
-// Attention with grouped heads over the paged cache, for rows of few tokens and heads of up to 64
-// elements: draft steps and verifications.  What bounds them is the cache's bytes and, at 32 KB a tile
+// Attention with grouped heads over the paged cache, for batches of few tokens a row (on average: a long
+// row among them is cut into units of 32 rows like any other) and heads of up to 64 elements: draft steps
+// and verifications.  What bounds them is the cache's bytes and, at 32 KB a tile
 // of keys and values, the way from one tile to the next.
 //
 // One pass over the keys with the running maximum m and sum l of a softmax, as in heads_chunk.cu.
@@ -12,7 +13,7 @@
 // Two CTAs share an SM: while one is in a softmax, the other's copies and products go on.
 //
 // What bounds it (HBM copy 6.8 TB/s measured; in a graph): 64 rows of a token, 64 / 8 heads of 64, pages of
-// 16, a window of 1024 and four first tokens, fp16, 136 MB: 43 us, 3.1 TB/s (in the other kernel 49).
+// 16, a window of 1024 and four first tokens, fp16, 136 MB: 37 us, 3.6 TB/s (in the other kernel 49).
 // 512 units of ten tiles on 304 CTAs: starts, ends and joins of units cut once or twice each.  (Two
 // producers, two buffers of weights: the same.)
 #include <algorithm>
