@@ -83,8 +83,6 @@ struct Unit {
     __device__ __forceinline__ int64_t weight(const Params &p) const { return START + max(tiles(p), 1); }
     // The number of its i-th key tile.
     __device__ __forceinline__ int key_tile(int i) const { return i < ns ? i : i - ns + w0; }
-    // The place in its list of the tile that the row's keys end in, if that is not a whole one.
-    __device__ __forceinline__ int tail() const { return len % TN != 0 ? ns + len / TN - w0 : -1; }
 };
 
 // An even cut of all units laid end to end: of the CTAs that take part, the first `rem` have

@@ -58,13 +58,12 @@ constexpr int AHEAD = 2;           // key tiles that the scores are ahead of the
 constexpr int ITEMS = 4;
 constexpr int MAX_SLOTS = 4;       // tiles of either ring
 
-// An item of a CTA: tiles i0 .. i1 - 1 of a unit's list of n, and the key tiles before it.  Its
-// `tiles` are at least one.  head -1: no more.
+// An item of a CTA: tiles i0 .. i1 - 1 of a unit's list of n.  Its `tiles` are at least one.  head -1:
+// no more.
 template <int TN>
 struct Item {
     Unit<TN> u;
     int row, head, i0, i1, n, tiles;
-    uint32_t g0;
 };
 
 // Barriers by tile are doubled, a phase for every other tile: who waits for a tile may be one behind,
@@ -80,49 +79,6 @@ struct __align__(16) Shared {
     int2 box[4][8];         // boxes of a tile, by producer
     float other[2][2][TM];  // what the two threads of a row tell each other, in turn, by half
 };
-
-// Whether all of two warps that share rows say yes.  They meet at barrier `bar` in everything they
-// do, so that after a wait that gave up none may go on without the others.
-__device__ __forceinline__ bool both(bool yes, int bar) {
-    uint32_t all;
-    __syncwarp();
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 q, %2, 0;\n\t"
-        "bar.red.and.pred p, %1, 64, q;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(all)
-        : "r"(bar), "r"(static_cast<uint32_t>(yes))
-        : "memory");
-    return all != 0;
-}
-
-// D[128, n] (+)= A[128, 16] B[16, n], A from tensor memory.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// Chunks side by side whose rows are the products' K axis.
-__device__ __forceinline__ uint64_t smem_desc_rows_k(uint32_t addr, uint32_t chunk) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(chunk >> 4) << 16;
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;
-    d |= static_cast<uint64_t>(1) << 46;
-    d |= static_cast<uint64_t>(2) << 61;
-    return d;
-}
-template <typename T>
-__host__ __device__ constexpr uint32_t idesc_of(int n, bool b_rows_k) {
-    return (1u << 4) | (T::mma_format << 7) | (T::mma_format << 10) |
-           (static_cast<uint32_t>(b_rows_k) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
-           (static_cast<uint32_t>(TM >> 4) << 24);
-}
 
 // NC: the 64-column chunks of a head.
 template <int NC>
@@ -241,7 +197,7 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
             return v;
         };
         uint32_t g = 0;  // the tile's number
-        for (uint32_t item = 0; both(there_is(item), pair_bar); ++item) {
+        for (uint32_t item = 0; all_say<64>(there_is(item), pair_bar); ++item) {
             // (what only the item's end needs stays in shared memory meanwhile)
             const volatile Item &my = sh.item[item % ITEMS];
             const int tiles = my.tiles, len = my.u.len, ns = my.u.ns, skip = my.u.w0 - ns, i0 = my.i0;
@@ -476,7 +432,7 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
     } else if (warp == 1) {
         if (elect_one()) {
             // ---- MMA issuer: a tile's products, then the scores of the tile two on
-            constexpr uint32_t id_s = idesc_of<T>(TN, false), id_o = idesc_of<T>(64 * NC, true);
+            constexpr uint32_t id_s = idesc_of<T>(TM, TN, false), id_o = idesc_of<T>(TM, 64 * NC, true);
             const uint64_t qd = smem_desc_sw128(q_s), kd = smem_desc_sw128(k_s), vd = smem_desc_rows_k(v_s, CHUNK);
             uint32_t gk = 0, gv = 0;  // the numbers of the next tiles
             for (uint32_t item = 0; there_is(item); ++item) {
@@ -523,7 +479,6 @@ k_heads_chunk(const __grid_constant__ Maps maps, const Params p) {
         // ---- the items after the first, each as soon as its place is left behind
         Item it = sh.item[0];
         for (uint32_t item = 1; it.head >= 0; ++item) {
-            it.g0 += it.tiles;
             next(it);
             if (!__all_sync(0xFFFFFFFFu, item < ITEMS || wait_far(sh, &sh.item_free[item % ITEMS],
                                                                   (item / ITEMS - 1) & 1)))

@@ -37,14 +37,13 @@ constexpr int S_COL = 0, O_COL = 2 * C;
 constexpr uint32_t TMEM_COLS = 128;
 static_assert(O_COL + W <= static_cast<int>(TMEM_COLS), "tensor memory");
 constexpr int NTHREADS = 224;  // warp 0 TMA, 1 MMA and TMEM, 2-5 softmax, 6 items and queries
-constexpr int SOFTMAX0 = 64;   // the first softmax thread
+constexpr int SOFTMAX0 = 64, SOFTMAX = 128;  // the first softmax thread, and how many
 constexpr int SLOTS = 5;             // chunks of the ring
 
-// Tiles i0 .. i1 - 1 of a unit's n (at least 1); g0: the CTA's tiles before it.  head -1: no more.
+// Tiles i0 .. i1 - 1 of a unit's n (at least 1).  head -1: no more.
 struct Item {
     Unit<TN> u;
     int row, head, i0, i1, n, tiles;
-    uint32_t g0;
 };
 
 struct __align__(16) Shared {
@@ -61,6 +60,7 @@ struct __align__(16) Shared {
 constexpr int EXTRA = static_cast<int>(sizeof(Shared));
 constexpr int SMEM = 2 * Q_BYTES + P_BYTES + SLOTS * CHUNK + EXTRA;
 static_assert(SMEM <= 113 * 1024 && SMEM > 75 * 1024, "two CTAs an SM, and no more: they take a quarter of its tensor memory");
+
 // The slot n chunks on, and its phase.
 __device__ __forceinline__ void step(int &s, uint32_t &ph, int n) {
     s += n;
@@ -70,33 +70,6 @@ __device__ __forceinline__ void step(int &s, uint32_t &ph, int n) {
     }
 }
 
-// D[ROWS, n] (+)= A[ROWS, 16] B[16, n], the accumulator folded into 128 lanes: lanes q * ROWS ..
-// hold the columns q * n / NQ ..
-__device__ __forceinline__ void mma_ws(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.ws.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// A chunk whose rows are the products' K axis.
-__device__ __forceinline__ uint64_t smem_desc_rows_k(uint32_t addr) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(1) << 16;  // (unused: one chunk of 64 columns)
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;
-    d |= static_cast<uint64_t>(1) << 46;
-    d |= static_cast<uint64_t>(2) << 61;
-    return d;
-}
-template <typename T>
-__host__ __device__ constexpr uint32_t idesc_of(int m, int n, bool b_rows_k) {
-    return (1u << 4) | (T::mma_format << 7) | (T::mma_format << 10) |
-           (static_cast<uint32_t>(b_rows_k) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
-           (static_cast<uint32_t>(m >> 4) << 24);
-}
 template <typename T>
 __global__ void __launch_bounds__(NTHREADS, CTAS)
 k_heads_few(const __grid_constant__ Maps maps, const Params p) {
@@ -224,7 +197,7 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
             // is issued, the products first, since they free slots.
             constexpr uint32_t id_s = idesc_of<T>(ROWS, TN, false), id_o = idesc_of<T>(ROWS, 64, true);
             const uint64_t qd = smem_desc_sw128(q_s), pd = smem_desc_sw128(p_s);
-            const uint64_t kd = smem_desc_sw128(ring), vd = smem_desc_rows_k(ring);
+            const uint64_t kd = smem_desc_sw128(ring), vd = smem_desc_rows_k(ring, 16);  // (one chunk: no step)
             int sa = 0, sb = 1;            // the next slots of tile a's keys and tile b's values
             uint32_t pa = 0, pb = 0;        // their phases
             uint32_t ga = 0, gb = 0;        // the numbers of tiles a and b
@@ -306,7 +279,6 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.q_full[item & 1]);
-            it.g0 += it.tiles;
             const bool more = next(it);
             if (!__all_sync(0xFFFFFFFFu, item == 0 || wait_far(sh, &sh.item_free[(item - 1) & 1],
                                                                ((item - 1) >> 1) & 1)))
@@ -482,17 +454,7 @@ k_heads_few(const __grid_constant__ Maps maps, const Params p) {
             tc_fence_before();
             __syncwarp();  // the whole warp is done with the item
             if (lane == 0) mbar_arrive(&sh.item_free[item & 1]);
-            // (the warps that share rows leave together: they meet in everything they do)
-            bool more = next_item(item);
-            uint32_t every;
-            __syncwarp();
-            asm volatile(
-                "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-                "bar.red.and.pred p, 1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                : "=r"(every)
-                : "r"(static_cast<uint32_t>(more))
-                : "memory");
-            if (!every) break;
+            if (!all_say<SOFTMAX>(next_item(item), 1)) break;
         }
     }
     if (warp == 6) walk.close(p);

@@ -187,35 +187,6 @@ __device__ __forceinline__ void wait_out(uint64_t *bar, int fills) {
         if (mbar_test(bar, (fills - 1) & 1)) return;
 }
 
-// D[64, n] (+)= A[64, 16] B[16, n] with the 64 rows' accumulator folded into 128 lanes: lanes
-// 0-63 hold the first n / 2 columns, lanes 64-127 the others.
-__device__ __forceinline__ void mma_ws(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.ws.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// The descriptor of a tile whose rows are the products' K axis (the "MN-major" form): its
-// 64-column chunks and its groups of 8 rows lie this many bytes apart.
-__device__ __forceinline__ uint64_t smem_desc_rows_k(uint32_t addr, uint32_t chunk_step, uint32_t group_step) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(chunk_step >> 4) << 16;
-    d |= static_cast<uint64_t>(group_step >> 4) << 32;
-    d |= static_cast<uint64_t>(1) << 46;
-    d |= static_cast<uint64_t>(2) << 61;
-    return d;
-}
-template <typename T>
-__host__ __device__ constexpr uint32_t idesc_of(int n, bool b_rows_k) {
-    return (1u << 4) | (T::mma_format << 7) | (T::mma_format << 10) |
-           (static_cast<uint32_t>(b_rows_k) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
-           (static_cast<uint32_t>(TM >> 4) << 24);
-}
-
 // What follows from L = 64 NL alone.  The output's columns come in pieces of 256, 128 and 64
 // (the widths of the folded accumulator); a slot of the latents' ring holds one piece.
 template <int NL>
@@ -490,7 +461,7 @@ k_latent_attn(const __grid_constant__ Maps maps, const Params p) {
             // ---- MMA issuer.  Two kinds of work wait for different things: the scores of
             // tile a for its chunks, the products of tile b for its weights.  Whichever is
             // there is issued, the products first, since they free the stage.
-            constexpr uint32_t id_qk = idesc_of<T>(TN, false);
+            constexpr uint32_t id_qk = idesc_of<T>(TM, TN, false);
             const uint64_t qd = smem_desc_sw128(q_s), pd = smem_desc_sw128(p_s);
             const uint64_t kd = smem_desc_sw128(kv_s), rd = smem_desc_sw128(rot_s);
             int item = 0;
@@ -508,7 +479,7 @@ k_latent_attn(const __grid_constant__ Maps maps, const Params p) {
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < Z::PIECES; ++k) {
-                    const uint32_t id = idesc_of<T>(Z::width(k) * 64, true);
+                    const uint32_t id = idesc_of<T>(TM, Z::width(k) * 64, true);
                     const uint64_t v = smem_desc_rows_k(kv_s, Z::chunk_step(k), Z::group_step(k)) +
                                        sb * (Z::SLOT_BYTES >> 4);
 #pragma unroll

@@ -126,22 +126,6 @@ __device__ __forceinline__ bool wait_far(Shared &sh, uint64_t *bar, uint32_t par
     return false;
 }
 
-// Whether all of two warps that share rows say yes.  They meet at barrier `bar` in everything they
-// do, so that after a wait that gave up none may go on without the others.
-__device__ __forceinline__ bool both(bool yes, int bar) {
-    uint32_t all;
-    __syncwarp();
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 q, %2, 0;\n\t"
-        "bar.red.and.pred p, %1, 64, q;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(all)
-        : "r"(bar), "r"(static_cast<uint32_t>(yes))
-        : "memory");
-    return all != 0;
-}
-
 // The bounded wait of a CTA that leaves, whatever the abort flag says.
 __device__ __forceinline__ void wait_out(uint64_t *bar, uint32_t parity) {
     for (uint32_t it = 0; it < WAIT_LIMIT; ++it)
@@ -152,34 +136,6 @@ __device__ __forceinline__ void wait_out(uint64_t *bar, uint32_t parity) {
 // at least 0), so that sequences never overlap and have no more pairs than the grid has CTAs.
 __device__ __forceinline__ int bound(const int32_t *cu, int i, int n, int before) {
     return max(min(cu[i], n), before);
-}
-
-// D[128, n] (+)= A[128, 16] B[16, n], A from tensor memory.  (Descriptors stay 64-bit values
-// from end to end: put together inside the asm they cost ten instructions a product.)
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// A tile whose rows are the products' K axis and whose 64-column chunks are CHUNK apart.
-__device__ __forceinline__ uint64_t smem_desc_rows_k(uint32_t addr) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(CHUNK >> 4) << 16;
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;
-    d |= static_cast<uint64_t>(1) << 46;
-    d |= static_cast<uint64_t>(2) << 61;
-    return d;
-}
-template <typename T>
-__host__ __device__ constexpr uint32_t idesc_of(int n, bool b_rows_k) {
-    return (1u << 4) | (T::mma_format << 7) | (T::mma_format << 10) |
-           (static_cast<uint32_t>(b_rows_k) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
-           (static_cast<uint32_t>(TM >> 4) << 24);
 }
 
 __device__ __forceinline__ int pairs_of(int queries) { return (queries + 2 * TM - 1) / (2 * TM); }
@@ -567,7 +523,7 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             tc_fence_before();
             __syncwarp();  // the whole warp is done with the item
             if (lane == 0) mbar_arrive(&sh.item_free[item & 1]);
-            if (!both(next_item(item), pair_bar)) break;
+            if (!all_say<64>(next_item(item), pair_bar)) break;
         }
     } else {
         if (warp == 0) {
@@ -641,10 +597,10 @@ k_latent_prefill(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         } else if (warp == 1) {
             if (elect_one()) {
                 // ---- MMA issuer: a tile's products, then its next scores, in turn
-                constexpr uint32_t id_s = idesc_of<T>(TN, false);
-                constexpr uint32_t id_o = idesc_of<T>(VC * 64, true), id_o64 = idesc_of<T>(64, true);
+                constexpr uint32_t id_s = idesc_of<T>(TM, TN, false);
+                constexpr uint32_t id_o = idesc_of<T>(TM, VC * 64, true), id_o64 = idesc_of<T>(TM, 64, true);
                 const uint64_t qd = smem_desc_sw128(q_s), kd = smem_desc_sw128(ring);
-                const uint64_t vd = smem_desc_rows_k(ring);
+                const uint64_t vd = smem_desc_rows_k(ring, CHUNK);
                 const auto scores = [&](int slot, int t) {
                     const uint32_t d = tmem + S_COL + t * 128;
                     const uint64_t a = qd + t * (KC * (CHUNK >> 4));
@@ -832,7 +788,7 @@ __global__ void k_wait_selftest(uint32_t limit, int32_t *status) {
             const int half = threadIdx.x >> 5;
             const bool there = wait_far(sh, half ? never : done, 0, limit);
             ok &= there == (half == 0);
-            got = both(there, 1);
+            got = all_say<64>(there, 1);
         } else {
             got = form == 0 ? wait(sh, never, 0, limit)
                   : form == 1 ? wait_long(sh, never, 0, limit) : wait_far(sh, never, 0, limit);

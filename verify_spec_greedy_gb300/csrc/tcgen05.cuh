@@ -56,6 +56,22 @@ __device__ __forceinline__ bool mbar_poll(uint64_t *bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// Whether all of THREADS threads, the warps that share rows, say yes.  They meet at barrier `bar` in
+// everything they do, so that after a wait that gave up none may go on without the others.
+template <int THREADS>
+__device__ __forceinline__ bool all_say(bool yes, int bar) {
+    uint32_t all;
+    __syncwarp();
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %2, 0;\n\t"
+        "bar.red.and.pred p, %1, %3, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(all)
+        : "r"(bar), "r"(static_cast<uint32_t>(yes)), "n"(THREADS)
+        : "memory");
+    return all != 0;
+}
 // One lane of a converged warp.  A branch on it tells the compiler that a single thread
 // runs: descriptors then stay in uniform registers (an MMA every 32 cycles instead of 44).
 __device__ __forceinline__ bool elect_one() {
@@ -101,7 +117,26 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr) {
     d |= static_cast<uint64_t>(2) << 61;                   // 128-byte swizzle
     return d;
 }
-// Instruction descriptor, kind::f16: fp32 accumulator, bf16 A and B, both K-major.
+// The descriptor of a tile whose rows are the products' K axis (the "MN-major" form): its
+// 64-column chunks and its groups of 8 rows lie this many bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_rows_k(uint32_t addr, uint32_t chunk_step,
+                                                     uint32_t group_step = 1024) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(chunk_step >> 4) << 16;
+    d |= static_cast<uint64_t>(group_step >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+// Instruction descriptor, kind::f16: fp32 accumulator, A and B of type T, B's rows its K axis or not.
+template <typename T>
+__host__ __device__ constexpr uint32_t idesc_of(int m, int n, bool b_rows_k) {
+    return (1u << 4) | (T::mma_format << 7) | (T::mma_format << 10) |
+           (static_cast<uint32_t>(b_rows_k) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(m >> 4) << 24);
+}
+// The same for bf16 A and B, both K-major.
 __host__ __device__ constexpr uint32_t instr_desc(int m, int n) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
            (static_cast<uint32_t>(m >> 4) << 24);
@@ -114,6 +149,28 @@ __device__ __forceinline__ void mma_bf16(uint32_t tmem_d, uint64_t adesc, uint64
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// D[128, n] (+)= A[128, 16] B[16, n], A from tensor memory.  (Descriptors stay 64-bit values
+// from end to end: put together inside the asm they cost ten instructions a product.)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// D[m, n] (+)= A[m, 16] B[16, n] for m of 32 or 64 rows, the accumulator folded into 128 lanes: lanes
+// q m .. hold the columns q n / (128 / m) ..
+__device__ __forceinline__ void mma_ws(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.ws.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
