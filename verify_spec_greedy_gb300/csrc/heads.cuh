@@ -12,7 +12,7 @@ namespace heads {
 using namespace tg;
 
 constexpr int SMS = 152;           // multiprocessors of a GB300
-constexpr int64_t START = 3;       // a unit's start and end, in key tiles (2: 5 % slower, 5: 1-7 %)
+constexpr int64_t START = 3;       // a unit's start and end, in key tiles (in heads_chunk.cu 2: 5 % slower, 5: 1-7 %)
 constexpr float LAZY = 8.0f;       // the running maximum may lag by a factor of 2^8
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr uint32_t POLL_LIMIT = 1u << 25;  // polls of some 20 ns: ~1 s

@@ -11,7 +11,8 @@ namespace {
 //   1 token a row, a window of 1024 and 4: 4 rows 14.4 / 15.5, 16 rows 18 / 20, 64 rows 37 / 49, 256 rows
 //   131 / 154; a window of 128: 64 rows 17 / 26, 256 rows 40 / 75; 256 rows over 50-100 keys 32 / 47, over
 //   500-1000 90 / 104, over 2000-4000 371 / 366; 4 tokens a row over 2000-4000 377 / 370
-// (heads of 128 elements over 500-4000 keys take the same time in both, heads of 256 more in it).
+// (Such units for heads of 128: 4 tokens a row 378 / 378, 256 rows over 50-1000 keys 143 / 106; of 256: 202 /
+// 133.)
 //
 // The host knows how many tokens a row has on average only.  A batch of drafts or verifications has the
 // same number in every row, so its tokens are a multiple of the rows; in one that mixes prompts with

@@ -29,15 +29,16 @@
 // second small kernel joins.
 //
 // What bounds it (HBM copy 6.8 TB/s, products 1885 TFLOP/s measured; in a graph):
-//   8 prompts of 77-1500 tokens, 32 / 4 heads of 128, pages of 16, bf16, 66 GFLOP: 95 us, 0.70 PFLOP/s.
+//   8 prompts of 77-1500 tokens, 32 / 4 heads of 128, pages of 16, bf16, 66 GFLOP: 93 us, 0.71 PFLOP/s.
 //     Units have six tiles on average, and nothing covers their starts and ends, which weigh as much
 //     as some three tiles (tensor pipe 31 %).
 //   6 rows of 1-1000 tokens behind up to 7001 keys, 40 / 8 heads of 128, pages of 48, fp16, 365 GFLOP:
-//     300 us, 1.22 PFLOP/s, 0.64.  A tile takes some 1,900 cycles, and the softmax of its 128 x 128
-//     scores by eight warps is the longest part (tensor pipe 55 %, issue slots 47 %, 2^x pipe 29 %).
-//   256 rows of 4 tokens over 500-4000 keys, 32 / 8 heads of 128, pages of 64, bf16, 2.39 GB: 378 us, 6.3
+//     300 us, 1.22 PFLOP/s, 0.64 (at 2070 MHz; in a long run the power limit leaves some 1800, and it is 322
+//     us).  A tile takes some 1,900 cycles, and the softmax of its 128 x 128 scores by eight warps is the
+//     longest part (tensor pipe 55 %, issue slots 47 %, 2^x pipe 29 %).
+//   256 rows of 4 tokens over 500-4000 keys, 32 / 8 heads of 128, pages of 64, bf16, 2.39 GB: 377 us, 6.3
 //     TB/s, 0.93 of the copy rate.
-//   8192 tokens, 16 / 2 heads of 256, pages of 128, bf16, 550 GFLOP: 465 us, 1.18 PFLOP/s, 0.63.  Tiles
+//   8192 tokens, 16 / 2 heads of 256, pages of 128, bf16, 550 GFLOP: 461 us, 1.19 PFLOP/s, 0.63.  Tiles
 //     are half as long, as two of 128 keys of such heads do not fit (tensor pipe 50 %, the products'
 //     reads of shared memory 50 %, issue slots 30 %).
 #include <algorithm>

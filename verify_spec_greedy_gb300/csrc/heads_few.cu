@@ -1,7 +1,7 @@
 // Attention with grouped heads over the paged cache, for batches of few tokens a row (on average: a long
 // row among them is cut into units of 32 rows like any other) and heads of up to 64 elements: draft steps
-// and verifications.  What bounds them is the cache's bytes and, at 32 KB a tile
-// of keys and values, the way from one tile to the next.
+// and verifications.  What bounds them is the cache's bytes and, at 32 KB a tile of keys and values, the way
+// from one tile to the next.
 //
 // One pass over the keys with the running maximum m and sum l of a softmax, as in heads_chunk.cu.
 // A unit's rows, the (token, head) rows of a key head, are 32, whose accumulators are folded into all
@@ -13,9 +13,9 @@
 // Two CTAs share an SM: while one is in a softmax, the other's copies and products go on.
 //
 // What bounds it (HBM copy 6.8 TB/s measured; in a graph): 64 rows of a token, 64 / 8 heads of 64, pages of
-// 16, a window of 1024 and four first tokens, fp16, 136 MB: 37 us, 3.6 TB/s (in the other kernel 49).
-// 512 units of ten tiles on 304 CTAs: starts, ends and joins of units cut once or twice each.  (Two
-// producers, two buffers of weights: the same.)
+// 16, a window of 1024 and four first tokens, fp16, 136 MB: 37 us, 3.6 TB/s (in the other kernel 49); 160
+// MB are read.  512 units of ten tiles on 304 CTAs: starts, ends and joins of units cut once or twice each.
+// (Two producers, two buffers of weights: the same.)
 #include <algorithm>
 
 #include "heads.cuh"

@@ -12,8 +12,9 @@
 // The copy is bytes, 16 KB a step and CTA.
 //
 // Measured in a graph: resize of 256 rows, 40,000 pages of 16: 11 us, a chain of some ten loads and
-// barriers and five windows.  Fork of 64 rows into four, with the copy of their last pages, 67 MB: 21
-// us.  Compaction of 8192 pages with its copy, 93 MB: 26 us, half of it the copy.
+// barriers and five windows (a call with 2^20 pages, of which the last are free: 320 us).  Fork of 64 rows
+// into four, with the copy of their last pages, 67 MB: 21 us.  Compaction of 8192 pages with its copy, 93
+// MB: 26 us, half of it the copy.
 #include "common.cuh"
 #include "kernels.h"
 
